@@ -1,14 +1,16 @@
 """ctypes binding of libgconv.so (the C ABI declared in include/gconv.h).
 
 Argument marshalling only: tensors must already be float32, contiguous and on
-the GPU; outputs and the workspace are allocated here with torch (device
+the GPU (the sequence operators at the end also take bfloat16, and strides
+where they say so); outputs and the workspace are allocated here with torch (device
 memory is torch's), and every op is enqueued on torch's current HIP stream.
 Nothing is computed in Python or by torch. When the library is missing the
 first call raises; there is no fallback.
 
 Names mirror the C entry points: gconv_fwd, gconv_bwd_data, gconv_bwd_filter,
 gconv_bwd_bias, gconv_output_dims, gconv_workspace_size, gconv_select_path,
-gconv_set_path_override.
+gconv_set_path_override; gconv_linattn_fwd, gconv_linattn_bwd,
+gconv_linattn_step.
 """
 from __future__ import annotations
 
@@ -26,13 +28,16 @@ OP_FWD, OP_BWD_DATA, OP_BWD_FILTER, OP_BWD_BIAS = 0, 1, 2, 3
 PATH_AUTO, PATH_DIRECT, PATH_SMALLGROUP, PATH_IGEMM, PATH_FC, PATH_POINTWISE = 0, 1, 2, 3, 4, 5
 EPILOGUE_NONE, EPILOGUE_RELU = 0, 1
 LAYOUT_NCHW, LAYOUT_NHWC = 0, 1
+F32, BF16 = 0, 1
+LINATTN_FWD, LINATTN_BWD = 0, 1
 PATH_NAMES = {PATH_AUTO: "auto", PATH_DIRECT: "direct", PATH_SMALLGROUP: "smallgroup",
               PATH_IGEMM: "igemm", PATH_FC: "fc", PATH_POINTWISE: "pointwise"}
 
 # Every symbol include/gconv.h declares.
 EXPORTS = ("gconv_output_dims", "gconv_workspace_size", "gconv_fwd", "gconv_fwd_ex", "gconv_bwd_data",
            "gconv_bwd_filter", "gconv_bwd_filter_static", "gconv_bwd_bias", "gconv_select_path",
-           "gconv_set_path_override", "gconv_status_string", "gconv_last_error", "gconv_version")
+           "gconv_set_path_override", "gconv_status_string", "gconv_last_error", "gconv_version",
+           "gconv_linattn_workspace_size", "gconv_linattn_fwd", "gconv_linattn_bwd", "gconv_linattn_step")
 
 
 class GconvError(RuntimeError):
@@ -46,6 +51,13 @@ class gconv_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in (
         "N", "C", "H", "W", "K", "kh", "kw", "stride_h", "stride_w", "pad_h", "pad_w",
         "dil_h", "dil_w", "groups", "pad_h_extra", "pad_w_extra", "layout")]
+
+
+class gconv_linattn_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "packed", "sequences", "tokens", "heads",
+                                               "kv_heads", "dk", "dv")] +
+                [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "do_stride")] +
+                [("scale", ctypes.c_double)])
 
 
 _lib = None
@@ -77,6 +89,10 @@ def load(path: str = LIB_PATH):
         "gconv_status_string": [I],
         "gconv_last_error": [],
         "gconv_version": [],
+        "gconv_linattn_workspace_size": [ctypes.POINTER(gconv_linattn_desc), I, ctypes.POINTER(S)],
+        "gconv_linattn_fwd": [ctypes.POINTER(gconv_linattn_desc)] + [P] * 9 + [S, P],
+        "gconv_linattn_bwd": [ctypes.POINTER(gconv_linattn_desc)] + [P] * 13 + [S, P],
+        "gconv_linattn_step": [ctypes.POINTER(gconv_linattn_desc)] + [P] * 6 + [ctypes.c_int64, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -397,3 +413,182 @@ class Plan:
         ws, nws, st = cls._prep(desc, OP_BWD_BIAS, dy.device, workspace)
         return cls("gconv_bwd_bias", (ctypes.byref(desc), _ptr(dy), _ptr(db), _ptr(ws), nws, st),
                    (desc, dy, db, ws))
+
+
+# ---------------------------------------------------------------- sequence operators
+
+def _seq(t, name, dtype=None, device=None):
+    """A GPU tensor of float32 or bfloat16 (of `dtype`, on `device`, if given)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a torch.Tensor" % name)
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU, got %s" % (name, t.device))
+    if device is not None and t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    return t
+
+
+def _dense(t, name, shape, dtype, device):
+    """A contiguous GPU tensor of one shape and type."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.device != device or not t.is_cuda:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
+def _dtype_code(t):
+    return BF16 if t.dtype == _torch().bfloat16 else F32
+
+
+def _last_axis(t, name):
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("the last axis of %s must be contiguous" % name)
+
+
+def _scratch(nbytes, device, workspace):
+    if workspace is not None:
+        have = workspace.numel() * workspace.element_size()
+        if have < nbytes:
+            raise ValueError("workspace holds %d bytes, %d needed" % (have, nbytes))
+        return workspace, have
+    if nbytes == 0:
+        return None, 0
+    torch = _torch()
+    return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+
+
+def _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state, do=None):
+    """Checks that the forward and the backward pass share; the descriptor and (N, state shape)."""
+    torch = _torch()
+    _seq(q, "q")
+    packed = cu_seqlens is not None
+    lead = 1 if packed else 2
+    for t, name in ((k, "k"), (v, "v")):
+        _seq(t, name, q.dtype, q.device)
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dim() != lead + 2:
+            raise ValueError("%s must be %s" % (name, "[T, heads, d] with cu_seqlens" if packed else "[N, T, heads, d]"))
+        _last_axis(t, name)
+        if t.shape[:lead] != q.shape[:lead]:
+            raise ValueError("%s has %s tokens, q %s" % (name, tuple(t.shape[:lead]), tuple(q.shape[:lead])))
+    H, dk = q.shape[-2:]
+    Hk, dv = v.shape[-2:]
+    if k.shape[-2] != Hk or k.shape[-1] != dk:
+        raise ValueError("k has heads and size %s, expected %s" % (tuple(k.shape[-2:]), (Hk, dk)))
+    _dense(log_decay, "log_decay", (H,), torch.float32, q.device)
+    if packed:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [sequences + 1]")
+        _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, q.device)
+    N = cu_seqlens.numel() - 1 if packed else q.shape[0]
+    states = (N, H, dk, dv)
+    if initial_state is not None:
+        _dense(initial_state, "initial_state", states, torch.float32, q.device)
+
+    def stride(t):
+        return (0,) + t.stride()[:2] if packed else t.stride()[:3]
+
+    i3 = ctypes.c_int64 * 3
+    if scale is None:
+        scale = dk ** -0.5
+    d = gconv_linattn_desc(_dtype_code(q), int(packed), N, q.shape[lead - 1], H, Hk, dk, dv, i3(*stride(q)), i3(*stride(k)),
+                           i3(*stride(v)), i3(), float(scale))
+    if do is not None:
+        _seq(do, "do", q.dtype, q.device)
+        if do.shape != q.shape[:-1] + (dv,):
+            raise ValueError("do has shape %s, expected %s" % (tuple(do.shape), tuple(q.shape[:-1]) + (dv,)))
+        _last_axis(do, "do")
+        d.do_stride = i3(*stride(do))
+    return d, states
+
+
+def gconv_linattn_workspace_size(desc: gconv_linattn_desc, op: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gconv_linattn_workspace_size(ctypes.byref(desc), int(op), ctypes.byref(n)),
+           "gconv_linattn_workspace_size")
+    return n.value
+
+
+def gconv_linattn_fwd(q, k, v, log_decay, *, scale=None, cu_seqlens=None, initial_state=None, workspace=None):
+    """Linear attention with a decay for each head: S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,
+    o_t = scale q_t S_t. q [N, T, H, dk], k [N, T, Hk, dk], v [N, T, Hk, dv] (H a multiple of Hk;
+    float32 or bfloat16, any strides with a contiguous last axis), or [T, heads, d] with
+    cu_seqlens (int32 [N + 1]) where sequences are packed. log_decay [H] float32; scale
+    defaults to dk^-0.5; initial_state [N, H, dk, dv] float32 or None.
+    Returns o (q's type) and the final state [N, H, dk, dv] float32."""
+    torch = _torch()
+    d, states = _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state)
+    o = torch.empty(q.shape[:-1] + (states[3],), dtype=q.dtype, device=q.device)
+    final = torch.empty(states, dtype=torch.float32, device=q.device)
+    ws, nws = _scratch(gconv_linattn_workspace_size(d, LINATTN_FWD), q.device, workspace)
+    _check(load().gconv_linattn_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens),
+                                    _ptr(initial_state), _ptr(o), _ptr(final), _ptr(ws), nws, _stream(q.device)),
+           "gconv_linattn_fwd")
+    return o, final
+
+
+def gconv_linattn_bwd(do, q, k, v, log_decay, *, scale=None, cu_seqlens=None, initial_state=None,
+                      d_final_state=None, workspace=None):
+    """Gradients of gconv_linattn_fwd for the gradient `do` of o and `d_final_state` of the final
+    state (None: 0). Returns dq, dk, dv (inputs' type and shape, dense) and the gradient of
+    initial_state (None if that is None)."""
+    torch = _torch()
+    d, states = _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state, do)
+    if d_final_state is not None:
+        _dense(d_final_state, "d_final_state", states, torch.float32, q.device)
+    dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+    ds = torch.empty(states, dtype=torch.float32, device=q.device) if initial_state is not None else None
+    ws, nws = _scratch(gconv_linattn_workspace_size(d, LINATTN_BWD), q.device, workspace)
+    _check(load().gconv_linattn_bwd(ctypes.byref(d), _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                    _ptr(cu_seqlens), _ptr(initial_state), _ptr(d_final_state), _ptr(dq), _ptr(dk),
+                                    _ptr(dv), _ptr(ds), _ptr(ws), nws, _stream(q.device)), "gconv_linattn_bwd")
+    return dq, dk, dv, ds
+
+
+def gconv_linattn_step(q, k, v, log_decay, state, *, scale=None, slots=None, out=None):
+    """One token of each of B sequences, in place on `state`: q [B, H, dk], k [B, Hk, dk],
+    v [B, Hk, dv] (float32 or bfloat16, any strides with a contiguous last axis), state
+    [slots, H, dk, dv] float32, slots int32 [B] (different ones; one out of range gives o = 0
+    and touches no state) or None for slot b. Returns o [B, H, dv]."""
+    torch = _torch()
+    _seq(q, "q")
+    for t, name in ((k, "k"), (v, "v")):
+        _seq(t, name, q.dtype, q.device)
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dim() != 3 or t.shape[0] != q.shape[0]:
+            raise ValueError("%s must be [B, heads, d]" % name)
+        _last_axis(t, name)
+    B, H, dk = q.shape
+    Hk, dv = v.shape[1:]
+    if k.shape[1] != Hk or k.shape[2] != dk:
+        raise ValueError("k has heads and size %s, expected %s" % (tuple(k.shape[1:]), (Hk, dk)))
+    _dense(log_decay, "log_decay", (H,), torch.float32, q.device)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be [slots, H, dk, dv]")
+    _dense(state, "state", (state.shape[0], H, dk, dv), torch.float32, q.device)
+    if slots is not None:
+        _dense(slots, "slots", (B,), torch.int32, q.device)
+    if out is None:
+        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+    else:
+        _dense(out, "out", (B, H, dv), q.dtype, q.device)
+    i3 = ctypes.c_int64 * 3
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    d = gconv_linattn_desc(_dtype_code(q), 0, B, 0, H, Hk, dk, dv, i3(sq[0], 0, sq[1]), i3(sk[0], 0, sk[1]),
+                           i3(sv[0], 0, sv[1]), i3(), float(dk ** -0.5 if scale is None else scale))
+    _check(load().gconv_linattn_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state),
+                                     _ptr(slots), state.shape[0], _ptr(out), _stream(q.device)), "gconv_linattn_step")
+    return out

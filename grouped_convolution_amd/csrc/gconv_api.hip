@@ -14,10 +14,8 @@
 #include "gconv_internal.h"
 
 namespace gconv {
-namespace {
 
-thread_local std::string g_last_error;
-std::atomic<int> g_path_override{GCONV_PATH_AUTO};
+static thread_local std::string g_last_error;
 
 int fail(int status, const char* fmt, ...)
 {
@@ -29,6 +27,18 @@ int fail(int status, const char* fmt, ...)
     g_last_error = buf;
     return status;
 }
+
+int finish()
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(GCONV_ERR_HIP, "HIP launch failed: %s", hipGetErrorString(e));
+    g_last_error.clear();
+    return GCONV_OK;
+}
+
+namespace {
+
+std::atomic<int> g_path_override{GCONV_PATH_AUTO};
 
 // Output extent with p0 zero rows before the input and p1 after it.
 int64_t out_extent(int64_t in, int64_t k, int64_t s, int64_t p0, int64_t p1, int64_t d)
@@ -449,14 +459,6 @@ int scratch_address(hipStream_t stream, void** out)
     return GCONV_OK;
 }
 
-int epilogue()
-{
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return fail(GCONV_ERR_HIP, "HIP launch failed: %s", hipGetErrorString(e));
-    g_last_error.clear();
-    return GCONV_OK;
-}
-
 }  // namespace
 }  // namespace gconv
 
@@ -531,7 +533,7 @@ int gconv_fwd_ex(const gconv_desc* d, const float* x, const float* w, const floa
         return fail(GCONV_ERR_ARG, "y overlaps an input");
     hipStream_t hs = (hipStream_t)stream;
     (void)hipGetLastError();
-    if (s.N == 0) return epilogue();
+    if (s.N == 0) return finish();
     if (p.native) {
         Shape sr = s;
         sr.relu = p.e.relu;
@@ -548,7 +550,7 @@ int gconv_fwd_ex(const gconv_desc* d, const float* x, const float* w, const floa
             // The flat MFMA kernel reads x and stores y channels-last itself.
             if (!igemm_fwd_nhwc_io(p.e, x, w, bias, y, hs))
                 st = fail(GCONV_ERR_UNSUPPORTED, "no MFMA kernel instance for this shape");
-            return st != GCONV_OK ? st : epilogue();
+            return st != GCONV_OK ? st : finish();
         }
         st = reorder(x, xs, s.N, (int64_t)s.H * s.W, s.C, hs);
         // The flat MFMA kernel stores y channels-last itself.
@@ -560,7 +562,7 @@ int gconv_fwd_ex(const gconv_desc* d, const float* x, const float* w, const floa
             if (st == GCONV_OK) st = reorder(ys, y, s.N, s.K, (int64_t)s.Ho * s.Wo, hs);
         }
     }
-    return st != GCONV_OK ? st : epilogue();
+    return st != GCONV_OK ? st : finish();
 }
 
 int gconv_bwd_data(const gconv_desc* d, const float* dy, const float* w, float* dx,
@@ -576,7 +578,7 @@ int gconv_bwd_data(const gconv_desc* d, const float* dy, const float* w, float* 
         return fail(GCONV_ERR_ARG, "dx overlaps an input");
     hipStream_t hs = (hipStream_t)stream;
     (void)hipGetLastError();
-    if (s.N == 0) return epilogue();
+    if (s.N == 0) return finish();
     if (p.native) {
         dw_nhwc_bwd_data(s, dy, w, dx, hs);
     } else if (!p.staged) {
@@ -591,7 +593,7 @@ int gconv_bwd_data(const gconv_desc* d, const float* dy, const float* w, float* 
             // The flat MFMA kernel reads dy and stores dx channels-last itself.
             if (!igemm_bwd_data_nhwc_io(p.e, dy, w, dx, hs))
                 st = fail(GCONV_ERR_UNSUPPORTED, "no MFMA kernel instance for this shape");
-            return st != GCONV_OK ? st : epilogue();
+            return st != GCONV_OK ? st : finish();
         }
         st = reorder(dy, dys, s.N, (int64_t)s.Ho * s.Wo, s.K, hs);
         if (st == GCONV_OK && p.path == GCONV_PATH_IGEMM && igemm_nhwc_out_supported(p.e, GCONV_OP_BWD_DATA)) {
@@ -602,7 +604,7 @@ int gconv_bwd_data(const gconv_desc* d, const float* dy, const float* w, float* 
             if (st == GCONV_OK) st = reorder(dxs, dx, s.N, s.C, (int64_t)s.H * s.W, hs);
         }
     }
-    return st != GCONV_OK ? st : epilogue();
+    return st != GCONV_OK ? st : finish();
 }
 
 int gconv_bwd_filter(const gconv_desc* d, const float* x, const float* dy, float* dw,
@@ -620,7 +622,7 @@ int gconv_bwd_filter(const gconv_desc* d, const float* x, const float* dy, float
     (void)hipGetLastError();
     if (s.N == 0) {
         fill_zero(dw, s.w_elems, hs);  // a sum over no images
-        return epilogue();
+        return finish();
     }
     if (p.native) {
         if (!dw_nhwc_bwd_filter(s, x, dy, dw, (float*)workspace, hs))
@@ -641,7 +643,7 @@ int gconv_bwd_filter(const gconv_desc* d, const float* x, const float* dy, float
         if (st == GCONV_OK) st = reorder(dy, dys, s.N, (int64_t)s.Ho * s.Wo, s.K, hs);
         if (st == GCONV_OK) st = run_bwd_filter(p.e, p.path, xs, dys, dw, rest, hs);
     }
-    return st != GCONV_OK ? st : epilogue();
+    return st != GCONV_OK ? st : finish();
 }
 
 int gconv_bwd_filter_static(const gconv_desc* d, const float* x, const float* dy, float* dw, void* stream)
@@ -671,11 +673,11 @@ int gconv_bwd_bias(const gconv_desc* d, const float* dy, float* db, void* worksp
     (void)hipGetLastError();
     if (s.N == 0) {
         fill_zero(db, s.K, hs);
-        return epilogue();
+        return finish();
     }
     // NHWC: the effective shape reads dy as [N*Ho*Wo, K] rows.
     bias_reduce(p.e, dy, db, (float*)workspace, hs);
-    return epilogue();
+    return finish();
 }
 
 const char* gconv_status_string(int status)

@@ -9,6 +9,11 @@
 
 namespace gconv {
 
+// Record the calling thread's last error and return `status`; finish() ends a
+// successful call: GCONV_OK with the error cleared, or a failed launch's status.
+int fail(int status, const char* fmt, ...);
+int finish();
+
 // A validated descriptor with the derived quantities every kernel needs.
 // 32-bit fields: the dispatcher refuses extents that do not fit.
 struct Shape {

@@ -251,6 +251,90 @@ const char* gconv_last_error(void);
 /* Library version: major*10000 + minor*100 + patch. */
 int gconv_version(void);
 
+/* ---- sequence operators ---------------------------------------------------
+ *
+ * Operators that stand next to 1x1 convolutions in sequence models: linear
+ * attention with a decay for each head, the gated norm around a block, and
+ * the orthogonalised update of a weight gradient. The conventions above hold
+ * (the caller owns every buffer, the stream, determinism, errors before
+ * anything is enqueued); tensors have one of two element types.
+ */
+typedef enum gconv_dtype {
+    GCONV_F32 = 0,
+    GCONV_BF16 = 1
+} gconv_dtype;
+
+/*
+ * Linear attention with a decay for each head. For a sequence of L tokens and
+ * a head h with lambda = exp(log_decay[h]), a state S (dk x dv, float32) that
+ * starts at initial_state (0 if that is NULL) takes in every token and then
+ * answers its query:
+ *
+ *   S_t = lambda S_{t-1} + k_t v_t^T        o_t = scale q_t S_t
+ *
+ * so that o_t = scale (sum_{j<=t} lambda^(t-j) (q_t . k_j) v_j
+ *                      + lambda^(t+1) q_t S_init), t from 0, and the final state is S_{L-1}.
+ * An infinity or a NaN in a later token does not reach an earlier one.
+ *
+ * Heads: q, o have `heads`; k, v have `kv_heads`, each shared by
+ * heads / kv_heads consecutive heads. States are per q head.
+ * Sequences: with packed == 0, `sequences` of `tokens` each. With packed != 0
+ * the tokens of all sequences follow one another, `tokens` in all, and
+ * cu_seqlens (int32, device memory, sequences + 1 values from 0 to `tokens`,
+ * not decreasing) says where each begins; a sequence may be empty.
+ * Strides are in elements: [0] between sequences (not read when packed), [1]
+ * between tokens, [2] between heads; the last axis is contiguous. Outputs
+ * are dense, [sequences, tokens, heads, d] or [tokens, heads, d].
+ * dk, dv from 1 to 128. log_decay [heads] float32; -infinity (no memory) and
+ * values above 0 (growth) are valid. States [sequences, heads, dk, dv]
+ * float32, dense.
+ */
+typedef struct gconv_linattn_desc {
+    int64_t dtype;              /* gconv_dtype of q, k, v, o and their gradients */
+    int64_t packed;
+    int64_t sequences, tokens;
+    int64_t heads, kv_heads;
+    int64_t dk, dv;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    int64_t do_stride[3];       /* of the gradient of o; read by gconv_linattn_bwd only */
+    double scale;
+} gconv_linattn_desc;
+
+typedef enum gconv_linattn_op {
+    GCONV_LINATTN_FWD = 0,
+    GCONV_LINATTN_BWD = 1
+} gconv_linattn_op;
+
+/* Bytes of workspace `op` (a gconv_linattn_op) needs, 16-byte aligned. */
+int gconv_linattn_workspace_size(const gconv_linattn_desc* d, int op, size_t* bytes);
+
+/* o and the final states of whole sequences. initial_state and final_state may be NULL. */
+int gconv_linattn_fwd(const gconv_linattn_desc* d, const void* q, const void* k, const void* v, const float* log_decay,
+                      const int32_t* cu_seqlens, const float* initial_state, void* o, float* final_state,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients for the gradient dout of o and d_final_state of the final state
+ * (NULL: 0): dq, dk, dv (dense, of the inputs' type; those of a shared head
+ * are summed over the heads that share it) and d_initial_state (may be NULL).
+ * initial_state as in the forward pass.
+ */
+int gconv_linattn_bwd(const gconv_linattn_desc* d, const void* dout, const void* q, const void* k, const void* v,
+                      const float* log_decay, const int32_t* cu_seqlens, const float* initial_state,
+                      const float* d_final_state, void* dq, void* dk, void* dv, float* d_initial_state,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of each of `sequences` sequences (packed and tokens are 0): takes
+ * the token into the state, in place, and answers its query. state is a pool
+ * of num_slots states [num_slots, heads, dk, dv]; sequence i uses number
+ * slots[i] (int32, device memory), or i where slots is NULL. Slots of one call
+ * must differ. A slot outside 0..num_slots-1 (say, -1 for an idle row) gives
+ * o = 0 and touches no state. Strides [1] are not read.
+ */
+int gconv_linattn_step(const gconv_linattn_desc* d, const void* q, const void* k, const void* v, const float* log_decay,
+                       float* state, const int32_t* slots, int64_t num_slots, void* o, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
