@@ -10,7 +10,7 @@ first call raises; there is no fallback.
 Names mirror the C entry points: gconv_fwd, gconv_bwd_data, gconv_bwd_filter,
 gconv_bwd_bias, gconv_output_dims, gconv_workspace_size, gconv_select_path,
 gconv_set_path_override; gconv_linattn_fwd, gconv_linattn_bwd,
-gconv_linattn_step.
+gconv_linattn_step, gconv_normgate_fwd, gconv_normgate_bwd.
 """
 from __future__ import annotations
 
@@ -30,6 +30,8 @@ EPILOGUE_NONE, EPILOGUE_RELU = 0, 1
 LAYOUT_NCHW, LAYOUT_NHWC = 0, 1
 F32, BF16 = 0, 1
 LINATTN_FWD, LINATTN_BWD = 0, 1
+GATE_NONE, GATE_FULL, GATE_SEQUENCE = 0, 1, 2
+ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 PATH_NAMES = {PATH_AUTO: "auto", PATH_DIRECT: "direct", PATH_SMALLGROUP: "smallgroup",
               PATH_IGEMM: "igemm", PATH_FC: "fc", PATH_POINTWISE: "pointwise"}
 
@@ -37,7 +39,8 @@ PATH_NAMES = {PATH_AUTO: "auto", PATH_DIRECT: "direct", PATH_SMALLGROUP: "smallg
 EXPORTS = ("gconv_output_dims", "gconv_workspace_size", "gconv_fwd", "gconv_fwd_ex", "gconv_bwd_data",
            "gconv_bwd_filter", "gconv_bwd_filter_static", "gconv_bwd_bias", "gconv_select_path",
            "gconv_set_path_override", "gconv_status_string", "gconv_last_error", "gconv_version",
-           "gconv_linattn_workspace_size", "gconv_linattn_fwd", "gconv_linattn_bwd", "gconv_linattn_step")
+           "gconv_linattn_workspace_size", "gconv_linattn_fwd", "gconv_linattn_bwd", "gconv_linattn_step",
+           "gconv_normgate_workspace_size", "gconv_normgate_fwd", "gconv_normgate_bwd")
 
 
 class GconvError(RuntimeError):
@@ -58,6 +61,12 @@ class gconv_linattn_desc(ctypes.Structure):
                                                "kv_heads", "dk", "dv")] +
                 [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "do_stride")] +
                 [("scale", ctypes.c_double)])
+
+
+class gconv_normgate_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "sequences", "tokens", "dim", "gate", "act")] +
+                [(n, ctypes.c_int64 * 2) for n in ("x_stride", "b_stride", "gate_stride", "dy_stride", "dh_stride")] +
+                [("eps", ctypes.c_double)])
 
 
 _lib = None
@@ -93,6 +102,9 @@ def load(path: str = LIB_PATH):
         "gconv_linattn_fwd": [ctypes.POINTER(gconv_linattn_desc)] + [P] * 9 + [S, P],
         "gconv_linattn_bwd": [ctypes.POINTER(gconv_linattn_desc)] + [P] * 13 + [S, P],
         "gconv_linattn_step": [ctypes.POINTER(gconv_linattn_desc)] + [P] * 6 + [ctypes.c_int64, P, P],
+        "gconv_normgate_workspace_size": [ctypes.POINTER(gconv_normgate_desc), ctypes.POINTER(S)],
+        "gconv_normgate_fwd": [ctypes.POINTER(gconv_normgate_desc)] + [P] * 9,
+        "gconv_normgate_bwd": [ctypes.POINTER(gconv_normgate_desc)] + [P] * 15 + [S, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -592,3 +604,72 @@ def gconv_linattn_step(q, k, v, log_decay, state, *, scale=None, slots=None, out
     _check(load().gconv_linattn_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state),
                                      _ptr(slots), state.shape[0], _ptr(out), _stream(q.device)), "gconv_linattn_step")
     return out
+
+
+def _normgate_desc(x, b, gate, act, w_post, scale, w_pre, eps, dy=None, dh=None):
+    """Checks that the forward and the backward pass share; the descriptor."""
+    _seq(b, "b")
+    if b.dim() < 2:
+        raise ValueError("b must be [N, T, D] or [T, D]")
+    if b.dim() > 3:
+        raise ValueError("b has %d axes, at most 3 are taken" % b.dim())
+    dim = b.shape[-1]
+    N, T = (b.shape[0], b.shape[1]) if b.dim() == 3 else (1, b.shape[0])
+    if act not in ACTS:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(sorted(ACTS)), act))
+    kind = GATE_NONE
+    i2 = ctypes.c_int64 * 2
+
+    def stride(t, name, shape):
+        if t is None:
+            return i2()
+        _seq(t, name, b.dtype, b.device)
+        if t.shape != shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+        _last_axis(t, name)
+        return i2(*(t.stride()[:2] if t.dim() == 3 else (0, t.stride(0))))
+
+    gshape = b.shape
+    if gate is not None:
+        kind = GATE_FULL
+        if isinstance(gate, _torch().Tensor) and gate.shape != b.shape:
+            kind, gshape = GATE_SEQUENCE, b.shape[:-2] + (1, dim)
+    for w, name in ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")):
+        if w is not None or name == "w_post":
+            _dense(w, name, (dim,), b.dtype, b.device)
+    return gconv_normgate_desc(_dtype_code(b), N, T, dim, kind, ACTS[act], stride(x, "x", b.shape), stride(b, "b", b.shape),
+                               stride(gate, "gate", gshape), stride(dy, "dy", b.shape), stride(dh, "dh", b.shape), float(eps))
+
+
+def gconv_normgate_fwd(x, b, *, w_post, gate=None, act="silu", scale=None, w_pre=None, eps=1e-6):
+    """The norms around a block: y = x + scale * act(gate) * rmsnorm(b) * w_post and
+    h = rmsnorm(y) * w_pre, over the last axis. b [N, T, D] or [T, D] (float32 or bfloat16, any
+    strides with a contiguous last axis); x like b or None; gate like b, or [N, 1, D] ([1, D])
+    for one row a sequence, or None; act "none", "sigmoid" or "silu"; w_post, scale, w_pre [D],
+    the last two may be None. Returns y and h (None without w_pre)."""
+    torch = _torch()
+    d = _normgate_desc(x, b, gate, act, w_post, scale, w_pre, eps)
+    y = torch.empty(b.shape, dtype=b.dtype, device=b.device)
+    h = torch.empty(b.shape, dtype=b.dtype, device=b.device) if w_pre is not None else None
+    _check(load().gconv_normgate_fwd(ctypes.byref(d), _ptr(x), _ptr(b), _ptr(gate), _ptr(w_post), _ptr(scale), _ptr(w_pre),
+                                     _ptr(y), _ptr(h), _stream(b.device)), "gconv_normgate_fwd")
+    return y, h
+
+
+def gconv_normgate_bwd(dy, dh, x, b, *, w_post, gate=None, act="silu", scale=None, w_pre=None, eps=1e-6, workspace=None):
+    """Gradients of gconv_normgate_fwd for dy of y and dh of h (None without w_pre). Returns
+    dx, db, dgate, dw_post, dscale, dw_pre, of the inputs' shapes and type (None for those that
+    are None)."""
+    torch = _torch()
+    d = _normgate_desc(x, b, gate, act, w_post, scale, w_pre, eps, _seq(dy, "dy"), dh)
+    if (dh is None) != (w_pre is None):
+        raise ValueError("dh must be given exactly when w_pre is")
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device) if t is not None else None  # noqa: E731
+    dx, db, dgate, dw_post, dscale, dw_pre = (new(t) for t in (x, b, gate, w_post, scale, w_pre))
+    n = ctypes.c_size_t()
+    _check(load().gconv_normgate_workspace_size(ctypes.byref(d), ctypes.byref(n)), "gconv_normgate_workspace_size")
+    ws, nws = _scratch(n.value, b.device, workspace)
+    _check(load().gconv_normgate_bwd(ctypes.byref(d), _ptr(dy), _ptr(dh), _ptr(x), _ptr(b), _ptr(gate), _ptr(w_post),
+                                     _ptr(scale), _ptr(w_pre), _ptr(dx), _ptr(db), _ptr(dgate), _ptr(dw_post), _ptr(dscale),
+                                     _ptr(dw_pre), _ptr(ws), nws, _stream(b.device)), "gconv_normgate_bwd")
+    return dx, db, dgate, dw_post, dscale, dw_pre

@@ -335,6 +335,57 @@ int gconv_linattn_bwd(const gconv_linattn_desc* d, const void* dout, const void*
 int gconv_linattn_step(const gconv_linattn_desc* d, const void* q, const void* k, const void* v, const float* log_decay,
                        float* state, const int32_t* slots, int64_t num_slots, void* o, void* stream);
 
+/*
+ * The norms before and after a block, with its gate and its residual scale:
+ *
+ *   y = x + scale * act(gate) * rmsnorm(b) * w_post      h = rmsnorm(y) * w_pre
+ *   rmsnorm(v) = v / sqrt(mean(v^2) + eps) over the last axis (`dim`)
+ *
+ * b is what the block gave, x the residual stream, h the next block's input.
+ * x, gate, scale, w_pre (and with it h) may be absent. h is taken from y
+ * before y is rounded to its type. Tensors [sequences, tokens, dim], strides
+ * in elements ([0] between sequences, [1] between tokens, the last axis
+ * contiguous); a gate of GCONV_GATE_SEQUENCE is one row for each sequence.
+ * Weights [dim] of the same type; outputs dense. dim up to 8192.
+ */
+typedef enum gconv_gate {
+    GCONV_GATE_NONE = 0,
+    GCONV_GATE_FULL = 1,      /* a gate for every element of b */
+    GCONV_GATE_SEQUENCE = 2   /* a row of gates for each sequence */
+} gconv_gate;
+
+typedef enum gconv_act {
+    GCONV_ACT_NONE = 0,       /* act(z) = z */
+    GCONV_ACT_SIGMOID = 1,    /* 1 / (1 + exp(-z)) */
+    GCONV_ACT_SILU = 2        /* z / (1 + exp(-z)) */
+} gconv_act;
+
+typedef struct gconv_normgate_desc {
+    int64_t dtype;            /* gconv_dtype of every tensor and weight */
+    int64_t sequences, tokens, dim;
+    int64_t gate, act;        /* gconv_gate, gconv_act */
+    int64_t x_stride[2], b_stride[2], gate_stride[2];
+    int64_t dy_stride[2], dh_stride[2];  /* read by gconv_normgate_bwd only */
+    double eps;
+} gconv_normgate_desc;
+
+/* Bytes of workspace gconv_normgate_bwd needs, 16-byte aligned (the forward pass needs none). */
+int gconv_normgate_workspace_size(const gconv_normgate_desc* d, size_t* bytes);
+
+int gconv_normgate_fwd(const gconv_normgate_desc* d, const void* x, const void* b, const void* gate, const void* w_post,
+                       const void* scale, const void* w_pre, void* y, void* h, void* stream);
+
+/*
+ * Gradients for dy of y and dh of h (given exactly when w_pre is). dx, db and
+ * a full gate's dgate are dense; dgate of a gate for each sequence is
+ * [sequences, dim], summed over its tokens. The weights' gradients are summed
+ * over all rows in float32 and rounded once. dx may be NULL; the others are
+ * given exactly when their inputs are.
+ */
+int gconv_normgate_bwd(const gconv_normgate_desc* d, const void* dy, const void* dh, const void* x, const void* b, const void* gate,
+                       const void* w_post, const void* scale, const void* w_pre, void* dx, void* db, void* dgate, void* dw_post,
+                       void* dscale, void* dw_pre, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,3 +35,57 @@ def check_mag(name, got, want, mag, rtol, atol=0.0):
     assert ratio.flatten()[i] <= 1, "%s: element %d got %r want %r mag %r: %.3g of the bound" % (
         name, i, got.flatten()[i].item(), want.flatten()[i].item(), mag.flatten()[i].item(), ratio.flatten()[i].item())
     return float(ratio.flatten()[i])
+
+
+def _act(z, act):
+    """act(z), its derivative, and the magnitude of the derivative's terms."""
+    s = 1 / (1 + torch.exp(-z))
+    if act == "none":
+        return z, torch.ones_like(z), torch.ones_like(z)
+    if act == "sigmoid":
+        return s, s * (1 - s), s * (1 - s)
+    return z * s, s + z * s * (1 - s), s + z.abs() * s * (1 - s)
+
+
+def normgate(x, b, gate, act, w_post, scale, w_pre, eps, dy=None, dh=None):
+    """The norms around a block and their gradients in 64 bits, [N, T, D]; {name: (value, magnitude of
+    its terms)}, from the formulas (not by autograd)."""
+    b = b.to(F64)
+    one = torch.ones(b.shape[-1], dtype=F64)
+    z = gate.to(F64).expand_as(b) if gate is not None else None
+    wp, sc = w_post.to(F64), scale.to(F64) if scale is not None else one
+    rb = (b.square().mean(-1, keepdim=True) + eps) ** -0.5
+    bn = b * rb
+    n = bn * wp
+    a, da, da_m = _act(z, act) if z is not None else (torch.ones_like(b),) * 3
+    t = sc * a * n
+    y = t + (x.to(F64) if x is not None else 0)
+    y_m = t.abs() + (x.to(F64).abs() if x is not None else 0)
+    out = {"y": (y, y_m)}
+    if w_pre is not None:
+        wq = w_pre.to(F64)
+        ry = (y.square().mean(-1, keepdim=True) + eps) ** -0.5
+        yn, yn_m = y * ry, y_m * ry
+        out["h"] = (yn * wq, yn_m * wq.abs())
+    if dy is None:
+        return out
+    d = dy.to(F64)
+    d_m = d.abs()
+    if w_pre is not None:
+        e = dh.to(F64) * wq
+        d = d + ry * (e - yn * (e * yn).mean(-1, keepdim=True))
+        d_m = d_m + ry * (e.abs() + yn_m * (e.abs() * yn_m).mean(-1, keepdim=True))
+        out["dw_pre"] = ((dh.to(F64) * yn).sum((0, 1)), (dh.to(F64).abs() * yn_m).sum((0, 1)))
+    if x is not None:
+        out["dx"] = (d, d_m)
+    f, f_m = d * sc * a * wp, d_m * (sc * a * wp).abs()
+    out["db"] = (rb * (f - bn * (f * bn).mean(-1, keepdim=True)), rb * (f_m + bn.abs() * (f_m * bn.abs()).mean(-1, keepdim=True)))
+    if z is not None:
+        g, g_m = d * sc * n * da, d_m * (sc * n).abs() * da_m
+        if gate.shape != b.shape:
+            g, g_m = g.sum(1, keepdim=True), g_m.sum(1, keepdim=True)
+        out["dgate"] = (g, g_m)
+    out["dw_post"] = ((d * sc * a * bn).sum((0, 1)), (d_m * (sc * a * bn).abs()).sum((0, 1)))
+    if scale is not None:
+        out["dscale"] = ((d * a * n).sum((0, 1)), (d_m * (a * n).abs()).sum((0, 1)))
+    return out
