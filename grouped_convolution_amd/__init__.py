@@ -10,7 +10,7 @@ from .binding import (GconvError, Plan, LAYOUT_NCHW, LAYOUT_NHWC, OP_BWD_BIAS, O
                       PATH_DIRECT, PATH_FC, PATH_IGEMM, PATH_NAMES, PATH_POINTWISE, PATH_SMALLGROUP, gconv_bwd_bias,
                       gconv_bwd_data, gconv_bwd_filter, gconv_desc, gconv_fwd, gconv_output_dims,
                       gconv_linattn_bwd, gconv_linattn_fwd, gconv_linattn_step, gconv_normgate_bwd,
-                      gconv_normgate_fwd, gconv_select_path, gconv_set_path_override,
+                      gconv_normgate_fwd, gconv_orthogonalize, gconv_select_path, gconv_set_path_override,
                       gconv_workspace_size, make_desc, same_padding)
 
 __all__ = ["GconvError", "Plan", "gconv_desc", "make_desc", "gconv_fwd", "gconv_bwd_data",
@@ -19,4 +19,4 @@ __all__ = ["GconvError", "Plan", "gconv_desc", "make_desc", "gconv_fwd", "gconv_
            "OP_BWD_FILTER", "OP_BWD_BIAS", "PATH_AUTO", "PATH_DIRECT", "PATH_SMALLGROUP",
            "PATH_IGEMM", "PATH_FC", "PATH_POINTWISE", "PATH_NAMES", "same_padding", "LAYOUT_NCHW",
            "LAYOUT_NHWC", "gconv_linattn_fwd", "gconv_linattn_bwd", "gconv_linattn_step", "gconv_normgate_fwd",
-           "gconv_normgate_bwd"]
+           "gconv_normgate_bwd", "gconv_orthogonalize"]

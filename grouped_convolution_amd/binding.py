@@ -10,7 +10,7 @@ first call raises; there is no fallback.
 Names mirror the C entry points: gconv_fwd, gconv_bwd_data, gconv_bwd_filter,
 gconv_bwd_bias, gconv_output_dims, gconv_workspace_size, gconv_select_path,
 gconv_set_path_override; gconv_linattn_fwd, gconv_linattn_bwd,
-gconv_linattn_step, gconv_normgate_fwd, gconv_normgate_bwd.
+gconv_linattn_step, gconv_normgate_fwd, gconv_normgate_bwd, gconv_orthogonalize.
 """
 from __future__ import annotations
 
@@ -40,7 +40,8 @@ EXPORTS = ("gconv_output_dims", "gconv_workspace_size", "gconv_fwd", "gconv_fwd_
            "gconv_bwd_filter", "gconv_bwd_filter_static", "gconv_bwd_bias", "gconv_select_path",
            "gconv_set_path_override", "gconv_status_string", "gconv_last_error", "gconv_version",
            "gconv_linattn_workspace_size", "gconv_linattn_fwd", "gconv_linattn_bwd", "gconv_linattn_step",
-           "gconv_normgate_workspace_size", "gconv_normgate_fwd", "gconv_normgate_bwd")
+           "gconv_normgate_workspace_size", "gconv_normgate_fwd", "gconv_normgate_bwd",
+           "gconv_orthogonalize_workspace_size", "gconv_orthogonalize")
 
 
 class GconvError(RuntimeError):
@@ -66,6 +67,11 @@ class gconv_linattn_desc(ctypes.Structure):
 class gconv_normgate_desc(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "sequences", "tokens", "dim", "gate", "act")] +
                 [(n, ctypes.c_int64 * 2) for n in ("x_stride", "b_stride", "gate_stride", "dy_stride", "dh_stride")] +
+                [("eps", ctypes.c_double)])
+
+
+class gconv_ortho_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "filters", "inner", "groups", "steps")] +
                 [("eps", ctypes.c_double)])
 
 
@@ -105,6 +111,8 @@ def load(path: str = LIB_PATH):
         "gconv_normgate_workspace_size": [ctypes.POINTER(gconv_normgate_desc), ctypes.POINTER(S)],
         "gconv_normgate_fwd": [ctypes.POINTER(gconv_normgate_desc)] + [P] * 9,
         "gconv_normgate_bwd": [ctypes.POINTER(gconv_normgate_desc)] + [P] * 15 + [S, P],
+        "gconv_orthogonalize_workspace_size": [ctypes.POINTER(gconv_ortho_desc), ctypes.POINTER(S)],
+        "gconv_orthogonalize": [ctypes.POINTER(gconv_ortho_desc), P, P, P, S, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -673,3 +681,27 @@ def gconv_normgate_bwd(dy, dh, x, b, *, w_post, gate=None, act="silu", scale=Non
                                      _ptr(scale), _ptr(w_pre), _ptr(dx), _ptr(db), _ptr(dgate), _ptr(dw_post), _ptr(dscale),
                                      _ptr(dw_pre), _ptr(ws), nws, _stream(b.device)), "gconv_normgate_bwd")
     return dx, db, dgate, dw_post, dscale, dw_pre
+
+
+def gconv_orthogonalize(u, *, groups=1, steps=5, eps=1e-7, out=None, workspace=None):
+    """The orthogonalised update of a weight gradient u [K, C/groups, kh, kw] (or [K, D]; float32 or
+    bfloat16, contiguous): each group's [K/groups, C/groups kh kw] matrix, scaled to norm 1, after
+    `steps` rounds of the Newton-Schulz iteration. Returns a bfloat16 tensor of u's shape."""
+    torch = _torch()
+    _seq(u, "u")
+    if u.dim() < 2:
+        raise ValueError("u must be [K, ...] with at least two axes")
+    if not u.is_contiguous():
+        raise ValueError("u must be contiguous")
+    K = u.shape[0]
+    d = gconv_ortho_desc(_dtype_code(u), K, u.numel() // K if K else 0, int(groups), int(steps), float(eps))
+    n = ctypes.c_size_t()
+    _check(load().gconv_orthogonalize_workspace_size(ctypes.byref(d), ctypes.byref(n)), "gconv_orthogonalize_workspace_size")
+    if out is None:
+        out = torch.empty(u.shape, dtype=torch.bfloat16, device=u.device)
+    else:
+        _dense(out, "out", u.shape, torch.bfloat16, u.device)
+    ws, nws = _scratch(n.value, u.device, workspace)
+    _check(load().gconv_orthogonalize(ctypes.byref(d), _ptr(u), _ptr(out), _ptr(ws), nws, _stream(u.device)),
+           "gconv_orthogonalize")
+    return out

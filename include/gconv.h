@@ -386,6 +386,37 @@ int gconv_normgate_bwd(const gconv_normgate_desc* d, const void* dy, const void*
                        const void* w_post, const void* scale, const void* w_pre, void* dx, void* db, void* dgate, void* dw_post,
                        void* dscale, void* dw_pre, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The orthogonalised update of a weight gradient. Each group's gradient, the
+ * filters / groups x inner matrix U (inner: C/groups * kh * kw), is scaled to
+ * X = U / (norm(U) + eps) in the Frobenius norm and sent through `steps`
+ * rounds of the Newton-Schulz iteration
+ *
+ *   X <- a X + (b A + c A^2) X,  A = X X^T,  (a, b, c) = (3.4445, -4.7750, 2.0315)
+ *
+ * (of the transposed matrix where U has more rows than columns), after which
+ * its singular values lie around 1. u [filters][inner] dense, of either type;
+ * out [filters][inner] in bfloat16, 8-byte aligned. The iterates are rounded
+ * to fp16 between products, whose sums are float32: the result is within
+ * 2e-3 of the exact one in the norm, and the output's rounding. A group that
+ * holds an infinity or a NaN gives NaN, and the other groups their own
+ * results. A group's matrix, its longer side padded to 64, holds up to 2^29
+ * elements, and neither side is above 2^24.
+ */
+typedef struct gconv_ortho_desc {
+    int64_t dtype;            /* gconv_dtype of u */
+    int64_t filters, inner;
+    int64_t groups;
+    int64_t steps;            /* 1 to 1000 */
+    double eps;
+} gconv_ortho_desc;
+
+/* Bytes of workspace gconv_orthogonalize needs, 16-byte aligned. */
+int gconv_orthogonalize_workspace_size(const gconv_ortho_desc* d, size_t* bytes);
+
+int gconv_orthogonalize(const gconv_ortho_desc* d, const void* u, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -89,3 +89,18 @@ def normgate(x, b, gate, act, w_post, scale, w_pre, eps, dy=None, dh=None):
     if scale is not None:
         out["dscale"] = ((d * a * n).sum((0, 1)), (d_m * (a * n).abs()).sum((0, 1)))
     return out
+
+
+def orthogonalize(u, groups, steps, eps):
+    """Newton-Schulz rounds of each group's matrix, scaled to norm 1, in 64 bits; u [K, D]."""
+    a, b, c = 3.4445, -4.7750, 2.0315
+    out = []
+    for x in u.to(F64).chunk(groups):
+        tall = x.shape[0] > x.shape[1]
+        x = x.T if tall else x
+        x = x / (x.square().sum().sqrt() + eps)
+        for _ in range(steps):
+            g = x @ x.T
+            x = a * x + (b * g + c * (g @ g)) @ x
+        out.append(x.T if tall else x)
+    return torch.cat(out)
