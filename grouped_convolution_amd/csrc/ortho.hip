@@ -44,6 +44,11 @@ typedef __attribute__((address_space(3))) char lds_char;
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScale = 4096.f;  // of X, A and B as they are stored
 constexpr float kRest = 2048.f;    // of the rest of X, over X
+// Rounds before the end that take X without its rest: noise of 2^-12 grows
+// 12 times at most there, and without it the strong directions come out a
+// little closer (128 x 1200: 2.3e-3 off for 2.4e-3; rank one 3.3e-3, and
+// 1.4e-2 with one round more).
+constexpr int kRestSteps = 2;
 constexpr int kStepK = 64;        // reduction length of a stage
 
 enum Op { GRAM = 0, SQUARE = 1, UPDATE = 2 };
@@ -59,6 +64,7 @@ struct Ortho {
     int m, n, np, mp;  // np, mp: row pitches, multiples of 64 (zeros past n, m)
     int tq, tp;      // tiles along the rows and columns of the output
     int tall;        // the result is stored transposed, [n][m]
+    int read_rest, write_rest;
 };
 
 // 64 lanes' 16 bytes from global memory straight to 1024 bytes of LDS. In
@@ -68,6 +74,13 @@ __device__ __forceinline__ void copy_lds(u4 rsrc, uint32_t lds, uint32_t off)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :: "s"(lds), "v"(off), "s"(rsrc) : "memory");
+}
+
+// Waits until at most N of this wave's loads are still under way.
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
 }
 
 __device__ __forceinline__ u4 resource(const void* p, uint32_t bytes)
@@ -194,7 +207,9 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void ortho_gemm(Ortho a)
     using SQ = AlongRows<BQ, NW, FQ>;
     using SP = std::conditional_t<OP == UPDATE, AcrossRows<BP, NW, FP>, AlongRows<BP, NW, FP>>;
     constexpr int kBuf = SQ::kBytes + SP::kBytes;
-    __shared__ __align__(1024) char lds[2 * kBuf];
+    constexpr int kLoads = SQ::kLoads + SP::kLoads;
+    constexpr int kRing = std::min(3, 160 * 1024 / kBuf);  // stages that the LDS of a CU holds
+    __shared__ __align__(1024) char lds[kRing * kBuf];
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -230,110 +245,138 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void ortho_gemm(Ortho a)
         for (int j = 0; j < FP; ++j) acc[i][j] = f4{0, 0, 0, 0};
 
     const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_char*)lds;
-    auto issue = [&](uint32_t buf) {
-#pragma unroll
-        for (int i = 0; i < SQ::kLoads; ++i) sq.load(rq, lds_at + buf, i, wave);
-#pragma unroll
-        for (int i = 0; i < SP::kLoads; ++i) sp.load(rp, lds_at + buf + SQ::kBytes, i, wave);
+    auto issue = [&](int n, uint32_t buf) {  // load n of a stage
+        if (n < SQ::kLoads) sq.load(rq, lds_at + buf, n, wave);
+        else sp.load(rp, lds_at + buf + SQ::kBytes, n - SQ::kLoads, wave);
     };
     u4 fq[2][FQ], fp[2][FP];
-    auto read = [&](int ks, uint32_t buf) {
-#pragma unroll
-        for (int j = 0; j < FP; ++j) fp[ks][j] = sp.frag(lds + buf + SQ::kBytes, j, ks);
-#pragma unroll
-        for (int i = 0; i < FQ; ++i) fq[ks][i] = sq.frag(lds + buf, i, ks);
+    auto read = [&](int ks, int n, uint32_t buf) {  // fragment n of half ks of a stage
+        if (n < FP) fp[ks][n] = sp.frag(lds + buf + SQ::kBytes, n, ks);
+        else fq[ks][n - FP] = sq.frag(lds + buf, n - FP, ks);
     };
-    auto multiply = [&](int ks) {
+    // Half a stage: its products, and spread among them the reads of the next
+    // half's fragments and (second halves) the loads of a stage.
+    constexpr int kMmas = FQ * FP;
+    auto half = [&](int ks, uint32_t from, uint32_t into) {
+        int rd = 0, ld = 0;
 #pragma unroll
-        for (int i = 0; i < FQ; ++i)
-#pragma unroll
-            for (int j = 0; j < FP; ++j) acc[i][j] = mma16(fp[ks][j], fq[ks][i], acc[i][j]);
-    };
-    constexpr int kReads = FQ + (OP == UPDATE ? 2 : 1) * FP, kMmas = FQ * FP;
-    // one LDS read after every few products, all of them in the first two thirds
-    auto interleave = [&]() {
-#pragma unroll
-        for (int i = 0; i < kReads; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, kMmas * 2 / 3 / kReads, 0);
+        for (int n = 0; n < kMmas; ++n) {
+            if (rd < FQ + FP && n * (FQ + FP) * 3 >= rd * kMmas * 2) read(ks ^ 1, rd++, from);
+            if (ks == 1 && ld < kLoads && n * kLoads >= ld * kMmas) issue(ld++, into);
+            const int i = n / FP, j = n % FP;
+            acc[i][j] = mma16(fp[ks][j], fq[ks][i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, kMmas, 0);
     };
-    // One stage: its second half is read while the first is multiplied; then,
-    // with the next stage landed and this one read by all, the one after next
-    // goes into its place and the next stage's first half is read. Loads past
-    // the last stage are made (and lead nowhere), so the loop has no branch.
-    issue(0);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int st = 0; st < kRing; ++st)
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) issue(n, st * kBuf);
+    wait_loads<(kRing - 1) * kLoads>();
     __builtin_amdgcn_s_barrier();
-    issue(kBuf);
-    read(0, 0);
+#pragma unroll
+    for (int n = 0; n < FQ + FP; ++n) read(0, n, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    // In the middle of a stage the next one has landed and this one has been
+    // read by all waves, so the stage kRing on is loaded into its place. Loads
+    // past the last stage are made and lead nowhere.
     uint32_t cur = 0;
     for (int kt = 0; kt < kt_end; ++kt) {
-        const uint32_t next = kBuf - cur;
-        __builtin_amdgcn_sched_barrier(0);
-        read(1, cur);
-        multiply(0);
-        interleave();
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        const uint32_t next = cur + kBuf == kRing * kBuf ? 0 : cur + kBuf;
+        half(0, cur, 0);
+        wait_loads<(kRing - 2) * kLoads>();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        issue(cur);
-        read(0, next);
-        multiply(1);
-        interleave();
+        half(1, next, cur);
         cur = next;
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may land after the workgroup's end
+    wait_loads<0>();  // no load may land after the workgroup's end
 
-    h16* rest = a.rest + grp * a.xs;
-    h16* out = a.out + grp * (OP == UPDATE ? a.xs : a.ss);
+    // Buffer accesses with offsets past the end where an element is not there:
+    // no branches, so a row of fragments is loaded while the last is stored.
+    auto offset = [&](int row, int col, int rows, int pitch) {
+        return row < rows && col < pitch ? (uint32_t)((row * (int64_t)pitch + col) * 2) : kOOB;
+    };
+    const int row0 = i0 + wq * (BQ / WQ) + li, col0 = j0 + wp * (BP / WP) + 4 * g;
+    if constexpr (OP == UPDATE) {
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(x, xbytes), rr = make_rsrc(a.rest + grp * a.xs, xbytes);
+        const __amdgpu_buffer_rsrc_t ro = make_rsrc(a.out + grp * a.xs, xbytes);
+        const __amdgpu_buffer_rsrc_t rl = make_rsrc((__bf16*)a.last + grp * a.us, a.last ? (uint32_t)a.us * 2 : 0);
+        h4 old[2][FP], old_rest[2][FP];
+        auto fetch = [&](int i) {
 #pragma unroll
-    for (int i = 0; i < FQ; ++i) {
-        const int row = i0 + wq * (BQ / WQ) + i * 16 + li;
+            for (int j = 0; j < FP; ++j) {
+                const uint32_t o = offset(row0 + i * 16, col0 + j * 16, a.m, a.np);
+                old[i & 1][j] = __builtin_bit_cast(h4, __builtin_amdgcn_raw_buffer_load_b64(rx, o, 0, 0));
+                if (a.read_rest) old_rest[i & 1][j] = __builtin_bit_cast(h4, __builtin_amdgcn_raw_buffer_load_b64(rr, o, 0, 0));
+            }
+        };
+        fetch(0);
 #pragma unroll
-        for (int j = 0; j < FP; ++j) {
-            const int col = j0 + wp * (BP / WP) + j * 16 + 4 * g;
-            f4 v = acc[i][j] * (1.f / kScale);
-            if constexpr (OP == UPDATE) {
-                if (row >= a.m || col >= a.np) continue;
-                const int64_t at = (int64_t)row * a.np + col;
-                const h4 old = *(const h4*)(x + at), old_rest = *(const h4*)(rest + at);
+        for (int i = 0; i < FQ; ++i) {
+            if (i + 1 < FQ) fetch(i + 1);
+            const int row = row0 + i * 16;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = fmaf(kA, fmaf((float)old_rest[r], 1.f / kRest, (float)old[r]), v[r]);
+            for (int j = 0; j < FP; ++j) {
+                const int col = col0 + j * 16;
+                f4 v = acc[i][j] * (1.f / kScale);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float o = (float)old[i & 1][j][r];
+                    if (a.read_rest) o = fmaf((float)old_rest[i & 1][j][r], 1.f / kRest, o);
+                    v[r] = fmaf(kA, o, v[r]);
+                }
                 if (!a.last) {
+                    const uint32_t o = offset(row, col, a.m, a.np);
                     h4 left;
-                    *(h4*)(out + at) = split4(v, &left);
-                    *(h4*)(rest + at) = left;
+                    const h4 w = split4(v, &left);
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, w), ro, o, 0, 0);
+                    if (a.write_rest) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, left), rr, o, 0, 0);
+                    continue;
+                }
+                v *= 1.f / kScale;
+                if (!a.tall && (a.n & 3) == 0) {
+                    __builtin_amdgcn_raw_buffer_store_b64(pack4(v), rl, offset(row, col, a.m, a.n), 0, 0);
                 } else {
-                    __bf16* last = (__bf16*)a.last + grp * a.us;
-                    v *= 1.f / kScale;
-                    if (a.tall) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (col + r < a.n) last[(int64_t)(col + r) * a.m + row] = (__bf16)v[r];
-                    } else if ((a.n & 3) == 0) {
-                        if (col < a.n) *(u2*)(last + (int64_t)row * a.n + col) = pack4(v);
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (col + r < a.n) last[(int64_t)row * a.n + col + r] = (__bf16)v[r];
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t o = a.tall ? offset(col + r, row, a.n, a.m) : offset(row, col + r, a.m, a.n);
+                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v[r]), rl, o, 0, 0);
                     }
                 }
-            } else {
-                if constexpr (OP == SQUARE) {
-                    h4 old = {0, 0, 0, 0};
-                    if (row < a.m && col < a.mp) old = *(const h4*)(s + (int64_t)row * a.mp + col);
+            }
+        }
+    } else {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(s, sbytes), ro = make_rsrc(a.out + grp * a.ss, sbytes);
+        h4 old[2][FP];
+        auto fetch = [&](int i) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = fmaf(kC, v[r], kB * (float)old[r]);
+            for (int j = 0; j < FP; ++j)
+                old[i & 1][j] = __builtin_bit_cast(h4, __builtin_amdgcn_raw_buffer_load_b64(
+                                                           rs, offset(row0 + i * 16, col0 + j * 16, a.m, a.mp), 0, 0));
+        };
+        if (OP == SQUARE) fetch(0);
+#pragma unroll
+        for (int i = 0; i < FQ; ++i) {
+            if (OP == SQUARE && i + 1 < FQ) fetch(i + 1);
+            const int row = row0 + i * 16;
+#pragma unroll
+            for (int j = 0; j < FP; ++j) {
+                const int col = col0 + j * 16;
+                f4 v = acc[i][j] * (1.f / kScale);
+                if constexpr (OP == SQUARE) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = fmaf(kC, v[r], kB * (float)old[i & 1][j][r]);
                 }
                 const h4 w = half4(v);
-                if (row < a.m && col < a.mp) *(h4*)(out + (int64_t)row * a.mp + col) = w;
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2, w), ro, offset(row, col, a.m, a.mp), 0, 0);
                 if (tq != tp) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (col + r < a.m && row < a.mp) out[(int64_t)(col + r) * a.mp + row] = w[r];
+                    for (int r = 0; r < 4; ++r) {
+                        const h16 e = w[r];
+                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, e), ro, offset(col + r, row, a.m, a.mp), 0, 0);
+                    }
                 }
             }
         }
@@ -539,12 +582,12 @@ void product(const Ortho& a, int64_t groups, hipStream_t st)
         }
     }
     switch (best) {
-        case 0: return launch<256, 256, 2, 2, OP>(a, groups, st);
+        case 0: return launch<256, 256, 2, 4, OP>(a, groups, st);
         case 1:
-            if constexpr (OP == UPDATE) return launch<256, 192, 2, 2, OP>(a, groups, st);
+            if constexpr (OP == UPDATE) return launch<256, 192, 4, 2, OP>(a, groups, st);
             return;
-        case 2: return launch<192, 192, 2, 2, OP>(a, groups, st);
-        case 3: return launch<128, 128, 2, 2, OP>(a, groups, st);
+        case 2: return launch<192, 192, 2, 4, OP>(a, groups, st);
+        case 3: return launch<128, 128, 2, 4, OP>(a, groups, st);
         default: return launch<64, 64, 2, 2, OP>(a, groups, st);
     }
 }
@@ -632,6 +675,8 @@ int gconv_orthogonalize(const gconv_ortho_desc* d, const void* u, void* out, voi
         a.s = B;
         a.out = y;
         a.last = i + 1 == d->steps ? out : nullptr;
+        a.read_rest = d->steps - i > kRestSteps;
+        a.write_rest = d->steps - i - 1 > kRestSteps;
         product<UPDATE>(a, p.groups, hs);
         std::swap(x, y);
     }
