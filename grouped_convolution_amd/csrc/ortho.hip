@@ -28,27 +28,11 @@
 #include <algorithm>
 
 #include "gconv.h"
-#include "gconv_internal.h"
-#include "device_util.h"
-#include "seq_util.h"
+#include "ortho_internal.h"
 
 namespace gconv {
 namespace {
 
-typedef _Float16 h16;
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-
-typedef __attribute__((address_space(3))) char lds_char;
-
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kScale = 4096.f;  // of X, A and B as they are stored
-constexpr float kRest = 2048.f;    // of the rest of X, over X
-// Rounds before the end that take X without its rest: noise of 2^-12 grows
-// 12 times at most there, and without it the strong directions come out a
-// little closer (128 x 1200: 2.3e-3 off for 2.4e-3; rank one 3.3e-3, and
-// 1.4e-2 with one round more).
-constexpr int kRestSteps = 2;
 constexpr int kStepK = 64;        // reduction length of a stage
 
 enum Op { GRAM = 0, SQUARE = 1, UPDATE = 2 };
@@ -66,29 +50,6 @@ struct Ortho {
     int tall;        // the result is stored transposed, [n][m]
     int read_rest, write_rest;
 };
-
-// 64 lanes' 16 bytes from global memory straight to 1024 bytes of LDS. In
-// assembly, as it writes no register: the compiler would otherwise wait for
-// every such load before any read of LDS, where the stages below wait once.
-__device__ __forceinline__ void copy_lds(u4 rsrc, uint32_t lds, uint32_t off)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(off), "s"(rsrc) : "memory");
-}
-
-// Waits until at most N of this wave's loads are still under way.
-template <int N>
-__device__ __forceinline__ void wait_loads()
-{
-    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
-}
-
-__device__ __forceinline__ u4 resource(const void* p, uint32_t bytes)
-{
-    const uint64_t v = (uint64_t)p;
-    return u4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v), (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)),
-              (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
-}
 
 // Stage of an operand whose reduction runs along its rows in memory: [R][64]
 // elements, the 16-byte pieces of row r at piece ^ (r & 7), so the 8 lanes
@@ -167,25 +128,6 @@ struct AcrossRows {
         return u4{lo[0], lo[1], hi[0], hi[1]};
     }
 };
-
-__device__ __forceinline__ f4 mma16(u4 a, u4 b, f4 c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
-}
-
-__device__ __forceinline__ h4 half4(f4 v)
-{
-    return h4{(h16)v[0], (h16)v[1], (h16)v[2], (h16)v[3]};
-}
-
-// v in fp16, and what that leaves, times kRest.
-__device__ __forceinline__ h4 split4(f4 v, h4* rest)
-{
-    const h4 h = half4(v);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) (*rest)[r] = (h16)((v[r] - (float)h[r]) * kRest);
-    return h;
-}
 
 // Tile L of the triangle q <= p: columns of tiles, top to bottom.
 __device__ __forceinline__ void triangle(int L, int* q, int* p)
@@ -512,13 +454,14 @@ int check_desc(const gconv_ortho_desc* d)
 struct Plan {
     int64_t m, n, mp, np, us, xs, ss, groups;
     int tall, blocks;
-    size_t x0, x1, rest, A, B, part, bytes;  // offsets in the workspace
+    int small;         // workgroups a group of the small kernels; 0: the general ones
+    size_t x0, x1, rest, A, B, norm, gram, bytes;  // offsets in the workspace
 };
 
 int make_plan(const gconv_ortho_desc* d, Plan* p)
 {
     const int64_t rows = d->filters / d->groups;
-    constexpr int64_t kMost = (int64_t)1 << 29;  // elements of a matrix: byte offsets stay below 2^31
+    constexpr int64_t kMost = (int64_t)1 << 29;     // elements of a matrix: byte offsets stay below 2^31
     constexpr int64_t kLongest = (int64_t)1 << 24;  // 64 rows past the last: below 2^32
     if (d->inner > kLongest || rows > kLongest) return fail(GCONV_ERR_UNSUPPORTED, "a group's matrix has a side above 2^24");
     p->groups = d->groups;
@@ -536,18 +479,27 @@ int make_plan(const gconv_ortho_desc* d, Plan* p)
     // about 2048 workgroups in all, 16 elements or more a thread
     const int64_t want = std::max<int64_t>(1, 2048 / d->groups);
     p->blocks = (int)std::min<int64_t>(want, (p->us + kNormThreads * 16 - 1) / (kNormThreads * 16));
+    p->small = ortho_small_blocks(p->m, p->np);
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t o = at;
         at += (n + 1023) / 1024 * 1024;
         return o;
     };
-    p->x0 = take((size_t)d->groups * p->xs * 2);
-    p->x1 = take((size_t)d->groups * p->xs * 2);
-    p->rest = take((size_t)d->groups * p->xs * 2);
-    p->A = take((size_t)d->groups * p->ss * 2);
-    p->B = take((size_t)d->groups * p->ss * 2);
-    p->part = take((size_t)d->groups * p->blocks * 8);
+    const size_t g = (size_t)d->groups;
+    p->rest = take(g * p->xs * 2);
+    if (p->small != 1) {
+        p->x0 = take(g * p->xs * 2);
+        p->norm = take(g * p->blocks * 8);
+    }
+    if (p->small == 0) {
+        p->x1 = take(g * p->xs * 2);
+        p->A = take(g * p->ss * 2);
+        p->B = take(g * p->ss * 2);
+        take(1024);  // loads past a matrix's last stage read up to here
+    } else {
+        p->gram = take(g * ortho_small_gram_bytes(p->m, p->small));
+    }
     p->bytes = at;
     return GCONV_OK;
 }
@@ -592,7 +544,37 @@ void product(const Ortho& a, int64_t groups, hipStream_t st)
     }
 }
 
+Prep prep(const OrthoArgs& a)
+{
+    const int64_t es = a.bf16 ? 2 : 4;
+    Prep r{};
+    r.u = a.u;
+    r.part = a.norm_part;
+    r.x = a.x;
+    r.rest = a.rest;
+    r.us = a.us;
+    r.xs = a.xs;
+    r.blocks = a.norm_blocks;
+    r.rows = a.rows;
+    r.cols = a.cols;
+    r.np = a.np;
+    r.tall = a.tall;
+    r.vec = ((uintptr_t)a.u & 15) == 0 && a.us * es % 16 == 0;
+    r.vec_rows = (uintptr_t)a.u % (4 * es) == 0 && a.cols % 4 == 0;
+    r.eps = a.eps;
+    return r;
+}
+
 }  // namespace
+
+void ortho_launch_norm(const OrthoArgs& a, hipStream_t st)
+{
+    const Prep r = prep(a);
+    const unsigned grid = (unsigned)(a.norm_blocks * a.groups);
+    if (a.bf16) ortho_norm<__bf16><<<grid, kNormThreads, 0, st>>>(r);
+    else ortho_norm<float><<<grid, kNormThreads, 0, st>>>(r);
+}
+
 }  // namespace gconv
 
 using namespace gconv;
@@ -604,7 +586,7 @@ int gconv_orthogonalize_workspace_size(const gconv_ortho_desc* d, size_t* bytes)
     int st = check_desc(d);
     if (st != GCONV_OK) return st;
     if (!bytes) return fail(GCONV_ERR_NULL, "bytes pointer is NULL");
-    Plan p;
+    Plan p{};
     st = make_plan(d, &p);
     if (st != GCONV_OK) return st;
     *bytes = p.bytes;
@@ -615,7 +597,7 @@ int gconv_orthogonalize(const gconv_ortho_desc* d, const void* u, void* out, voi
 {
     int st = check_desc(d);
     if (st != GCONV_OK) return st;
-    Plan p;
+    Plan p{};
     st = make_plan(d, &p);
     if (st != GCONV_OK) return st;
     if (!u || !out) return fail(GCONV_ERR_NULL, "u and out must be non-NULL");
@@ -630,29 +612,35 @@ int gconv_orthogonalize(const gconv_ortho_desc* d, const void* u, void* out, voi
     (void)hipGetLastError();
     char* w = (char*)workspace;
 
-    Prep r{};
-    r.u = u;
-    r.part = (double*)(w + p.part);
-    r.x = (h16*)(w + p.x0);
-    r.rest = (h16*)(w + p.rest);
-    r.us = p.us;
-    r.xs = p.xs;
-    r.blocks = p.blocks;
-    r.rows = (int)(d->filters / d->groups);
-    r.cols = (int)d->inner;
-    r.np = (int)p.np;
-    r.tall = p.tall;
-    r.vec = ((uintptr_t)u & 15) == 0 && p.us * es % 16 == 0;
-    r.vec_rows = (uintptr_t)u % (4 * es) == 0 && d->inner % 4 == 0;
-    r.eps = d->eps;
-    const unsigned ng = (unsigned)(p.blocks * p.groups), ns = (unsigned)((p.m + 63) / 64 * (p.np / 64) * p.groups);
-    if (d->dtype == GCONV_BF16) {
-        ortho_norm<__bf16><<<ng, kNormThreads, 0, hs>>>(r);
-        ortho_scale<__bf16><<<ns, 256, 0, hs>>>(r);
-    } else {
-        ortho_norm<float><<<ng, kNormThreads, 0, hs>>>(r);
-        ortho_scale<float><<<ns, 256, 0, hs>>>(r);
+    OrthoArgs o{};
+    o.u = u;
+    o.bf16 = d->dtype == GCONV_BF16;
+    o.out = out;
+    o.x = (h16*)(w + p.x0);
+    o.rest = (h16*)(w + p.rest);
+    o.norm_part = (double*)(w + p.norm);
+    o.gram_part = (float*)(w + p.gram);
+    o.groups = p.groups;
+    o.steps = d->steps;
+    o.us = p.us;
+    o.xs = p.xs;
+    o.rows = (int)(d->filters / d->groups);
+    o.cols = (int)d->inner;
+    o.m = (int)p.m;
+    o.n = (int)p.n;
+    o.np = (int)p.np;
+    o.tall = p.tall;
+    o.norm_blocks = p.blocks;
+    o.eps = d->eps;
+    if (p.small > 0) {
+        ortho_small(o, p.small, hs);
+        return finish();
     }
+
+    ortho_launch_norm(o, hs);
+    const unsigned ns = (unsigned)((p.m + 63) / 64 * (p.np / 64) * p.groups);
+    if (o.bf16) ortho_scale<__bf16><<<ns, 256, 0, hs>>>(prep(o));
+    else ortho_scale<float><<<ns, 256, 0, hs>>>(prep(o));
 
     Ortho a{};
     a.rest = (h16*)(w + p.rest);

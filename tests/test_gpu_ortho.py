@@ -62,6 +62,14 @@ def test_sizes(type_, m, n):
     run("size", make(m + n, type_, m, n))
 
 
+# one workgroup, and several, by the rows that are kept in registers; the longest of each
+@pytest.mark.parametrize("m,n", [(20, 30), (32, 704), (32, 705), (9, 5000), (40, 512), (64, 513), (50, 3000), (96, 448), (80, 449),
+                                 (70, 2222), (128, 256), (128, 321), (100, 8200), (3, 70000), (110, 20000), (400, 128), (2000, 66)])
+@pytest.mark.parametrize("type_", ["fp32", "bf16"])
+def test_few_rows(type_, m, n):
+    run("few rows", make(m + n, type_, m, n))
+
+
 @pytest.mark.parametrize("m,n", [(1100, 1300), (2000, 2050), (2500, 1025), (4000, 4100), (1700, 8000)])
 def test_large(m, n):
     run("large", make(m + n, "fp32", m, n))
