@@ -41,6 +41,7 @@ struct Operand {
     int hdiv;                // q heads that share one of its heads
     int dim;
     int vec;                 // rows start on 16 bytes and hold whole 16-byte pieces
+    const char* end;         // of the tensor's last row; NULL where that is not known
 };
 
 struct Pass {
@@ -123,32 +124,105 @@ __device__ __forceinline__ const T* row_of(const Operand& o, const Pass& a, cons
     return (const T*)o.p + (a.cu ? 0 : (int64_t)p.n * o.seq) + tok * o.tok + (int64_t)(h / o.hdiv) * o.head;
 }
 
+// Reads of an operand's rows, 16 bytes a lane, for tokens t0 .. t0 + n - 1 of a
+// head. All loads of a chunk are in flight at once, so none may have a branch
+// with a wait in it (one by one they took 8 us a chunk). VEC: every row holds
+// whole aligned 16-byte pieces, and buffer loads give 0 outside. Otherwise a
+// piece is read where it starts, whatever its alignment and although it may
+// reach past its row, and `mask` clears what is not the row's when the value
+// is used; only a chunk at the tensor's very end reads element by element.
+template <typename T, bool VEC>
+struct Reader {
+    static constexpr int E = 16 / (int)sizeof(T);
+    const T* low;    // the chunk's row at the lowest address
+    int64_t tok;
+    int n, dim, reverse;
+    bool edge;
+    __amdgpu_buffer_rsrc_t rsrc;
+
+    __device__ __forceinline__ Reader(const Operand& o, const Pass& a, const Place& p, int h, int t0, int n_)
+        : tok(o.tok), n(n_), dim(o.dim), reverse(a.reverse)
+    {
+        low = row_of<T>(o, a, p, h, a.reverse ? t0 + n - 1 : t0);
+        if constexpr (VEC) {
+            rsrc = make_rsrc(low, (uint32_t)(((n - 1) * tok + dim) * (int64_t)sizeof(T)));
+        } else {
+            edge = !o.end || (const char*)(low + (n - 1) * tok + (dim + E - 1) / E * E) > o.end;
+        }
+    }
+    __device__ __forceinline__ u4 load(int row, int col) const
+    {
+        const bool live = row < n && col < dim;
+        const int r = reverse ? n - 1 - row : row;
+        if constexpr (VEC) {
+            return __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(
+                                              rsrc, live ? (uint32_t)(r * (int)tok + col) * (uint32_t)sizeof(T) : kOOB, 0, 0));
+        } else {
+            struct __attribute__((packed, aligned(sizeof(T)))) Loose { u4 v; };
+            return ((const Loose*)(low + (live ? r * tok + col : 0)))->v;
+        }
+    }
+    __device__ __forceinline__ u4 load_edge(int row, int col) const
+    {
+        if (row >= n) return u4{0, 0, 0, 0};
+        return load16<T>(low + (reverse ? n - 1 - row : row) * tok, col, dim, false);
+    }
+    static __device__ __forceinline__ u4 mask(u4 v, int row, int col, int n, int dim)
+    {
+        if constexpr (!VEC) {
+            const int keep = row < n ? dim - col : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 2) v[i] = keep >= 2 * i + 2 ? v[i] : keep == 2 * i + 1 ? v[i] & 0xffffu : 0u;
+                else v[i] = keep > i ? v[i] : 0u;
+            }
+        }
+        return v;
+    }
+};
+
 // A chunk of 64 rows x D of an operand: global memory -> registers -> LDS.
-template <typename T, int D>
+template <typename T, int D, bool VEC>
 struct Stage {
+    static constexpr int E = 16 / (int)sizeof(T);
     static constexpr int kVpr = D * (int)sizeof(T) / 16;            // 16-byte pieces of a row
     static constexpr int kN = kChunk * kVpr / kThreads;             // pieces of a thread
-    static constexpr int kPitch = D + 16 / (int)sizeof(T);
+    // bf16: 32 bytes past a multiple of 256 (or 160), so that the 8 rows x 32
+    // bytes of a transposing read and the 16 rows of a fragment's lanes lie in
+    // different banks; fp32: 16 bytes past it, for the 4 rows x 64 bytes of its
+    // column reads
+    static constexpr int kPitch = D + (sizeof(T) == 2 ? 16 : 4);
     u4 r[kN];
+    int rows, dim;
 
     __device__ __forceinline__ void load(const Operand& o, const Pass& a, const Place& p, int h, int t0, int n, int tid)
     {
-        const T* base = row_of<T>(o, a, p, h, t0);
-        const int64_t step = a.reverse ? -o.tok : o.tok;
+        const Reader<T, VEC> in(o, a, p, h, t0, n);
+        rows = n;
+        dim = o.dim;
+        if (!VEC && in.edge) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int idx = tid + i * kThreads;
+                r[i] = in.load_edge(idx / kVpr, idx % kVpr * E);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int idx = tid + i * kThreads, row = idx / kVpr, c = idx % kVpr;
-            r[i] = u4{0, 0, 0, 0};
-            if (row < n) r[i] = load16<T>(base + row * step, c * (16 / (int)sizeof(T)), o.dim, o.vec);
+            const int idx = tid + i * kThreads;
+            r[i] = in.load(idx / kVpr, idx % kVpr * E);
         }
     }
 
-    __device__ __forceinline__ void store(T* tile, int tid) const
+    template <int P = kPitch>
+    __device__ __forceinline__ void store(T* tile, int tid)
     {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int idx = tid + i * kThreads, row = idx / kVpr, c = idx % kVpr;
-            *(u4*)(tile + row * kPitch + c * (16 / (int)sizeof(T))) = r[i];
+            r[i] = Reader<T, VEC>::mask(r[i], row, c * E, rows, dim);
+            *(u4*)(tile + row * P + c * E) = r[i];
         }
     }
 
@@ -171,7 +245,8 @@ __device__ __forceinline__ void row_weights(const float* w, int row0, int lane, 
 }
 
 // w x v as fragments that add up to it: one fp32 fragment, or NT bf16 parts of
-// 8 bits each (three hold the float32 product, its error below 2^-24).
+// 8 bits each, cut off one after another (three hold all 24 bits of the
+// float32 product). An infinity or a NaN is the first part's alone.
 template <typename T, int NT>
 __device__ __forceinline__ void weighted(u4 v, const float* w, u4* out)
 {
@@ -181,20 +256,40 @@ __device__ __forceinline__ void weighted(u4 v, const float* w, u4* out)
         for (int i = 0; i < 4; ++i) x[i] *= w[i];
         out[0] = __builtin_bit_cast(u4, x);
     } else {
-        const bf8 b = __builtin_bit_cast(bf8, v);
-        float x[8];
+        float x[8], z = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (float)b[i] * w[i];
+        for (int i = 0; i < 8; ++i) {
+            x[i] = __builtin_bit_cast(float, i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16) * w[i];
+            z = fmaf(x[i], 0.f, z);  // a NaN where one is not finite
+        }
+        if (__any(z != 0.f)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // a NaN whose bits are all in the low half stays one
+                if (x[i] != x[i]) x[i] = __builtin_bit_cast(float, 0x7fc00000u);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a = __builtin_bit_cast(uint32_t, x[2 * i]), b = __builtin_bit_cast(uint32_t, x[2 * i + 1]);
+                    out[t][i] = a >> 16 | b & 0xffff0000u;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float top = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x[i]) & 0xffff0000u);
+                    x[i] = finite_bits<float>(x[i]) ? x[i] - top : 0.f;
+                }
+            }
+            return;
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            bf8 part;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                part[i] = (__bf16)x[i];
-                // what the part leaves; nothing where it took an infinity or a NaN
-                if (t + 1 < NT) x[i] = finite_bits<float>(x[i]) && finite_bits<__bf16>(part[i]) ? x[i] - (float)part[i] : 0.f;
+            for (int i = 0; i < 4; ++i)
+                out[t][i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, x[2 * i + 1]), __builtin_bit_cast(uint32_t, x[2 * i]), 0x07060302u);
+            if (t + 1 < NT) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] -= __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x[i]) & 0xffff0000u);
             }
-            out[t] = __builtin_bit_cast(u4, part);
         }
     }
 }
@@ -204,11 +299,11 @@ __device__ __forceinline__ void weighted(u4 v, const float* w, u4* out)
 // L = vscale sum_j lambda^(n-1-j) k_j v_j^T over the segment's n tokens, one
 // workgroup a (segment, head). The weighted values are split into three bf16
 // parts, so the states keep float32 accuracy: they come back to the caller.
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads) void segment_sums(Pass a)
+template <typename T, int DK, int DV, bool VEC>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void segment_sums(Pass a)
 {
-    using SK = Stage<T, DK>;
-    using SV = Stage<T, DV>;
+    using SK = Stage<T, DK, VEC>;
+    using SV = Stage<T, DV, VEC>;
     constexpr int NT = sizeof(T) == 2 ? 3 : 1;
     constexpr int RT = DK / 16, CT = DV / 64;
     __shared__ __align__(16) T Ks[kChunk * SK::kPitch];
@@ -224,7 +319,6 @@ __global__ __launch_bounds__(kThreads) void segment_sums(Pass a)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const float g = a.log_decay[h];
-    const float l64 = dpow(g, kChunk);
 
     f4 S[RT][CT];
 #pragma unroll
@@ -234,26 +328,20 @@ __global__ __launch_bounds__(kThreads) void segment_sums(Pass a)
 
     SK sk;
     SV sv;
-    sk.load(a.k, a, p, h, t0, min(kChunk, n), tid);
-    sv.load(a.v, a, p, h, t0, min(kChunk, n), tid);
-    for (int c0 = 0; c0 < n; c0 += kChunk) {
-        const int m = min(kChunk, n - c0);
+    // From the last chunk to the first: chunk_outputs starts with the first, and
+    // what was read last is still in the cache behind the L2s.
+    const int first = (n - 1) / kChunk * kChunk;
+    sk.load(a.k, a, p, h, t0 + first, n - first, tid);
+    sv.load(a.v, a, p, h, t0 + first, n - first, tid);
+    for (int c0 = first; c0 >= 0; c0 -= kChunk) {
         __syncthreads();
         sk.store(Ks, tid);
         sv.store(Vs, tid);
-        if (tid < kChunk) wt[tid] = tid < m ? dpow(g, m - 1 - tid) : 0.f;
+        if (tid < kChunk) wt[tid] = c0 + tid < n ? dpow(g, n - 1 - c0 - tid) : 0.f;
         __syncthreads();
-        if (c0 + kChunk < n) {
-            const int m2 = min(kChunk, n - c0 - kChunk);
-            sk.load(a.k, a, p, h, t0 + c0 + kChunk, m2, tid);
-            sv.load(a.v, a, p, h, t0 + c0 + kChunk, m2, tid);
-        }
-        const float decay = m == kChunk ? l64 : dpow(g, m);
         if (c0 > 0) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int c = 0; c < CT; ++c) S[r][c] *= decay;
+            sk.load(a.k, a, p, h, t0 + c0 - kChunk, kChunk, tid);
+            sv.load(a.v, a, p, h, t0 + c0 - kChunk, kChunk, tid);
         }
 #pragma unroll
         for (int ks = 0; ks < kChunk; ks += Frag<T>::kStep) {
@@ -286,6 +374,8 @@ __global__ __launch_bounds__(kThreads) void segment_sums(Pass a)
 //
 // Replaces each segment's sum by the state before it and writes the final
 // state. One thread four rows of a column; a segment is one step of the scan.
+// Bound by memory: the 33 MB of states of 512 segments take 13 us, 5.1 TB/s.
+// (More loads in flight than U, clamped at the end, took 30 us.)
 template <int DK, int DV>
 __global__ __launch_bounds__(kThreads) void scan_states(Pass a)
 {
@@ -337,28 +427,39 @@ __global__ __launch_bounds__(kThreads) void scan_states(Pass a)
 
 // ---- the outputs of a segment, chunk by chunk ----------------------------------
 //
-// One workgroup of four waves a (segment, head). Each wave answers 16 queries
-// of the chunk and owns a quarter of the state's columns:
-//   P^T = K Q^T        accumulator tiles, weighted and masked, packed into the
-//                      fragments of the next product as they lie
+// One workgroup of four waves a (segment, head). Each wave owns a quarter of
+// the state's columns, in registers, and answers all 64 queries for them:
+//   P^T = K Q^T        16 queries a wave; weighted, masked, and exchanged
+//                      through LDS
 //   O^T = S^T Q^T, scaled by lambda^(i+1) (one factor a lane), + V^T P^T
 //   S   = lambda^64 S + K^T (w V)
-// In bf16 the products' operands P, S and w V are rounded to bf16, as q, k and
-// v are: each rounding is at most 2^-8 of a term, the size of the output's own.
-// The accumulators, the state and the weights stay in float32, and the
-// caller's final state does not come from here but from segment_sums.
-template <typename T, int DK, int DV>
+// The accumulators of S, packed, are the fragments of its product as they lie,
+// and a wave reads no values but its own columns', for the output and the
+// state both. (With the queries dealt to the waves instead, each of them read
+// all of S and V: 142 us for 32768 tokens x 16 heads.)
+// In bf16 the products' operands P and S are rounded to bf16, as q, k and v
+// are: each rounding is at most 2^-8 of a term, the size of the output's own.
+// The accumulators, the state and the weights stay in float32; w V goes in as
+// two bf16 parts of 8 bits, so that the state does not gather roundings from
+// chunk to chunk (one part: the output 2.7e-3 off in the 2-norm where two give
+// 2.4e-3 and its own rounding is 1.7e-3). The caller's final state does not
+// come from here but from segment_sums.
+template <typename T, int DK, int DV, bool VEC>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void chunk_outputs(Pass a)
 {
-    using SK = Stage<T, DK>;
-    using SV = Stage<T, DV>;
-    constexpr int E = Frag<T>::kElems, KST = Frag<T>::kStep;
-    constexpr int RT = DK / 16, CT = DV / 64, OT = DV / 16, QS = DK / KST;
-    constexpr int TPK = KST / 16;  // 16-token tiles of one reduction step
-    constexpr int SP = SK::kPitch;
+    using SK = Stage<T, DK, VEC>;
+    using SV = Stage<T, DV, VEC>;
+    constexpr int KST = Frag<T>::kStep;
+    constexpr int RT = DK / 16, CT = DV / 64, QS = DK / KST;
+    constexpr int QT = kChunk / 16;  // tiles of 16 queries
+    constexpr int TPK = KST / 16;    // 16-token tiles of one reduction step
+    constexpr int NT = sizeof(T) == 2 ? 2 : 1;
+    // 16 bytes past a multiple of 128: 16 rows x 16 bytes in different banks
+    constexpr int QP = DK + 16 / (int)sizeof(T), PP = kChunk + 16 / (int)sizeof(T);
     __shared__ __align__(16) T Ks[kChunk * SK::kPitch];
     __shared__ __align__(16) T Vs[kChunk * SV::kPitch];
-    __shared__ __align__(16) T St[DV * SP];
+    __shared__ __align__(16) T Qs[kChunk * QP];
+    __shared__ __align__(16) T Ps[kChunk * PP];
     __shared__ __align__(16) float wt[kChunk];
     __shared__ float pw[kChunk + 1];
     __shared__ int nonfin[2];
@@ -372,28 +473,35 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void chunk_output
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const float ld = a.log_decay[h];
-
-    SK sk;
+    auto out_at = [&](int t) {  // the output row of token t of the segment
+        const int64_t tok = p.start + (a.reverse ? p.len - 1 - (t0 + t) : t0 + t);
+        return (a.cu ? 0 : (int64_t)p.n * a.out_seq) + tok * a.out_tok + (int64_t)h * a.out_head;
+    };
+    SK sk, sq;
     SV sv;
-    sk.load(a.k, a, p, h, t0, min(kChunk, n), tid);
-    sv.load(a.v, a, p, h, t0, min(kChunk, n), tid);
+    auto load = [&](int c0) {
+        const int m = min(kChunk, n - c0);
+        sk.load(a.k, a, p, h, t0 + c0, m, tid);
+        sv.load(a.v, a, p, h, t0 + c0, m, tid);
+        sq.load(a.q, a, p, h, t0 + c0, m, tid);
+    };
+    load(0);
 
     // The state before the segment, in the layout the update produces.
     f4 S[RT][CT];
     const float* st = a.states + ((int64_t)slot * a.heads + h) * (DK * DV);
+    if (!a.state_t) {
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        const int col = (wave * CT + c) * 16 + li;
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int row = r * 16 + 4 * g;
-            if (!a.state_t) {
-                S[r][c] = *(const f4*)(st + col * DK + row);
-            } else {
+            for (int r = 0; r < RT; ++r) S[r][c] = *(const f4*)(st + ((wave * CT + c) * 16 + li) * DK + r * 16 + 4 * g);
+    } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[r][c][i] = st[(row + i) * DV + col];
-            }
-        }
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[r][c][i] = st[(r * 16 + 4 * g + i) * DV + (wave * CT + c) * 16 + li];
     }
     if (tid <= kChunk) pw[tid] = dpow(ld, tid);
     if (tid < kChunk) wt[tid] = a.vscale * dpow(ld, kChunk - 1 - tid);
@@ -414,128 +522,142 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void chunk_output
         __syncthreads();  // the last chunk's tiles have been read (and nonfin is set up)
         sk.store(Ks, tid);
         sv.store(Vs, tid);
+        sq.template store<QP>(Qs, tid);
         if (sv.nonfinite()) nonfin[par] = 1;
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            T* col = St + ((wave * CT + c) * 16 + li) * SP + 4 * g;
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                if constexpr (sizeof(T) == 2) *(u2*)(col + r * 16) = pack4(S[r][c]);
-                else *(f4*)(col + r * 16) = S[r][c];
-            }
-        }
-        const int qi = wave * 16 + li;  // this lane's query in the chunk
-        const bool live = qi < m;
-        const T* qrow = row_of<T>(a.q, a, p, h, live ? t0 + c0 + qi : t0);
-        u4 fq[QS];
-#pragma unroll
-        for (int s = 0; s < QS; ++s) {
-            fq[s] = u4{0, 0, 0, 0};
-            if (live) fq[s] = load16<T>(qrow, s * KST + g * E, a.q.dim, a.q.vec);
-        }
         __syncthreads();
         const bool more = c0 + kChunk < n;
-        if (more) {
-            const int m2 = min(kChunk, n - c0 - kChunk);
-            sk.load(a.k, a, p, h, t0 + c0 + kChunk, m2, tid);
-            sv.load(a.v, a, p, h, t0 + c0 + kChunk, m2, tid);
-        }
+        if (more) load(c0 + kChunk);
         const bool odd = nonfin[par] != 0;
         if (tid == 0) nonfin[par ^ 1] = 0;
 
-        // the state's answer
-        const bool lead = p.s == 0 && c0 == 0;
-        f4 O[OT];
+        // the products of the wave's queries with the chunk's keys up to them
+        {
+            u4 fq[QS];
 #pragma unroll
-        for (int t = 0; t < OT; ++t) {
-            O[t] = f4{0, 0, 0, 0};
+            for (int s = 0; s < QS; ++s) fq[s] = frag_cols<T>(Qs, QP, wave * 16, s * KST, lane);
 #pragma unroll
-            for (int s = 0; s < QS; ++s) O[t] = mma<T>(frag_cols<T>(St, SP, t * 16, s * KST, lane), fq[s], O[t]);
-        }
-        const float rd = a.iscale * pw[qi + (lead ? a.e0 : 1)];
+            for (int jt = 0; jt < QT; ++jt) {
+                if (jt >= (wave / TPK + 1) * TPK) break;  // the reduction steps that the query's products take
+                f4 P = {0, 0, 0, 0};
+                if (jt <= wave) {
 #pragma unroll
-        for (int t = 0; t < OT; ++t) O[t] *= rd;
-
-        // the chunk's own tokens, up to the query
+                    for (int s = 0; s < QS; ++s) P = mma<T>(frag_cols<T>(Ks, SK::kPitch, jt * 16, s * KST, lane), fq[s], P);
+                    if (jt == wave) {
 #pragma unroll
-        for (int ks = 0; ks < kChunk / KST; ++ks) {
-            if (ks * TPK > wave) break;
-            f4 P[TPK];
+                        for (int r = 0; r < 4; ++r) P[r] = li >= 4 * g + r ? P[r] * wdiag[r] : 0.f;
+                    } else {
+                        const int far = wave - jt - 1;
+                        const float f = far == 0 ? 1.f : far == 1 ? p16 : p32;
 #pragma unroll
-            for (int u = 0; u < TPK; ++u) {
-                const int jt = ks * TPK + u;
-                P[u] = f4{0, 0, 0, 0};
-                if (jt > wave) continue;
-#pragma unroll
-                for (int s = 0; s < QS; ++s) P[u] = mma<T>(frag_cols<T>(Ks, SK::kPitch, jt * 16, s * KST, lane), fq[s], P[u]);
-                if (jt == wave) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) P[u][r] = li >= 4 * g + r ? P[u][r] * wdiag[r] : 0.f;
-                } else {
-                    const int far = wave - jt - 1;
-                    const float f = far == 0 ? 1.f : far == 1 ? p16 : p32;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) P[u][r] *= woff[r] * f;
+                        for (int r = 0; r < 4; ++r) P[r] *= woff[r] * f;
+                    }
                 }
+                T* to = Ps + (wave * 16 + li) * PP + jt * 16 + 4 * g;
+                if constexpr (sizeof(T) == 2) *(u2*)to = pack4(P);
+                else *(f4*)to = P;
             }
-            u4 fp;
-            if constexpr (sizeof(T) == 2) {
-                const u2 lo = pack4(P[0]), hi = pack4(P[1]);
-                fp = u4{lo[0], lo[1], hi[0], hi[1]};
-            } else {
-                fp = __builtin_bit_cast(u4, P[0]);
-            }
+        }
+
+        // the state's answers
+        const bool lead = p.s == 0 && c0 == 0;
+        f4 O[QT][CT];
+        {
+            u4 fs[QS][CT];
 #pragma unroll
-            for (int t = 0; t < OT; ++t) {
-                u4 fv = frag_rows(Vs, SV::kPitch, ks * KST, t * 16, lane);
+            for (int s = 0; s < QS; ++s)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    if constexpr (sizeof(T) == 2) {
+                        const u2 lo = pack4(S[2 * s][c]), hi = pack4(S[2 * s + 1][c]);
+                        fs[s][c] = u4{lo[0], lo[1], hi[0], hi[1]};
+                    } else {
+                        fs[s][c] = __builtin_bit_cast(u4, S[s][c]);
+                    }
+                }
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c) O[t][c] = f4{0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < QS; ++s) {
+                    const u4 fq = frag_split<T>(Qs, QP, t * 16, s * KST, lane);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) O[t][c] = mma<T>(fs[s][c], fq, O[t][c]);
+                }
+                const float rd = a.iscale * pw[t * 16 + li + (lead ? a.e0 : 1)];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) O[t][c] *= rd;
+            }
+        }
+        __syncthreads();  // P is there
+
+        // the chunk's own tokens, up to each query
+        u4 fv[kChunk / KST][CT];
+#pragma unroll
+        for (int ks = 0; ks < kChunk / KST; ++ks)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) fv[ks][c] = frag_rows(Vs, SV::kPitch, ks * KST, (wave * CT + c) * 16, lane);
+#pragma unroll
+        for (int ks = 0; ks < kChunk / KST; ++ks)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
                 // masked weights are 0, and 0 x infinity is a NaN: such values are
                 // kept out of the product and added by themselves below
-                if (odd) fv = drop_nonfinite<T>(fv);
-                O[t] = mma<T>(fv, fp, O[t]);
+                u4 v = fv[ks][c];
+                if (odd) v = drop_nonfinite<T>(v);
+#pragma unroll
+                for (int t = ks * TPK; t < QT; ++t)
+                    O[t][c] = mma<T>(v, frag_split<T>(Ps, PP, t * 16, ks * KST, lane), O[t][c]);
             }
-        }
-        if (odd && live) {
-#pragma unroll 1
-            for (int j = 0; j <= qi; ++j) {
-                const T* krow = Ks + j * SK::kPitch;
-                float dot = 0.f;
-#pragma unroll 1
-                for (int d = 0; d < a.k.dim; ++d) dot += (float)qrow[d] * (float)krow[d];
-                dot *= a.pscale * pw[qi - j];
+        if (odd) {
 #pragma unroll
-                for (int t = 0; t < OT; ++t)
+            for (int t = 0; t < QT; ++t) {
+                const int qi = t * 16 + li;
+                const T* qrow = Qs + qi * QP;
+#pragma unroll 1
+                for (int j = 0; j <= qi; ++j) {
+                    const T* krow = Ks + j * SK::kPitch;
+                    float dot = 0.f;
+#pragma unroll 1
+                    for (int d = 0; d < a.k.dim; ++d) dot += (float)qrow[d] * (float)krow[d];
+                    dot *= a.pscale * pw[qi - j];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const T v = Vs[j * SV::kPitch + t * 16 + 4 * g + r];
-                        if (!finite_bits<T>(v)) O[t][r] += dot * (float)v;
-                    }
+                    for (int c = 0; c < CT; ++c)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const T v = Vs[j * SV::kPitch + (wave * CT + c) * 16 + 4 * g + r];
+                            if (!finite_bits<T>(v)) O[t][c][r] += dot * (float)v;
+                        }
+                }
             }
         }
 
-        if (live) {
-            const int64_t tok = p.start + (a.reverse ? p.len - 1 - (t0 + c0 + qi) : t0 + c0 + qi);
-            const int64_t at = (a.cu ? 0 : (int64_t)p.n * a.out_seq) + tok * a.out_tok + (int64_t)h * a.out_head;
-            const bool quads = (a.dv & 3) == 0;  // dense rows: quads of outputs are aligned
+        const bool quads = (a.dv & 3) == 0;  // dense rows: quads of outputs are aligned
 #pragma unroll
-            for (int t = 0; t < OT; ++t) {
-                const int col = t * 16 + 4 * g;
+        for (int t = 0; t < QT; ++t) {
+            const int qi = t * 16 + li;
+            if (qi >= m) continue;
+            const int64_t at = out_at(c0 + qi);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const int col = (wave * CT + c) * 16 + 4 * g;
                 if (a.out_f32 || sizeof(T) == 4) {
                     float* o = (float*)a.out + at + col;
                     if (quads) {
-                        if (col < a.dv) *(f4*)o = O[t];
+                        if (col < a.dv) *(f4*)o = O[t][c];
                     } else {
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            if (col + r < a.dv) o[r] = O[t][r];
+                            if (col + r < a.dv) o[r] = O[t][c][r];
                     }
                 } else {
                     T* o = (T*)a.out + at + col;
                     if (quads) {
-                        if (col < a.dv) *(u2*)o = pack4(O[t]);
+                        if (col < a.dv) *(u2*)o = pack4(O[t][c]);
                     } else {
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            if (col + r < a.dv) o[r] = (T)O[t][r];
+                            if (col + r < a.dv) o[r] = (T)O[t][c][r];
                     }
                 }
             }
@@ -549,18 +671,19 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void chunk_output
 #pragma unroll
                 for (int c = 0; c < CT; ++c) S[r][c] *= d;
 #pragma unroll
-            for (int ks = 0; ks < kChunk; ks += KST) {
+            for (int ks = 0; ks < kChunk / KST; ++ks) {
                 float w[8];
-                row_weights<T>(wt, ks, lane, w);
-                u4 fv[CT];
+                row_weights<T>(wt, ks * KST, lane, w);
+                u4 fw[CT][NT];
 #pragma unroll
-                for (int c = 0; c < CT; ++c)
-                    weighted<T, 1>(frag_rows(Vs, SV::kPitch, ks, (wave * CT + c) * 16, lane), w, &fv[c]);
+                for (int c = 0; c < CT; ++c) weighted<T, NT>(fv[ks][c], w, fw[c]);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const u4 fk = frag_rows(Ks, SK::kPitch, ks, r * 16, lane);
+                    const u4 fk = frag_rows(Ks, SK::kPitch, ks * KST, r * 16, lane);
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) S[r][c] = mma<T>(fk, fv[c], S[r][c]);
+                    for (int c = 0; c < CT; ++c)
+#pragma unroll
+                        for (int t = NT - 1; t >= 0; --t) S[r][c] = mma<T>(fk, fw[c][t], S[r][c]);
                 }
             }
         }
@@ -570,17 +693,34 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void chunk_output
 // ---- gradients of shared heads ---------------------------------------------------
 //
 // out[row][kh][d] = sum over the rep heads that share kh, in order, of the
-// float32 gradients part[row][kh rep + i][d].
-template <typename T>
+// float32 gradients part[row][kh rep + i][d]; four elements a thread where d
+// is a multiple of four. Bound by reading the parts, which mostly still are in
+// the cache behind the L2s: so it follows the kernel that makes them at once.
+template <typename T, int W>
 __global__ __launch_bounds__(kThreads) void sum_heads(const float* part, T* out, int64_t count, int rep, int d)
 {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    typedef float vec __attribute__((ext_vector_type(W)));
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * W;
     if (i >= count) return;
     const int64_t row = i / d;
     const float* q = part + row * rep * d + i % d;
-    float s = q[0];
-    for (int r = 1; r < rep; ++r) s += q[(int64_t)r * d];
-    out[i] = (T)s;
+    vec s = *(const vec*)q;
+#pragma unroll 4
+    for (int r = 1; r < rep; ++r) s += *(const vec*)(q + (int64_t)r * d);
+    struct __attribute__((aligned(sizeof(T)))) Out { T e[W]; } o;
+#pragma unroll
+    for (int k = 0; k < W; ++k) o.e[k] = (T)s[k];
+    *(Out*)(out + i) = o;
+}
+
+template <typename T>
+void launch_sum_heads(const float* part, void* out, int64_t count, int rep, int d, hipStream_t st)
+{
+    const int w = d % 4 == 0 ? 4 : 1;
+    const unsigned grid = (unsigned)((count / w + kThreads - 1) / kThreads);
+    if (grid == 0) return;
+    if (w == 4) sum_heads<T, 4><<<grid, kThreads, 0, st>>>(part, (T*)out, count, rep, d);
+    else sum_heads<T, 1><<<grid, kThreads, 0, st>>>(part, (T*)out, count, rep, d);
 }
 
 // ---- one token --------------------------------------------------------------------
@@ -711,12 +851,16 @@ struct Plan {
 int pad64(int64_t d) { return d <= 64 ? 64 : 128; }
 
 // Segments x heads come to about 512 workgroups, two for each of the 256 CUs
-// (both fit: 70 KB of LDS each), and a segment is whole chunks.
+// (both fit: 64 KB of LDS each), and a segment is whole chunks. Each of packed
+// sequences ends in a part of one, so as many fewer are planned, down to half
+// (7264 tokens in 12 sequences: 110 us, 120 with segments for 512 workgroups
+// before the parts).
 int make_plan(const gconv_linattn_desc* d, Plan* p)
 {
     p->rows = d->packed ? d->tokens : d->sequences * d->tokens;
     const int64_t per_head = std::max<int64_t>(1, 512 / d->heads);
-    const int64_t seg = (p->rows + per_head - 1) / per_head;
+    const int64_t whole = d->packed ? std::max((per_head + 1) / 2, per_head - d->sequences) : per_head;
+    const int64_t seg = (p->rows + whole - 1) / whole;
     p->seg = (int)std::max<int64_t>(kChunk, (seg + kChunk - 1) / kChunk * kChunk);
     p->slots_per_seq = (int)((d->tokens + p->seg - 1) / p->seg);
     const int64_t slots = d->packed ? d->tokens / p->seg + d->sequences : d->sequences * p->slots_per_seq;
@@ -728,10 +872,20 @@ int make_plan(const gconv_linattn_desc* d, Plan* p)
     return GCONV_OK;
 }
 
-Operand operand(const void* p, const int64_t* stride, int hdiv, int64_t dim, int64_t es)
+// The end of a strided tensor whose strides are not negative, else NULL.
+const char* end_of(const gconv_linattn_desc* d, const void* p, const int64_t* s, int64_t heads, int64_t dim, int64_t es)
 {
-    Operand o{p, stride[0], stride[1], stride[2], hdiv, (int)dim, 0};
-    o.vec = ((uintptr_t)p & 15) == 0 && stride[0] * es % 16 == 0 && stride[1] * es % 16 == 0 && stride[2] * es % 16 == 0 &&
+    if (s[1] < 0 || s[2] < 0 || (!d->packed && s[0] < 0) || d->tokens < 1 || d->sequences < 1) return nullptr;
+    int64_t last = (d->tokens - 1) * s[1] + (heads - 1) * s[2] + dim;
+    if (!d->packed) last += (d->sequences - 1) * s[0];
+    return (const char*)p + last * es;
+}
+
+Operand operand(const gconv_linattn_desc* d, const void* p, const int64_t* stride, int64_t heads, int hdiv, int64_t dim, int64_t es)
+{
+    Operand o{p, stride[0], stride[1], stride[2], hdiv, (int)dim, 0, end_of(d, p, stride, heads, dim, es)};
+    // (a chunk's 64 rows span less than 2^31 bytes)
+    o.vec = stride[1] >= 0 && stride[1] < ((int64_t)1 << 22) && ((uintptr_t)p & 15) == 0 && stride[0] * es % 16 == 0 && stride[1] * es % 16 == 0 && stride[2] * es % 16 == 0 &&
             dim * es % 16 == 0;
     return o;
 }
@@ -739,7 +893,11 @@ Operand operand(const void* p, const int64_t* stride, int hdiv, int64_t dim, int
 template <typename T, int DK, int DV>
 void launch_states(const Pass& a, hipStream_t st)
 {
-    if (a.slots > 0) segment_sums<T, DK, DV><<<a.slots * a.heads, kThreads, 0, st>>>(a);
+    const unsigned grid = a.slots * a.heads;
+    if (grid > 0) {
+        if (a.k.vec && a.v.vec) segment_sums<T, DK, DV, true><<<grid, kThreads, 0, st>>>(a);
+        else segment_sums<T, DK, DV, false><<<grid, kThreads, 0, st>>>(a);
+    }
     if (a.sequences > 0)
         scan_states<DK, DV><<<a.sequences * a.heads * (DK * DV / 4 / kThreads), kThreads, 0, st>>>(a);
 }
@@ -753,15 +911,22 @@ void states(const Pass& a, int DK, int DV, hipStream_t st)
     else launch_states<T, 128, 128>(a, st);
 }
 
+template <typename T, int DK, int DV>
+void launch_outputs(const Pass& a, hipStream_t st)
+{
+    const unsigned grid = a.slots * a.heads;
+    if (grid == 0) return;
+    if (a.q.vec && a.k.vec && a.v.vec) chunk_outputs<T, DK, DV, true><<<grid, kThreads, 0, st>>>(a);
+    else chunk_outputs<T, DK, DV, false><<<grid, kThreads, 0, st>>>(a);
+}
+
 template <typename T>
 void outputs(const Pass& a, int DK, int DV, hipStream_t st)
 {
-    const int grid = a.slots * a.heads;
-    if (grid == 0) return;
-    if (DK == 64 && DV == 64) chunk_outputs<T, 64, 64><<<grid, kThreads, 0, st>>>(a);
-    else if (DK == 64) chunk_outputs<T, 64, 128><<<grid, kThreads, 0, st>>>(a);
-    else if (DV == 64) chunk_outputs<T, 128, 64><<<grid, kThreads, 0, st>>>(a);
-    else chunk_outputs<T, 128, 128><<<grid, kThreads, 0, st>>>(a);
+    if (DK == 64 && DV == 64) launch_outputs<T, 64, 64>(a, st);
+    else if (DK == 64) launch_outputs<T, 64, 128>(a, st);
+    else if (DV == 64) launch_outputs<T, 128, 64>(a, st);
+    else launch_outputs<T, 128, 128>(a, st);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -770,8 +935,8 @@ size_t workspace_bytes(const gconv_linattn_desc* d, const Plan& p, int op)
 {
     const size_t one = up256((size_t)p.state_elems * 4);
     if (op == GCONV_LINATTN_FWD) return one;
-    // float32 gradients of each q head where heads share k and v
-    const size_t part = d->heads != d->kv_heads ? up256((size_t)p.rows * d->heads * (d->dk + d->dv) * 4) : 0;
+    // float32 gradients of each q head where heads share k and v, of one of the two at a time
+    const size_t part = d->heads != d->kv_heads ? up256((size_t)p.rows * d->heads * std::max(d->dk, d->dv) * 4) : 0;
     return one + part;
 }
 
@@ -847,11 +1012,11 @@ int run_bwd(const gconv_linattn_desc* d, const Plan& p, const Pass& a, const Ope
     r.final_more = 1;
     states<T>(r, p.DK, p.DV, st);
     r.out_f32 = part != nullptr;
-    float* part_dv = part ? part + p.rows * d->heads * d->dk : nullptr;
     Pass v = r;
     v.q = a.k;
-    dense_out(&v, part ? part_dv : dv, d->heads, d->dv);
+    dense_out(&v, part ? part : dv, d->heads, d->dv);
     outputs<T>(v, p.DK, p.DV, st);
+    if (part) launch_sum_heads<T>(part, dv, p.rows * d->kv_heads * d->dv, rep, (int)d->dv, st);
     Pass k = r;
     k.q = a.v;
     k.k = dout;
@@ -861,11 +1026,7 @@ int run_bwd(const gconv_linattn_desc* d, const Plan& p, const Pass& a, const Ope
     k.state_t = 1;
     dense_out(&k, part ? part : dk, d->heads, d->dk);
     outputs<T>(k, p.DV, p.DK, st);
-    if (part && p.rows > 0) {
-        const int64_t nk = p.rows * d->kv_heads * d->dk, nv = p.rows * d->kv_heads * d->dv;
-        sum_heads<T><<<(unsigned)((nk + kThreads - 1) / kThreads), kThreads, 0, st>>>(part, (T*)dk, nk, rep, (int)d->dk);
-        sum_heads<T><<<(unsigned)((nv + kThreads - 1) / kThreads), kThreads, 0, st>>>(part_dv, (T*)dv, nv, rep, (int)d->dv);
-    }
+    if (part) launch_sum_heads<T>(part, dk, p.rows * d->kv_heads * d->dk, rep, (int)d->dk, st);
     return finish();
 }
 
@@ -910,9 +1071,9 @@ int common(const gconv_linattn_desc* d, int op, const void* q, const void* k, co
     const int64_t es = d->dtype == GCONV_BF16 ? 2 : 4;
     const int rep = (int)(d->heads / d->kv_heads);
     *a = Pass{};
-    a->q = operand(q, d->q_stride, 1, d->dk, es);
-    a->k = operand(k, d->k_stride, rep, d->dk, es);
-    a->v = operand(v, d->v_stride, rep, d->dv, es);
+    a->q = operand(d, q, d->q_stride, d->heads, 1, d->dk, es);
+    a->k = operand(d, k, d->k_stride, d->kv_heads, rep, d->dk, es);
+    a->v = operand(d, v, d->v_stride, d->kv_heads, rep, d->dv, es);
     a->log_decay = log_decay;
     a->cu = cu;
     a->tokens = d->tokens;
@@ -984,7 +1145,7 @@ int gconv_linattn_bwd(const gconv_linattn_desc* d, const void* dout, const void*
         for (int j = 0; j < i; ++j)
             if (meets(out[i], out[j])) return fail(GCONV_ERR_ARG, "two gradients overlap");
     a.init = initial_state;
-    const Operand od = operand(dout, d->do_stride, 1, d->dv, es);
+    const Operand od = operand(d, dout, d->do_stride, d->heads, 1, d->dv, es);
     float* part = nullptr;
     if (d->heads != d->kv_heads) part = (float*)((char*)workspace + up256((size_t)p.state_elems * 4));
     hipStream_t hs = (hipStream_t)stream;
@@ -1018,9 +1179,9 @@ int gconv_linattn_step(const gconv_linattn_desc* d, const void* q, const void* k
     if (d->sequences == 0) return finish();
     Step a{};
     const int rep = (int)(d->heads / d->kv_heads);
-    a.q = operand(q, d->q_stride, 1, d->dk, es);
-    a.k = operand(k, d->k_stride, rep, d->dk, es);
-    a.v = operand(v, d->v_stride, rep, d->dv, es);
+    a.q = operand(d, q, d->q_stride, d->heads, 1, d->dk, es);
+    a.k = operand(d, k, d->k_stride, d->kv_heads, rep, d->dk, es);
+    a.v = operand(d, v, d->v_stride, d->kv_heads, rep, d->dv, es);
     a.log_decay = log_decay;
     a.state = state;
     a.slots = slots;

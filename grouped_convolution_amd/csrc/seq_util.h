@@ -93,6 +93,16 @@ __device__ __forceinline__ u4 frag_cols(const T* tile, int pitch, int row0, int 
     return *(const u4*)(tile + (row0 + (lane & 15)) * pitch + col0 + (lane >> 4) * Frag<T>::kElems);
 }
 
+// The same with the reduction in the order of frag_rows.
+template <typename T>
+__device__ __forceinline__ u4 frag_split(const T* tile, int pitch, int row0, int col0, int lane)
+{
+    const T* p = tile + (row0 + (lane & 15)) * pitch + col0 + (lane >> 4) * 4;
+    if constexpr (sizeof(T) == 4) return *(const u4*)p;
+    const u2 lo = *(const u2*)p, hi = *(const u2*)(p + 16);
+    return u4{lo[0], lo[1], hi[0], hi[1]};
+}
+
 // 16 bytes of a row that holds `dim` elements, from element `col` (a multiple
 // of the 16 bytes); elements past the row read 0. `vec`: rows start on 16
 // bytes and hold whole 16-byte pieces.
