@@ -225,9 +225,15 @@ def version() -> int:
 
 # ---------------------------------------------------------------- tensor level
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev_f32(t, name):
@@ -250,6 +256,16 @@ def _ptr(t):
 def _stream(device):
     torch = _torch()
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _addr(t):
+    """_ptr as a plain number, which ctypes takes for a pointer at less cost."""
+    return t.data_ptr() if t is not None else None
+
+
+def _raw_stream(device):
+    """_stream as a plain number: torch's own short way to it, where a call's cost counts."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _workspace(desc, op, device, workspace):
@@ -469,6 +485,28 @@ def _dense(t, name, shape, dtype, device):
     return t
 
 
+# What a call's descriptor and checks come to depends on its tensors' shapes, strides, types and
+# devices alone, so it is kept by those: a repeated call of a decoding loop costs the host a
+# lookup in place of the checks (one token 14 -> 8 us a call).
+_plans = {}
+
+
+def _plan(kind, tensors, numbers, make):
+    """make()'s answer, kept by the layout of `tensors` and by `numbers` (plain numbers, texts or None)."""
+    try:
+        key = (kind, numbers, tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in tensors]))
+        plan = _plans.get(key)
+    except (AttributeError, TypeError):  # not tensors: make() says what is wrong
+        return make()
+    if plan is None:
+        plan = make()
+        if all(n is None or type(n) in (int, float, str) for n in numbers):
+            if len(_plans) >= 4096:
+                _plans.clear()
+            _plans[key] = plan
+    return plan
+
+
 def _dtype_code(t):
     return BF16 if t.dtype == _torch().bfloat16 else F32
 
@@ -549,14 +587,16 @@ def gconv_linattn_fwd(q, k, v, log_decay, *, scale=None, cu_seqlens=None, initia
     cu_seqlens (int32 [N + 1]) where sequences are packed. log_decay [H] float32; scale
     defaults to dk^-0.5; initial_state [N, H, dk, dv] float32 or None.
     Returns o (q's type) and the final state [N, H, dk, dv] float32."""
-    torch = _torch()
-    d, states = _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state)
-    o = torch.empty(q.shape[:-1] + (states[3],), dtype=q.dtype, device=q.device)
-    final = torch.empty(states, dtype=torch.float32, device=q.device)
-    ws, nws = _scratch(gconv_linattn_workspace_size(d, LINATTN_FWD), q.device, workspace)
-    _check(load().gconv_linattn_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens),
-                                    _ptr(initial_state), _ptr(o), _ptr(final), _ptr(ws), nws, _stream(q.device)),
-           "gconv_linattn_fwd")
+    def make():
+        d, states = _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state)
+        return ctypes.byref(d), states, q.shape[:-1] + (states[3],), gconv_linattn_workspace_size(d, LINATTN_FWD)
+
+    d, states, shape, need = _plan("linattn_fwd", (q, k, v, log_decay, cu_seqlens, initial_state), (scale,), make)
+    o = q.new_empty(shape)
+    final = log_decay.new_empty(states)
+    ws, nws = _scratch(need, q.device, workspace)
+    _check(load().gconv_linattn_fwd(d, _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens), _addr(initial_state),
+                                    _addr(o), _addr(final), _addr(ws), nws, _raw_stream(q.device)), "gconv_linattn_fwd")
     return o, final
 
 
@@ -565,24 +605,23 @@ def gconv_linattn_bwd(do, q, k, v, log_decay, *, scale=None, cu_seqlens=None, in
     """Gradients of gconv_linattn_fwd for the gradient `do` of o and `d_final_state` of the final
     state (None: 0). Returns dq, dk, dv (inputs' type and shape, dense) and the gradient of
     initial_state (None if that is None)."""
-    torch = _torch()
-    d, states = _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state, do)
-    if d_final_state is not None:
-        _dense(d_final_state, "d_final_state", states, torch.float32, q.device)
-    dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-    ds = torch.empty(states, dtype=torch.float32, device=q.device) if initial_state is not None else None
-    ws, nws = _scratch(gconv_linattn_workspace_size(d, LINATTN_BWD), q.device, workspace)
-    _check(load().gconv_linattn_bwd(ctypes.byref(d), _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                    _ptr(cu_seqlens), _ptr(initial_state), _ptr(d_final_state), _ptr(dq), _ptr(dk),
-                                    _ptr(dv), _ptr(ds), _ptr(ws), nws, _stream(q.device)), "gconv_linattn_bwd")
+    def make():
+        d, states = _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state, do)
+        if d_final_state is not None:
+            _dense(d_final_state, "d_final_state", states, _torch().float32, q.device)
+        return ctypes.byref(d), states, gconv_linattn_workspace_size(d, LINATTN_BWD)
+
+    d, states, need = _plan("linattn_bwd", (do, q, k, v, log_decay, cu_seqlens, initial_state, d_final_state), (scale,), make)
+    dq, dk, dv = (t.new_empty(t.shape) for t in (q, k, v))
+    ds = log_decay.new_empty(states) if initial_state is not None else None
+    ws, nws = _scratch(need, q.device, workspace)
+    _check(load().gconv_linattn_bwd(d, _addr(do), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens),
+                                    _addr(initial_state), _addr(d_final_state), _addr(dq), _addr(dk), _addr(dv), _addr(ds),
+                                    _addr(ws), nws, _raw_stream(q.device)), "gconv_linattn_bwd")
     return dq, dk, dv, ds
 
 
-def gconv_linattn_step(q, k, v, log_decay, state, *, scale=None, slots=None, out=None):
-    """One token of each of B sequences, in place on `state`: q [B, H, dk], k [B, Hk, dk],
-    v [B, Hk, dv] (float32 or bfloat16, any strides with a contiguous last axis), state
-    [slots, H, dk, dv] float32, slots int32 [B] (different ones; one out of range gives o = 0
-    and touches no state) or None for slot b. Returns o [B, H, dv]."""
+def _linattn_step_plan(q, k, v, log_decay, state, scale, slots, out):
     torch = _torch()
     _seq(q, "q")
     for t, name in ((k, "k"), (v, "v")):
@@ -601,16 +640,26 @@ def gconv_linattn_step(q, k, v, log_decay, state, *, scale=None, slots=None, out
     _dense(state, "state", (state.shape[0], H, dk, dv), torch.float32, q.device)
     if slots is not None:
         _dense(slots, "slots", (B,), torch.int32, q.device)
-    if out is None:
-        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
-    else:
+    if out is not None:
         _dense(out, "out", (B, H, dv), q.dtype, q.device)
     i3 = ctypes.c_int64 * 3
     sq, sk, sv = q.stride(), k.stride(), v.stride()
     d = gconv_linattn_desc(_dtype_code(q), 0, B, 0, H, Hk, dk, dv, i3(sq[0], 0, sq[1]), i3(sk[0], 0, sk[1]),
                            i3(sv[0], 0, sv[1]), i3(), float(dk ** -0.5 if scale is None else scale))
-    _check(load().gconv_linattn_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state),
-                                     _ptr(slots), state.shape[0], _ptr(out), _stream(q.device)), "gconv_linattn_step")
+    return ctypes.byref(d), (B, H, dv), state.shape[0], load().gconv_linattn_step
+
+
+def gconv_linattn_step(q, k, v, log_decay, state, *, scale=None, slots=None, out=None):
+    """One token of each of B sequences, in place on `state`: q [B, H, dk], k [B, Hk, dk],
+    v [B, Hk, dv] (float32 or bfloat16, any strides with a contiguous last axis), state
+    [slots, H, dk, dv] float32, slots int32 [B] (different ones; one out of range gives o = 0
+    and touches no state) or None for slot b. Returns o [B, H, dv]."""
+    d, shape, num, call = _plan("linattn_step", (q, k, v, log_decay, state, slots, out), (scale,),
+                                lambda: _linattn_step_plan(q, k, v, log_decay, state, scale, slots, out))
+    if out is None:
+        out = q.new_empty(shape)
+    _check(call(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), _addr(slots), num,
+                out.data_ptr(), _raw_stream(q.device)), "gconv_linattn_step")
     return out
 
 
@@ -655,12 +704,12 @@ def gconv_normgate_fwd(x, b, *, w_post, gate=None, act="silu", scale=None, w_pre
     strides with a contiguous last axis); x like b or None; gate like b, or [N, 1, D] ([1, D])
     for one row a sequence, or None; act "none", "sigmoid" or "silu"; w_post, scale, w_pre [D],
     the last two may be None. Returns y and h (None without w_pre)."""
-    torch = _torch()
-    d = _normgate_desc(x, b, gate, act, w_post, scale, w_pre, eps)
-    y = torch.empty(b.shape, dtype=b.dtype, device=b.device)
-    h = torch.empty(b.shape, dtype=b.dtype, device=b.device) if w_pre is not None else None
-    _check(load().gconv_normgate_fwd(ctypes.byref(d), _ptr(x), _ptr(b), _ptr(gate), _ptr(w_post), _ptr(scale), _ptr(w_pre),
-                                     _ptr(y), _ptr(h), _stream(b.device)), "gconv_normgate_fwd")
+    d = _plan("normgate_fwd", (x, b, gate, w_post, scale, w_pre), (act, eps),
+              lambda: ctypes.byref(_normgate_desc(x, b, gate, act, w_post, scale, w_pre, eps)))
+    y = b.new_empty(b.shape)
+    h = b.new_empty(b.shape) if w_pre is not None else None
+    _check(load().gconv_normgate_fwd(d, _addr(x), b.data_ptr(), _addr(gate), w_post.data_ptr(), _addr(scale), _addr(w_pre),
+                                     y.data_ptr(), _addr(h), _raw_stream(b.device)), "gconv_normgate_fwd")
     return y, h
 
 
@@ -668,40 +717,46 @@ def gconv_normgate_bwd(dy, dh, x, b, *, w_post, gate=None, act="silu", scale=Non
     """Gradients of gconv_normgate_fwd for dy of y and dh of h (None without w_pre). Returns
     dx, db, dgate, dw_post, dscale, dw_pre, of the inputs' shapes and type (None for those that
     are None)."""
-    torch = _torch()
-    d = _normgate_desc(x, b, gate, act, w_post, scale, w_pre, eps, _seq(dy, "dy"), dh)
-    if (dh is None) != (w_pre is None):
-        raise ValueError("dh must be given exactly when w_pre is")
-    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device) if t is not None else None  # noqa: E731
-    dx, db, dgate, dw_post, dscale, dw_pre = (new(t) for t in (x, b, gate, w_post, scale, w_pre))
-    n = ctypes.c_size_t()
-    _check(load().gconv_normgate_workspace_size(ctypes.byref(d), ctypes.byref(n)), "gconv_normgate_workspace_size")
-    ws, nws = _scratch(n.value, b.device, workspace)
-    _check(load().gconv_normgate_bwd(ctypes.byref(d), _ptr(dy), _ptr(dh), _ptr(x), _ptr(b), _ptr(gate), _ptr(w_post),
-                                     _ptr(scale), _ptr(w_pre), _ptr(dx), _ptr(db), _ptr(dgate), _ptr(dw_post), _ptr(dscale),
-                                     _ptr(dw_pre), _ptr(ws), nws, _stream(b.device)), "gconv_normgate_bwd")
-    return dx, db, dgate, dw_post, dscale, dw_pre
+    def make():
+        d = _normgate_desc(x, b, gate, act, w_post, scale, w_pre, eps, _seq(dy, "dy"), dh)
+        if (dh is None) != (w_pre is None):
+            raise ValueError("dh must be given exactly when w_pre is")
+        n = ctypes.c_size_t()
+        _check(load().gconv_normgate_workspace_size(ctypes.byref(d), ctypes.byref(n)), "gconv_normgate_workspace_size")
+        return ctypes.byref(d), n.value
+
+    d, need = _plan("normgate_bwd", (dy, dh, x, b, gate, w_post, scale, w_pre), (act, eps), make)
+    out = [t.new_empty(t.shape) if t is not None else None for t in (x, b, gate, w_post, scale, w_pre)]
+    ws, nws = _scratch(need, b.device, workspace)
+    _check(load().gconv_normgate_bwd(d, _addr(dy), _addr(dh), _addr(x), _addr(b), _addr(gate), _addr(w_post), _addr(scale),
+                                     _addr(w_pre), *(_addr(t) for t in out), _addr(ws), nws, _raw_stream(b.device)),
+           "gconv_normgate_bwd")
+    return tuple(out)
 
 
 def gconv_orthogonalize(u, *, groups=1, steps=5, eps=1e-7, out=None, workspace=None):
     """The orthogonalised update of a weight gradient u [K, C/groups, kh, kw] (or [K, D]; float32 or
     bfloat16, contiguous): each group's [K/groups, C/groups kh kw] matrix, scaled to norm 1, after
     `steps` rounds of the Newton-Schulz iteration. Returns a bfloat16 tensor of u's shape."""
-    torch = _torch()
-    _seq(u, "u")
-    if u.dim() < 2:
-        raise ValueError("u must be [K, ...] with at least two axes")
-    if not u.is_contiguous():
-        raise ValueError("u must be contiguous")
-    K = u.shape[0]
-    d = gconv_ortho_desc(_dtype_code(u), K, u.numel() // K if K else 0, int(groups), int(steps), float(eps))
-    n = ctypes.c_size_t()
-    _check(load().gconv_orthogonalize_workspace_size(ctypes.byref(d), ctypes.byref(n)), "gconv_orthogonalize_workspace_size")
+    def make():
+        torch = _torch()
+        _seq(u, "u")
+        if u.dim() < 2:
+            raise ValueError("u must be [K, ...] with at least two axes")
+        if not u.is_contiguous():
+            raise ValueError("u must be contiguous")
+        if out is not None:
+            _dense(out, "out", u.shape, torch.bfloat16, u.device)
+        K = u.shape[0]
+        d = gconv_ortho_desc(_dtype_code(u), K, u.numel() // K if K else 0, int(groups), int(steps), float(eps))
+        n = ctypes.c_size_t()
+        _check(load().gconv_orthogonalize_workspace_size(ctypes.byref(d), ctypes.byref(n)), "gconv_orthogonalize_workspace_size")
+        return ctypes.byref(d), n.value
+
+    d, need = _plan("orthogonalize", (u, out), (groups, steps, eps), make)
     if out is None:
-        out = torch.empty(u.shape, dtype=torch.bfloat16, device=u.device)
-    else:
-        _dense(out, "out", u.shape, torch.bfloat16, u.device)
-    ws, nws = _scratch(n.value, u.device, workspace)
-    _check(load().gconv_orthogonalize(ctypes.byref(d), _ptr(u), _ptr(out), _ptr(ws), nws, _stream(u.device)),
+        out = u.new_empty(u.shape, dtype=_torch().bfloat16)
+    ws, nws = _scratch(need, u.device, workspace)
+    _check(load().gconv_orthogonalize(d, u.data_ptr(), out.data_ptr(), _addr(ws), nws, _raw_stream(u.device)),
            "gconv_orthogonalize")
     return out

@@ -935,8 +935,8 @@ size_t workspace_bytes(const gconv_linattn_desc* d, const Plan& p, int op)
 {
     const size_t one = up256((size_t)p.state_elems * 4);
     if (op == GCONV_LINATTN_FWD) return one;
-    // float32 gradients of each q head where heads share k and v, of one of the two at a time
-    const size_t part = d->heads != d->kv_heads ? up256((size_t)p.rows * d->heads * std::max(d->dk, d->dv) * 4) : 0;
+    // float32 gradients of each q head where heads share k and v
+    const size_t part = d->heads != d->kv_heads ? up256((size_t)p.rows * d->heads * d->dk * 4) + up256((size_t)p.rows * d->heads * d->dv * 4) : 0;
     return one + part;
 }
 
@@ -1012,11 +1012,12 @@ int run_bwd(const gconv_linattn_desc* d, const Plan& p, const Pass& a, const Ope
     r.final_more = 1;
     states<T>(r, p.DK, p.DV, st);
     r.out_f32 = part != nullptr;
+    float* part_dv = part ? part + up256((size_t)p.rows * d->heads * d->dk * 4) / 4 : nullptr;
     Pass v = r;
     v.q = a.k;
-    dense_out(&v, part ? part : dv, d->heads, d->dv);
+    dense_out(&v, part ? part_dv : dv, d->heads, d->dv);
     outputs<T>(v, p.DK, p.DV, st);
-    if (part) launch_sum_heads<T>(part, dv, p.rows * d->kv_heads * d->dv, rep, (int)d->dv, st);
+    if (part) launch_sum_heads<T>(part_dv, dv, p.rows * d->kv_heads * d->dv, rep, (int)d->dv, st);
     Pass k = r;
     k.q = a.v;
     k.k = dout;
