@@ -389,7 +389,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(Norm a)
 }
 
 // out[which][col] = sum over `count` partial rows, in an order fixed by the
-// shape: 64 columns a workgroup, 16 slices of the rows, then the slices.
+// shape: 64 columns a workgroup, 16 slices of the rows, then the slices. The
+// first layer of the grid folds the weights' gradients, the others those of
+// the sequences' gates.
 template <typename T>
 struct Fold {
     const float* part;
@@ -399,14 +401,16 @@ struct Fold {
 };
 
 template <typename T>
-__global__ __launch_bounds__(1024) void fold_rows(Fold<T> a)
+__global__ __launch_bounds__(1024) void fold_rows(Fold<T> weights, Fold<T> gates)
 {
     __shared__ float red[16][65];
     const int c = threadIdx.x & 63, slice = threadIdx.x >> 6;
     const int col = blockIdx.x * 64 + c, which = blockIdx.y;
-    T* out = gridDim.z > 1 ? a.out[0] : which == 0 ? a.out[0] : which == 1 ? a.out[1] : a.out[2];
+    const Fold<T>& a = blockIdx.z == 0 ? weights : gates;
+    const int group = blockIdx.z == 0 ? 0 : blockIdx.z - 1;
+    T* out = which == 0 ? a.out[0] : which == 1 ? a.out[1] : a.out[2];
     if (!out) return;
-    const float* p = a.part + blockIdx.z * a.group_stride + (int64_t)which * a.dim + col;
+    const float* p = a.part + group * a.group_stride + (int64_t)which * a.dim + col;
     float s = 0.f;
     if (col < a.dim) {
         int i = slice;
@@ -422,7 +426,7 @@ __global__ __launch_bounds__(1024) void fold_rows(Fold<T> a)
         float v = 0.f;
 #pragma unroll
         for (int k = 0; k < 16; ++k) v += red[k][c];
-        out[(int64_t)blockIdx.z * a.dim + col] = (T)v;
+        out[(int64_t)group * a.dim + col] = (T)v;
     }
 }
 
@@ -533,11 +537,10 @@ void run_bwd(const gconv_normgate_desc* d, const Norm& a, const Grid& g, void* d
     if (g.blocks > 0) launch<T>(a, tpr, true, g.blocks, st);
     Fold<T> f{a.part, (int64_t)3 * d->dim, 0, g.blocks, (int)d->dim, {(T*)dw_post, (T*)dscale, (T*)dw_pre}};
     const unsigned cols = (unsigned)((d->dim + 63) / 64);
-    fold_rows<T><<<dim3(cols, 3, 1), 1024, 0, st>>>(f);
-    if (a.gate_part) {
-        Fold<T> s{a.gate_part, d->dim, (int64_t)g.splits * d->dim, g.splits, (int)d->dim, {(T*)a.dgate, nullptr, nullptr}};
-        fold_rows<T><<<dim3(cols, 1, (unsigned)g.groups), 1024, 0, st>>>(s);
-    }
+    Fold<T> s{};
+    if (a.gate_part)
+        s = Fold<T>{a.gate_part, d->dim, (int64_t)g.splits * d->dim, g.splits, (int)d->dim, {(T*)a.dgate, nullptr, nullptr}};
+    fold_rows<T><<<dim3(cols, 3, a.gate_part ? 1 + (unsigned)g.groups : 1), 1024, 0, st>>>(f, s);
 }
 
 void fill(const gconv_normgate_desc* d, Norm* a)
