@@ -5,10 +5,15 @@
 //   h = y * ry * w_pre,                              ry = (mean y^2 + eps)^-1/2
 //
 // A row is held in registers from its one read to its one write: TPR threads a
-// row, eight elements (VPT 16-byte pieces) a thread, so both norms and every
+// row (4 to 1024: 962626 rows of 32 by 16 threads each took 783 us, forward and
+// backward, 200 by 4), eight elements (VPT 16-byte pieces) a thread, so both norms and every
 // product cost no second pass. Workgroups walk over rows with the weights in registers. What
-// bounds it is HBM: (b, gate, x in; y, h out) forward, and the same with their
-// gradients backward.
+// bounds it is HBM: (b, gate, x in; y, h out) forward, at the copy rate (16384
+// rows of 4096: 125 us, 5.3 TB/s), and the same with their gradients backward,
+// where the sums over rows and up to five tensors' values leave room for one or
+// two waves a SIMD (262144 rows of 128: 79 us, 4.2 TB/s; 16384 of 4096: 345 us,
+// 3.1 TB/s). Tried and dropped: loading the next row ahead (forward 127 -> 147
+// us: fewer waves), reading past odd rows' ends and masking (76 -> 102 us).
 //
 // Backward, with e = dh w_pre and yn = y ry:
 //   dy' = dy + ry (e - yn mean(e yn))                          dx = dy'
@@ -44,6 +49,7 @@ struct Norm {
     int splits;         // workgroups of a group, or 1 with `groups` spread over the grid
     int64_t group_rows;
     int dim, act, gate_seq;
+    int flat;           // rows follow one another at their token strides: the sequence is not asked for
     float eps, inv_dim;
 };
 
@@ -138,6 +144,17 @@ __device__ __forceinline__ const T* row_ptr(const Rows& r, int64_t n, int64_t t)
     return (const T*)r.p + n * r.seq + t * r.tok;
 }
 
+// Row r's sequence and its token in that. (A 64-bit division costs more than
+// the rest of a short row.)
+__device__ __forceinline__ void place_of(const Norm& a, int64_t r, int64_t* n, int64_t* t)
+{
+    *n = 0;
+    *t = r;
+    if (a.flat) return;
+    *n = a.rows <= 0x7fffffff ? (int64_t)((uint32_t)r / (uint32_t)a.tokens) : r / a.tokens;
+    *t = r - *n * a.tokens;
+}
+
 template <typename T, int TPR>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(Norm a)
 {
@@ -155,7 +172,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(Norm a)
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
         const bool live = r0 + sub < a.rows;
         const int64_t r = live ? r0 + sub : r0;
-        const int64_t n = r / a.tokens, t = r - n * a.tokens;
+        int64_t n, t;
+        place_of(a, r, &n, &t);
         u4 rb_[VPT], rg[VPT], rx[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -270,7 +288,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(Norm a)
         for (int64_t q0 = (int64_t)split * RPB; q0 < a.group_rows; q0 += (int64_t)a.splits * RPB) {
             const bool live = q0 + sub < a.group_rows;
             const int64_t r = (int64_t)g * a.group_rows + (live ? q0 + sub : q0);
-            const int64_t n = r / a.tokens, t = r - n * a.tokens;
+            int64_t n = g, t = r - (int64_t)g * a.group_rows;
+            if (!GSEQ) place_of(a, r, &n, &t);
             u4 rb_[VPT], rg[VPT], rx[VPT], rdy[VPT], rdh[VPT];
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -455,7 +474,7 @@ int check_desc(const gconv_normgate_desc* d)
 // Threads a row: the power of two that holds it at eight elements each.
 int row_threads(const gconv_normgate_desc* d)
 {
-    int tpr = 16;
+    int tpr = 4;
     while (tpr * kPerThread < d->dim) tpr *= 2;
     return tpr;
 }
@@ -520,6 +539,8 @@ template <typename T>
 void launch(const Norm& a, int tpr, bool bwd, int blocks, hipStream_t st)
 {
     switch (tpr) {
+        case 4: launch_row<T, 4>(a, bwd, blocks, st); break;
+        case 8: launch_row<T, 8>(a, bwd, blocks, st); break;
         case 16: launch_row<T, 16>(a, bwd, blocks, st); break;
         case 32: launch_row<T, 32>(a, bwd, blocks, st); break;
         case 64: launch_row<T, 64>(a, bwd, blocks, st); break;
@@ -543,8 +564,14 @@ void run_bwd(const gconv_normgate_desc* d, const Norm& a, const Grid& g, void* d
     fold_rows<T><<<dim3(cols, 3, a.gate_part ? 1 + (unsigned)g.groups : 1), 1024, 0, st>>>(f, s);
 }
 
+bool follow(const gconv_normgate_desc* d, const Rows& r)
+{
+    return !r.p || d->sequences == 1 || r.seq == d->tokens * r.tok;
+}
+
 void fill(const gconv_normgate_desc* d, Norm* a)
 {
+    a->flat = follow(d, a->x) && follow(d, a->b) && follow(d, a->gate) && follow(d, a->dy) && follow(d, a->dh);
     a->tokens = std::max<int64_t>(d->tokens, 1);
     a->rows = d->sequences * d->tokens;
     a->dim = (int)d->dim;
@@ -593,10 +620,10 @@ int gconv_normgate_fwd(const gconv_normgate_desc* d, const void* x, const void* 
     (void)hipGetLastError();
     if (rows == 0) return finish();
     Norm a{};
-    fill(d, &a);
     a.x = Rows{x, d->x_stride[0], d->x_stride[1]};
     a.b = Rows{b, d->b_stride[0], d->b_stride[1]};
-    a.gate = Rows{gate, d->gate_stride[0], a.gate_seq ? 0 : d->gate_stride[1]};
+    a.gate = Rows{gate, d->gate_stride[0], d->gate == GCONV_GATE_SEQUENCE ? 0 : d->gate_stride[1]};
+    fill(d, &a);
     a.w_post = w_post;
     a.scale = scale;
     a.w_pre = w_pre;
@@ -646,12 +673,12 @@ int gconv_normgate_bwd(const gconv_normgate_desc* d, const void* dy, const void*
     hipStream_t hs = (hipStream_t)stream;
     (void)hipGetLastError();
     Norm a{};
-    fill(d, &a);
     a.x = Rows{x, d->x_stride[0], d->x_stride[1]};
     a.b = Rows{b, d->b_stride[0], d->b_stride[1]};
-    a.gate = Rows{gate, d->gate_stride[0], a.gate_seq ? 0 : d->gate_stride[1]};
+    a.gate = Rows{gate, d->gate_stride[0], d->gate == GCONV_GATE_SEQUENCE ? 0 : d->gate_stride[1]};
     a.dy = Rows{dy, d->dy_stride[0], d->dy_stride[1]};
     a.dh = Rows{dh, d->dh_stride[0], d->dh_stride[1]};
+    fill(d, &a);
     a.w_post = w_post;
     a.scale = scale;
     a.w_pre = w_pre;
