@@ -14,7 +14,9 @@
 //   chunk_outputs  walks the chunks of a segment with its state in registers
 // so the tokens are read once (k and v twice) and states pass through memory
 // once a segment only. The host picks the segment length so that segments x
-// heads give about two workgroups a CU.
+// heads give about two workgroups a CU. All three are bound by memory: 32768
+// tokens x 16 heads take 66 us for 268 MB, 14 for 67 and 129 for 537 (4.1, 4.9
+// and 4.2 TB/s; a large copy reaches 5.2).
 //
 // The gradients are the same recurrence with the roles of the tensors changed,
 // forwards for dq and backwards in time for dk and dv:
@@ -728,7 +730,8 @@ void launch_sum_heads(const float* part, void* out, int64_t count, int rep, int 
 // A workgroup updates CW columns of one head's state: each thread reads its
 // pieces of the state (all in flight at once), adds k v^T, writes them back
 // and keeps q_row x S; the rows' partial answers meet in LDS. Bound by the
-// state's traffic, 8 dk dv bytes a head.
+// state's traffic, 8 dk dv bytes a head (256 tokens of 16 heads: 120 us for
+// 541 MB, 4.5 TB/s); one token of 16 heads by its latency, 5.3 us.
 struct Step {
     Operand q, k, v;
     const float* log_decay;

@@ -12,8 +12,12 @@
 //   SQUARE  B[i][j]  = b A[i][j] + c sum_k A[i][k] A[j][k]   likewise
 //   UPDATE  X'[i][j] = a X[i][j] + sum_k B[i][k] X[k][j]
 //
-// Bound by the matrix pipes: 5 rounds of 4096 x 9216 are 2.7 TFLOP with the
-// symmetric halves left out.
+// Bound by the matrix pipes and the power they draw: 5 rounds of 4096 x 9216
+// are 2.7 TFLOP with the symmetric halves left out and take 2.55 ms, 1.04
+// PFLOP/s; the loops over stages run at 1.22 (a large fp16 library product
+// reaches 1.39 here), and zeros in place of data, which draw less power, take a
+// sixth less. What is left outside the loops is the update's epilogue, 28 us of
+// each of its three rounds, in which all of the chip reads and writes X.
 //
 // X, A and B are kept in fp16, times 2^12, and the products in float32.
 // Rounding them is what the matrix pipes ask for; fp16 has 11 bits where bf16
@@ -141,6 +145,8 @@ __device__ __forceinline__ void triangle(int L, int* q, int* p)
 
 // One BQ x BP tile of an output. The matrix instruction's rows run along the
 // output's columns, so a lane holds four consecutive elements of an output row.
+// Eight waves, two a SIMD, so that one multiplies while the other waits (with
+// four larger ones: Gram matrix 185 us for 151), over a ring of 64-long stages.
 template <int BQ, int BP, int WQ, int WP, int OP>
 __global__ __launch_bounds__(64 * WQ * WP, 1) void ortho_gemm(Ortho a)
 {
@@ -514,12 +520,17 @@ void launch(Ortho a, int64_t groups, hipStream_t st)
 }
 
 // The tile whose whole rounds of 256 workgroups take least: its area, over the
-// share of the matrix pipes that its kernel keeps busy.
+// rate of its kernel against the largest tile's, from products of 4096 x 9216
+// (us a round of that area, epilogues included; update: 256x256 104, 256x192
+// 130, 192x192 122, 128x128 146, 64x64 210; Gram matrix: 178, -, 258, 270,
+// 637). There the rule takes 256x192 for the update (293 us; 256x256 leaves a
+// quarter of its third round: 313) and 192x192 for the Gram matrix, whose 253
+// tiles fill the chip once (145 us; 256x256 has 136 tiles: 178).
 template <int OP>
 void product(const Ortho& a, int64_t groups, hipStream_t st)
 {
     struct Tile { int q, p; double rate; };
-    constexpr Tile tiles[] = {{256, 256, 1.0}, {256, 192, 1.0}, {192, 192, 0.95}, {128, 128, 0.7}, {64, 64, 0.35}};
+    constexpr Tile tiles[] = {{256, 256, 1.0}, {256, 192, 0.8}, {192, 192, 0.75}, {128, 128, 0.68}, {64, 64, 0.4}};
     int best = 0;
     double least = 0;
     for (int i = 0; i < 5; ++i) {
