@@ -70,6 +70,14 @@ __device__ __forceinline__ u4 load_loose(const T* row, int col, int dim)
     return __builtin_bit_cast(u4, e);
 }
 
+// Pieces of ones.
+template <typename T>
+__device__ __forceinline__ u4 ones()
+{
+    constexpr uint32_t one = sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
+    return u4{one, one, one, one};
+}
+
 template <typename T>
 struct Vals {
     static constexpr int E = 16 / sizeof(T);
@@ -242,7 +250,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(Norm a)
     for (int i = 0; i < VPT; ++i) {
         const int col = (i * TPR + lane) * E;
         wp[i] = load_loose((const T*)a.w_post, col, a.dim);
-        if (a.scale) sc[i] = load_loose((const T*)a.scale, col, a.dim);
+        sc[i] = a.scale ? load_loose((const T*)a.scale, col, a.dim) : ones<T>();
         if (PRE) wq[i] = load_loose((const T*)a.w_pre, col, a.dim);
 #pragma unroll
         for (int e = 0; e < E; ++e) s_post[i][e] = s_scale[i][e] = s_pre[i][e] = s_gate[i][e] = 0.f;
@@ -290,15 +298,18 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(Norm a)
             const int64_t r = (int64_t)g * a.group_rows + (live ? q0 + sub : q0);
             int64_t n = g, t = r - (int64_t)g * a.group_rows;
             if (!GSEQ) place_of(a, r, &n, &t);
+            // What is absent counts as what leaves the formulas as they are (a gate
+            // of ones, x = 0), and a row past the last has no gradient, so nothing
+            // below has a branch for it.
             u4 rb_[VPT], rg[VPT], rx[VPT], rdy[VPT], rdh[VPT];
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int col = (i * TPR + lane) * E;
                 rb_[i] = load_loose(row_ptr<T>(a.b, n, t), col, a.dim);
-                if (a.gate.p) rg[i] = load_loose(row_ptr<T>(a.gate, n, t), col, a.dim);
+                rg[i] = a.gate.p ? load_loose(row_ptr<T>(a.gate, n, t), col, a.dim) : ones<T>();
                 rdy[i] = load_loose(row_ptr<T>(a.dy, n, t), col, a.dim);
                 if constexpr (PRE) {
-                    if (a.x.p) rx[i] = load_loose(row_ptr<T>(a.x, n, t), col, a.dim);
+                    rx[i] = a.x.p ? load_loose(row_ptr<T>(a.x, n, t), col, a.dim) : u4{0, 0, 0, 0};
                     rdh[i] = load_loose(row_ptr<T>(a.dh, n, t), col, a.dim);
                 }
             }
@@ -310,24 +321,35 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(Norm a)
                 for (int e = 0; e < E; ++e) ss = fmaf(b.v[e], b.v[e], ss);
             }
             const float rb = rsqrtf(row_sum<TPR>(ss, red[0], wave) * a.inv_dim + a.eps);
+            // the gate's sigmoid, 1 where the activation has none: act(z) is it times z (or 1)
+            float sg[VPT][E];
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) sg[i][e] = 1.f;
+            if (a.act != GCONV_ACT_NONE) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const Vals<T> z(rg[i]);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sg[i][e] = sigmoid(z.v[e]);
+                }
+            }
+            const bool plain = a.act == GCONV_ACT_SIGMOID;
             float ry = 0.f, m1 = 0.f;
+            Vals<T> y[VPT];
             if constexpr (PRE) {
                 float sy = 0.f, se = 0.f;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const Vals<T> b(rb_[i]), dh(rdh[i]), wpv(wp[i]), wqv(wq[i]);
-                    Vals<T> gt, x, scv;
-                    if (a.scale) scv = Vals<T>(sc[i]);
-                    if (a.gate.p) gt = Vals<T>(rg[i]);
-                    if (a.x.p) x = Vals<T>(rx[i]);
+                    if (!live) rdy[i] = rdh[i] = u4{0, 0, 0, 0};
+                    const Vals<T> b(rb_[i]), dh(rdh[i]), wpv(wp[i]), wqv(wq[i]), z(rg[i]), x(rx[i]), scv(sc[i]);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        float v = b.v[e] * rb * wpv.v[e];
-                        if (a.gate.p) v *= act_of(gt.v[e], a.act);
-                        if (a.scale) v *= scv.v[e];
-                        if (a.x.p) v += x.v[e];
-                        sy = fmaf(v, v, sy);
-                        se = fmaf(dh.v[e] * wqv.v[e], v, se);
+                        const float av = sg[i][e] * (plain ? 1.f : z.v[e]);
+                        y[i].v[e] = fmaf(b.v[e] * rb * wpv.v[e] * av, scv.v[e], x.v[e]);
+                        sy = fmaf(y[i].v[e], y[i].v[e], sy);
+                        se = fmaf(dh.v[e] * wqv.v[e], y[i].v[e], se);
                     }
                 }
                 ry = rsqrtf(row_sum<TPR>(sy, red[1], wave) * a.inv_dim + a.eps);
@@ -339,37 +361,30 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(Norm a)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int col = (i * TPR + lane) * E;
-                const Vals<T> b(rb_[i]), wpv(wp[i]);
-                Vals<T> gt, x, dh, dyv(rdy[i]), dz, scv, wqv;
-                if (a.scale) scv = Vals<T>(sc[i]);
-                if (a.gate.p) gt = Vals<T>(rg[i]);
+                if (!PRE && !live) rdy[i] = u4{0, 0, 0, 0};
+                const Vals<T> b(rb_[i]), wpv(wp[i]), z(rg[i]), scv(sc[i]);
+                Vals<T> dyv(rdy[i]), dz, dh, wqv;
                 if constexpr (PRE) {
                     dh = Vals<T>(rdh[i]);
                     wqv = Vals<T>(wq[i]);
-                    if (a.x.p) x = Vals<T>(rx[i]);
                 }
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
+                    const float zz = plain ? 1.f : z.v[e], sig = sg[i][e], av = sig * zz;
+                    const float da = a.act == GCONV_ACT_NONE ? 1.f : fmaf(zz, sig * (1.f - sig), plain ? 0.f : sig);
                     const float bn = b.v[e] * rb, nn = bn * wpv.v[e];
-                    float av = 1.f, da = 0.f;
-                    if (a.gate.p) da = act_grad(gt.v[e], a.act, &av);
-                    const float s = a.scale ? scv.v[e] : 1.f;
                     float d = dyv.v[e];
                     if constexpr (PRE) {
-                        float v = nn * av * s;
-                        if (a.x.p) v += x.v[e];
-                        const float yn = v * ry;
+                        const float yn = y[i].v[e] * ry;
                         d += ry * (dh.v[e] * wqv.v[e] - yn * m1);
-                        if (live) s_pre[i][e] = fmaf(dh.v[e], yn, s_pre[i][e]);
+                        s_pre[i][e] = fmaf(dh.v[e], yn, s_pre[i][e]);
                     }
                     dyv.v[e] = d;
-                    const float du = d * s;
-                    if (live) {
-                        s_post[i][e] = fmaf(du * av, bn, s_post[i][e]);
-                        s_scale[i][e] = fmaf(d * av, nn, s_scale[i][e]);
-                    }
+                    const float du = d * scv.v[e];
+                    s_post[i][e] = fmaf(du * av, bn, s_post[i][e]);
+                    s_scale[i][e] = fmaf(d * av, nn, s_scale[i][e]);
                     dz.v[e] = du * nn * da;
-                    if (GSEQ && live) s_gate[i][e] += dz.v[e];
+                    if (GSEQ) s_gate[i][e] += dz.v[e];
                     f[i].v[e] = du * av * wpv.v[e];
                     sf = fmaf(f[i].v[e], bn, sf);
                 }
@@ -575,7 +590,7 @@ void fill(const gconv_normgate_desc* d, Norm* a)
     a->tokens = std::max<int64_t>(d->tokens, 1);
     a->rows = d->sequences * d->tokens;
     a->dim = (int)d->dim;
-    a->act = (int)d->act;
+    a->act = d->gate == GCONV_GATE_NONE ? GCONV_ACT_NONE : (int)d->act;
     a->gate_seq = d->gate == GCONV_GATE_SEQUENCE;
     a->eps = (float)d->eps;
     a->inv_dim = 1.f / (float)d->dim;
