@@ -235,6 +235,18 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_fwd(Norm a)
     }
 }
 
+// Keeps the weights in registers as they were loaded: converted outside the
+// loop over rows they would take up twice as many. Where 1024 threads leave 128
+// registers each (4000 rows of 8000, forward and backward: 346 us for 409;
+// shorter rows lose some 2%).
+constexpr int kTight = 1024;
+template <int N>
+__device__ __forceinline__ void keep_raw(u4 (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+
 // One workgroup: the rows split, split + splits, ... of a group, or (splits ==
 // 1) whole groups, a stretch of them.
 template <typename T, int TPR, bool PRE, bool GSEQ>
@@ -312,6 +324,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd(Norm a)
                     rx[i] = a.x.p ? load_loose(row_ptr<T>(a.x, n, t), col, a.dim) : u4{0, 0, 0, 0};
                     rdh[i] = load_loose(row_ptr<T>(a.dh, n, t), col, a.dim);
                 }
+            }
+            if constexpr (TPR >= kTight) {
+                keep_raw(wp);
+                keep_raw(sc);
+                if (PRE) keep_raw(wq);
             }
             float ss = 0.f;
 #pragma unroll
