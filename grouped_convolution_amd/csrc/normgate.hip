@@ -5,14 +5,14 @@
 //   h = y * ry * w_pre,                              ry = (mean y^2 + eps)^-1/2
 //
 // A row is held in registers from its one read to its one write: TPR threads a
-// row (4 to 1024: 962626 rows of 32 by 16 threads each took 783 us, forward and
-// backward, 200 by 4), eight elements (VPT 16-byte pieces) a thread, so both norms and every
+// row (4 to 1024: 962626 rows of 32 took 783 us, forward and backward, by 16
+// threads each, 200 by 4 and 173 without branches), eight elements (VPT 16-byte pieces) a thread, so both norms and every
 // product cost no second pass. Workgroups walk over rows with the weights in registers. What
 // bounds it is HBM: (b, gate, x in; y, h out) forward, at the copy rate (16384
 // rows of 4096: 125 us, 5.3 TB/s), and the same with their gradients backward,
 // where the sums over rows and up to five tensors' values leave room for one or
-// two waves a SIMD (262144 rows of 128: 79 us, 4.2 TB/s; 16384 of 4096: 345 us,
-// 3.1 TB/s). Tried and dropped: loading the next row ahead (forward 127 -> 147
+// three waves a SIMD (262144 rows of 128: 72 us, 4.7 TB/s; 16384 of 4096: 274
+// us, 3.9 TB/s). Tried and dropped: loading the next row ahead (forward 127 -> 147
 // us: fewer waves), reading past odd rows' ends and masking (76 -> 102 us).
 //
 // Backward, with e = dh w_pre and yn = y ry:

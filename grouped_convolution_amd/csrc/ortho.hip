@@ -156,7 +156,11 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void ortho_gemm(Ortho a)
     using SP = std::conditional_t<OP == UPDATE, AcrossRows<BP, NW, FP>, AlongRows<BP, NW, FP>>;
     constexpr int kBuf = SQ::kBytes + SP::kBytes;
     constexpr int kLoads = SQ::kLoads + SP::kLoads;
-    constexpr int kRing = std::min(3, 160 * 1024 / kBuf);  // stages that the LDS of a CU holds
+    // Stages that the LDS of a CU holds, 3 at most, and 4 of the smallest tile,
+    // whose stages are too short for a load to arrive in two of them (300 x 5000
+    // 157 us for 176, 1024 x 2304 167 for 180; 8 groups of 512 x 512, which put
+    // several workgroups on a CU, 123 for 118; 6 stages 171, 172, 151).
+    constexpr int kRing = std::min(BQ == 64 ? 4 : 3, 160 * 1024 / kBuf);
     __shared__ __align__(1024) char lds[kRing * kBuf];
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;

@@ -1,5 +1,5 @@
-// ortho_small.hip -- the orthogonalised update of matrices of at most 128 rows
-// (gfx950): few products, so what counts is the number of launches and the
+// ortho_small.hip -- the orthogonalised update of matrices of at most 96 rows,
+// or 128 rows of at most 256 columns (gfx950): few products, so what counts is the number of launches and the
 // waits between them.
 //
 // A workgroup of eight waves keeps a block of X's columns in LDS with the
@@ -19,8 +19,8 @@
 //
 // A and B are split into two fp16 parts each (22 bits): with so few products
 // the second part is nearly free, and small matrices average less rounding
-// away (20 x 30: 2.3e-3 off where one part gives 2.7e-3; 128 x 1200: 1.8e-3
-// for 2.4e-3, the bf16 output's own rounding being 1.7e-3).
+// away (20 x 30: 2.1e-3 off where one part gives 2.7e-3; 100 x 100: 1.9e-3
+// for 2.2e-3, the bf16 output's own rounding being 1.7e-3).
 #include <algorithm>
 
 #include "ortho_internal.h"
@@ -39,8 +39,8 @@ enum Mode { WHOLE = 0, START = 1, ROUND = 2 };
 // kMoreBlocks: blocks of kShortCols columns up to which more blocks are
 // quicker than longer ones, for all that each adds up all blocks' sums.
 constexpr int kWholeCols[4] = {704, 512, 448, 256};
-constexpr int kBlockCols[4] = {1024, 512, 320, 256};
-constexpr int kMoreBlocks[4] = {64, 24, 12, 10};
+constexpr int kBlockCols[3] = {1024, 512, 320};
+constexpr int kMoreBlocks[3] = {64, 24, 12};
 constexpr int kShortCols = 128;
 
 struct Small {
@@ -66,7 +66,7 @@ template <int FT, typename T, int MODE>
 __global__ __launch_bounds__(kThreads, 1) void ortho_small_kernel(Small a)
 {
     constexpr int MP = 32 * FT;               // rows, padded with zeros
-    constexpr int XP = (MODE == WHOLE ? kWholeCols : kBlockCols)[FT - 1] * 2;
+    constexpr int XP = (MODE == WHOLE ? kWholeCols[FT - 1] : kBlockCols[FT - 1 < 2 ? FT - 1 : 2]) * 2;
     constexpr int MPITCH = MP * 2 + 16;       // of A's and B's parts
     constexpr int PART = MP * MPITCH;
     __shared__ __align__(16) char X[MP * XP];
@@ -436,14 +436,16 @@ template <int FT, typename T>
 void run(const Small& s, hipStream_t st)
 {
     const unsigned grid = (unsigned)(s.o.groups * s.blocks);
-    if (s.blocks == 1) {
+    if (FT == 4 || s.blocks == 1) {
         ortho_small_kernel<FT, T, WHOLE><<<grid, kThreads, 0, st>>>(s);
         return;
     }
-    ortho_launch_norm(s.o, st);
-    ortho_small_kernel<FT, T, START><<<grid, kThreads, 0, st>>>(s);
-    Small r = s;
-    for (r.step = 0; r.step < s.o.steps; ++r.step) ortho_small_kernel<FT, T, ROUND><<<grid, kThreads, 0, st>>>(r);
+    if constexpr (FT < 4) {
+        ortho_launch_norm(s.o, st);
+        ortho_small_kernel<FT, T, START><<<grid, kThreads, 0, st>>>(s);
+        Small r = s;
+        for (r.step = 0; r.step < s.o.steps; ++r.step) ortho_small_kernel<FT, T, ROUND><<<grid, kThreads, 0, st>>>(r);
+    }
 }
 
 template <typename T>
@@ -464,11 +466,11 @@ int ortho_small_blocks(int64_t m, int64_t np)
     if (m > 128) return 0;
     const int ft = (int)(m + 31) / 32 - 1;
     if (np <= kWholeCols[ft]) return 1;
-    // Above 96 rows the general kernels are quicker up to long matrices
-    // (128 x 1200: 87 us for 111; 128 x 10000: 256 for 226).
-    if (m > 96 && np < 6144) return 0;
+    // Above 96 rows the general kernels are quicker (2 groups of 128 x 1200: 84
+    // us, 112 by several workgroups here; 128 x 10000: 206 and 226).
+    if (m > 96) return 0;
     // Every block adds up all blocks' Gram matrices: past 64 of them (of up to
-    // 64 KB) the general kernels take over.
+    // 36 KB) the general kernels take over.
     const int64_t least = (np + kBlockCols[ft] - 1) / kBlockCols[ft];
     if (least > 64) return 0;
     return (int)std::max<int64_t>(least, std::min<int64_t>(np / kShortCols, kMoreBlocks[ft]));
