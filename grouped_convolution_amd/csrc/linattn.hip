@@ -167,7 +167,7 @@ struct Reader {
     __device__ __forceinline__ u4 load_edge(int row, int col) const
     {
         if (row >= n) return u4{0, 0, 0, 0};
-        return load16<T>(low + (reverse ? n - 1 - row : row) * tok, col, dim, false);
+        return load16<T>(low + (reverse ? n - 1 - row : row) * tok, col, dim);
     }
     static __device__ __forceinline__ u4 mask(u4 v, int row, int col, int n, int dim)
     {

@@ -106,26 +106,11 @@ struct Vals {
 
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
-// act(z) and its derivative.
+// act(z).
 __device__ __forceinline__ float act_of(float z, int act)
 {
     return act == GCONV_ACT_NONE ? z : act == GCONV_ACT_SIGMOID ? sigmoid(z) : z * sigmoid(z);
 }
-__device__ __forceinline__ float act_grad(float z, int act, float* a)
-{
-    if (act == GCONV_ACT_NONE) {
-        *a = z;
-        return 1.f;
-    }
-    const float s = sigmoid(z);
-    if (act == GCONV_ACT_SIGMOID) {
-        *a = s;
-        return s * (1.f - s);
-    }
-    *a = z * s;
-    return s + z * s * (1.f - s);
-}
-
 // Sum over the TPR threads of a row, the same in all of them. `red`: one float
 // a wave; every call of a kernel alternates between two of them.
 template <int TPR>

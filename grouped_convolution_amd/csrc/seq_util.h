@@ -103,17 +103,11 @@ __device__ __forceinline__ u4 frag_split(const T* tile, int pitch, int row0, int
     return u4{lo[0], lo[1], hi[0], hi[1]};
 }
 
-// 16 bytes of a row that holds `dim` elements, from element `col` (a multiple
-// of the 16 bytes); elements past the row read 0. `vec`: rows start on 16
-// bytes and hold whole 16-byte pieces.
+// 16 bytes of a row that holds `dim` elements, from element `col`, read one by
+// one; elements past the row read 0.
 template <typename T>
-__device__ __forceinline__ u4 load16(const T* row, int col, int dim, bool vec)
+__device__ __forceinline__ u4 load16(const T* row, int col, int dim)
 {
-    u4 v = {0, 0, 0, 0};
-    if (vec) {
-        if (col < dim) v = *(const u4*)(row + col);
-        return v;
-    }
     constexpr int E = 16 / sizeof(T);
     T e[E];
 #pragma unroll

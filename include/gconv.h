@@ -397,8 +397,9 @@ int gconv_normgate_bwd(const gconv_normgate_desc* d, const void* dy, const void*
  * (of the transposed matrix where U has more rows than columns), after which
  * its singular values lie around 1. u [filters][inner] dense, of either type;
  * out [filters][inner] in bfloat16, 8-byte aligned. The iterates are rounded
- * to fp16 between products, whose sums are float32: the result is within
- * 2e-3 of the exact one in the norm, and the output's rounding. A group that
+ * to fp16 between products, whose sums are float32: for gradients of any rank
+ * the result is within 3e-3 of the exact one in the norm, and the output's
+ * rounding. A group that
  * holds an infinity or a NaN gives NaN, and the other groups their own
  * results. A group's matrix, its longer side padded to 64, holds up to 2^29
  * elements, and neither side is above 2^24.
