@@ -665,6 +665,9 @@ int gconv_normgate_bwd(const gconv_normgate_desc* d, const void* dy, const void*
     if (!w_post || !dw_post || (some && (!dy || !b || !db))) return fail(GCONV_ERR_NULL, "dy, b, w_post, db and dw_post must be non-NULL");
     if ((d->gate != GCONV_GATE_NONE) != (gate != nullptr) && some) return fail(GCONV_ERR_NULL, "gate must be given unless there is none");
     if ((gate != nullptr) != (dgate != nullptr) && some) return fail(GCONV_ERR_NULL, "gate and dgate go together");
+    // (a sequence without tokens has a gate whose gradient, 0, is written)
+    if (d->gate == GCONV_GATE_SEQUENCE && d->sequences > 0 && !dgate)
+        return fail(GCONV_ERR_NULL, "dgate must be non-NULL for a gate for each sequence");
     if ((scale != nullptr) != (dscale != nullptr)) return fail(GCONV_ERR_NULL, "scale and dscale go together");
     if ((w_pre != nullptr) != (dw_pre != nullptr) || ((w_pre != nullptr) != (dh != nullptr) && some))
         return fail(GCONV_ERR_NULL, "w_pre, dh and dw_pre go together");

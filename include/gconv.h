@@ -378,9 +378,10 @@ int gconv_normgate_fwd(const gconv_normgate_desc* d, const void* x, const void* 
 /*
  * Gradients for dy of y and dh of h (given exactly when w_pre is). dx, db and
  * a full gate's dgate are dense; dgate of a gate for each sequence is
- * [sequences, dim], summed over its tokens. The weights' gradients are summed
- * over all rows in float32 and rounded once. dx may be NULL; the others are
- * given exactly when their inputs are.
+ * [sequences, dim], summed over its tokens (0 without tokens, so it is given
+ * then too). The weights' gradients are summed over all rows in float32 and
+ * rounded once. dx may be NULL; the others are given exactly when their inputs
+ * are.
  */
 int gconv_normgate_bwd(const gconv_normgate_desc* d, const void* dy, const void* dh, const void* x, const void* b, const void* gate,
                        const void* w_post, const void* scale, const void* w_pre, void* dx, void* db, void* dgate, void* dw_post,

@@ -84,3 +84,10 @@ def test_python_checks():
         G.gconv_normgate_fwd(None, b, w_post=torch.ones(8))
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         G.gconv_normgate_fwd(None, b.double(), w_post=torch.ones(8))
+
+
+def test_gradient_of_a_sequence_gate_without_tokens():
+    """The sums over no tokens are still written: [sequences, dim] zeros, so there has to be a place for them."""
+    d = desc(gate=B.GATE_SEQUENCE, tokens=0)
+    assert bwd(d, dgate=None) == 1
+    assert bwd(d, gate=None, dgate=None) == 1
