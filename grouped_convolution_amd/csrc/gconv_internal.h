@@ -14,6 +14,9 @@ namespace gconv {
 int fail(int status, const char* fmt, ...);
 int finish();
 
+// Workgroups of one launch: HIP takes fewer than 2^32 threads.
+constexpr int64_t max_blocks(int64_t threads) { return (((int64_t)1 << 32) - 1) / threads; }
+
 // A validated descriptor with the derived quantities every kernel needs.
 // 32-bit fields: the dispatcher refuses extents that do not fit.
 struct Shape {

@@ -378,10 +378,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void segment_sums
 // state. One thread four rows of a column; a segment is one step of the scan.
 // Bound by memory: the 33 MB of states of 512 segments take 13 us, 5.1 TB/s.
 // (More loads in flight than U, clamped at the end, took 30 us.)
+constexpr int scan_parts(int DK, int DV) { return DK * DV / 4 / kThreads; }  // workgroups of a state
+
 template <int DK, int DV>
 __global__ __launch_bounds__(kThreads) void scan_states(Pass a)
 {
-    constexpr int kParts = DK * DV / 4 / kThreads;
+    constexpr int kParts = scan_parts(DK, DV);
     const int part = blockIdx.x % kParts, nh = blockIdx.x / kParts;
     const int h = nh % a.heads, n = nh / a.heads;
     // 16 columns x 16 quads of rows a workgroup pass: 64-byte pieces on both sides
@@ -715,13 +717,16 @@ __global__ __launch_bounds__(kThreads) void sum_heads(const float* part, T* out,
     *(Out*)(out + i) = o;
 }
 
+int sum_heads_width(int64_t d) { return d % 4 == 0 ? 4 : 1; }
+
+int64_t sum_heads_blocks(int64_t count, int64_t d) { return (count / sum_heads_width(d) + kThreads - 1) / kThreads; }
+
 template <typename T>
 void launch_sum_heads(const float* part, void* out, int64_t count, int rep, int d, hipStream_t st)
 {
-    const int w = d % 4 == 0 ? 4 : 1;
-    const unsigned grid = (unsigned)((count / w + kThreads - 1) / kThreads);
+    const unsigned grid = (unsigned)sum_heads_blocks(count, d);
     if (grid == 0) return;
-    if (w == 4) sum_heads<T, 4><<<grid, kThreads, 0, st>>>(part, (T*)out, count, rep, d);
+    if (sum_heads_width(d) == 4) sum_heads<T, 4><<<grid, kThreads, 0, st>>>(part, (T*)out, count, rep, d);
     else sum_heads<T, 1><<<grid, kThreads, 0, st>>>(part, (T*)out, count, rep, d);
 }
 
@@ -858,7 +863,7 @@ int pad64(int64_t d) { return d <= 64 ? 64 : 128; }
 // sequences ends in a part of one, so as many fewer are planned, down to half
 // (7264 tokens in 12 sequences: 110 us, 120 with segments for 512 workgroups
 // before the parts).
-int make_plan(const gconv_linattn_desc* d, Plan* p)
+int make_plan(const gconv_linattn_desc* d, int op, Plan* p)
 {
     p->rows = d->packed ? d->tokens : d->sequences * d->tokens;
     const int64_t per_head = std::max<int64_t>(1, 512 / d->heads);
@@ -867,10 +872,15 @@ int make_plan(const gconv_linattn_desc* d, Plan* p)
     p->seg = (int)std::max<int64_t>(kChunk, (seg + kChunk - 1) / kChunk * kChunk);
     p->slots_per_seq = (int)((d->tokens + p->seg - 1) / p->seg);
     const int64_t slots = d->packed ? d->tokens / p->seg + d->sequences : d->sequences * p->slots_per_seq;
-    if (slots * d->heads > kMaxTokens) return fail(GCONV_ERR_UNSUPPORTED, "too many sequences x heads");
-    p->slots = (int)slots;
     p->DK = pad64(d->dk);
     p->DV = pad64(d->dv);
+    if (slots * d->heads > max_blocks(kThreads) || d->sequences * d->heads * scan_parts(p->DK, p->DV) > max_blocks(kThreads))
+        return fail(GCONV_ERR_UNSUPPORTED, "too many sequences x heads");
+    if (op == GCONV_LINATTN_BWD && d->heads != d->kv_heads &&
+        (sum_heads_blocks(p->rows * d->kv_heads * d->dk, d->dk) > max_blocks(kThreads) ||
+         sum_heads_blocks(p->rows * d->kv_heads * d->dv, d->dv) > max_blocks(kThreads)))
+        return fail(GCONV_ERR_UNSUPPORTED, "too many tokens x kv_heads");
+    p->slots = (int)slots;
     p->state_elems = slots * d->heads * p->DK * p->DV;
     return GCONV_OK;
 }
@@ -902,7 +912,7 @@ void launch_states(const Pass& a, hipStream_t st)
         else segment_sums<T, DK, DV, false><<<grid, kThreads, 0, st>>>(a);
     }
     if (a.sequences > 0)
-        scan_states<DK, DV><<<a.sequences * a.heads * (DK * DV / 4 / kThreads), kThreads, 0, st>>>(a);
+        scan_states<DK, DV><<<(unsigned)(a.sequences * a.heads * scan_parts(DK, DV)), kThreads, 0, st>>>(a);
 }
 
 template <typename T>
@@ -1048,7 +1058,7 @@ int gconv_linattn_workspace_size(const gconv_linattn_desc* d, int op, size_t* by
     if (!bytes) return fail(GCONV_ERR_NULL, "bytes pointer is NULL");
     if (op != GCONV_LINATTN_FWD && op != GCONV_LINATTN_BWD) return fail(GCONV_ERR_ARG, "bad op %d", op);
     Plan p;
-    st = make_plan(d, &p);
+    st = make_plan(d, op, &p);
     if (st != GCONV_OK) return st;
     *bytes = workspace_bytes(d, p, op);
     return GCONV_OK;
@@ -1062,7 +1072,7 @@ int common(const gconv_linattn_desc* d, int op, const void* q, const void* k, co
 {
     int st = check_desc(d, false);
     if (st != GCONV_OK) return st;
-    st = make_plan(d, p);
+    st = make_plan(d, op, p);
     if (st != GCONV_OK) return st;
     const bool some = p->rows > 0 && d->sequences > 0;
     if (p->rows > 0 && d->sequences == 0) return fail(GCONV_ERR_SHAPE, "tokens without a sequence");
@@ -1178,6 +1188,8 @@ int gconv_linattn_step(const gconv_linattn_desc* d, const void* q, const void* k
         for (const Range& r : in)
             if (meets(w, r)) return fail(GCONV_ERR_ARG, "o or state overlaps an input");
     if (meets(out[0], out[1])) return fail(GCONV_ERR_ARG, "o overlaps state");
+    const int64_t bh = d->sequences * d->heads;
+    if (bh > max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many sequences x heads");
     hipStream_t hs = (hipStream_t)stream;
     (void)hipGetLastError();
     if (d->sequences == 0) return finish();
@@ -1197,7 +1209,6 @@ int gconv_linattn_step(const gconv_linattn_desc* d, const void* q, const void* k
     a.scale = (float)d->scale;
     a.vec = ((uintptr_t)state & 15) == 0 && d->dv % 4 == 0;
     // Few heads in all: 32 columns a workgroup, four times as many of them.
-    const int64_t bh = d->sequences * d->heads;
     const int cw = bh < 512 ? 32 : 128;
     const unsigned grid = (unsigned)(bh * ((d->dv + cw - 1) / cw));
     if (d->dtype == GCONV_BF16) {

@@ -490,6 +490,10 @@ int make_plan(const gconv_ortho_desc* d, Plan* p)
     const int64_t want = std::max<int64_t>(1, 2048 / d->groups);
     p->blocks = (int)std::min<int64_t>(want, (p->us + kNormThreads * 16 - 1) / (kNormThreads * 16));
     p->small = ortho_small_blocks(p->m, p->np);
+    // (no launch of the general kernels has more threads than one with a workgroup for each 64 x 64 of X)
+    if (p->small > 0 ? d->groups * p->small > max_blocks(kSmallThreads)
+                     : d->groups * (p->mp / 64) * (p->np / 64) > max_blocks(256))
+        return fail(GCONV_ERR_UNSUPPORTED, "too many groups");
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t o = at;

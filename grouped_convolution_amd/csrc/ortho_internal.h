@@ -85,6 +85,7 @@ struct OrthoArgs {
 void ortho_launch_norm(const OrthoArgs& a, hipStream_t st);
 
 // ---- at most 128 rows (ortho_small.hip) ------------------------------------------
+constexpr int kSmallThreads = 512;
 // Workgroups a group takes: 1 where its X fits one workgroup's LDS, 0 where
 // the general kernels are the better choice.
 int ortho_small_blocks(int64_t m, int64_t np);

@@ -28,7 +28,7 @@
 namespace gconv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = kSmallThreads;
 
 enum Mode { WHOLE = 0, START = 1, ROUND = 2 };
 

@@ -123,3 +123,25 @@ def test_python_checks():
         G.gconv_linattn_fwd(q.half(), q.half(), q.half(), torch.zeros(2))
     with pytest.raises(ValueError, match="torch.Tensor"):
         G.gconv_linattn_step(None, q, q, torch.zeros(2), q)
+
+
+def test_more_workgroups_than_a_launch_takes():
+    """A launch takes fewer than 2^32 threads, 256 a workgroup: what would need more is refused beforehand."""
+    size = B.gconv_linattn_workspace_size
+    # the scan over segments: 16 workgroups a state of 128 x 128, 4 of 64 x 64
+    for sequences, dim, ok in ((1 << 16, 128, False), ((1 << 16) - 1, 128, True), (1 << 17, 64, True), (1 << 18, 64, False),
+                               (1 << 24, 128, False)):
+        d = desc(sequences=sequences, tokens=1, heads=16, kv_heads=16, dk=dim, dv=dim)
+        if ok:
+            assert size(d, B.LINATTN_FWD) > 0 and size(d, B.LINATTN_BWD) > 0
+            continue
+        assert fwd(d) == 6 and bwd(d) == 6
+        with pytest.raises(B.GconvError) as e:
+            size(d, B.LINATTN_FWD)
+        assert e.value.status == 6
+    # the sum over shared heads: an element a thread in odd head sizes, four in others
+    odd = desc(sequences=1, tokens=1 << 23, heads=16, kv_heads=8, dk=127, dv=64)
+    assert size(odd, B.LINATTN_FWD) > 0 and bwd(odd) == 6
+    assert size(desc(sequences=1, tokens=1 << 23, heads=16, kv_heads=8, dk=128, dv=64), B.LINATTN_BWD) > 0
+    # the single-token step: a workgroup a head here
+    assert step(desc(tokens=0, sequences=1 << 20, heads=16, kv_heads=16, dk=1, dv=1), num=1 << 20) == 6

@@ -55,3 +55,12 @@ def test_python_checks():
         G.gconv_orthogonalize(torch.zeros(4, 4))
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         G.gconv_orthogonalize(torch.zeros(4, 4).half())
+
+
+def test_more_workgroups_than_a_launch_takes():
+    """A launch takes fewer than 2^32 threads: many groups of several workgroups each are refused beforehand."""
+    for bad, good in ((dict(filters=1 << 20, inner=1024, groups=1 << 20), dict(filters=1 << 19, inner=1024, groups=1 << 19)),
+                      (dict(filters=200 << 20, inner=200, groups=1 << 20), dict(filters=200 << 19, inner=200, groups=1 << 19))):
+        d = desc(**bad)
+        assert size(d)[0] == 6 and call(d) == 6
+        assert size(desc(**good))[0] == 0
