@@ -43,12 +43,17 @@ __device__ __forceinline__ h4 split4(f4 v, h4* rest)
 
 // 64 lanes' 16 bytes from global memory straight to 1024 bytes of LDS. In
 // assembly, as it writes no register: the compiler would otherwise wait for
-// every such load before any read of LDS, where the stages below wait once.
+// every such load before any read of LDS, where the stages below wait once. M0
+// is said to be written, and no one needs it kept, which is what the compiler
+// warns of.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_lds(u4 rsrc, uint32_t lds, uint32_t off)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(off), "s"(rsrc) : "memory");
+                 :: "s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Waits until at most N of this wave's loads are still under way.
 template <int N>
