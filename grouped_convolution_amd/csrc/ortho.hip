@@ -112,7 +112,7 @@ struct AcrossRows {
             const int q = (i * NW + wave) * 64 + lane, row = q / kPieces, p = q % kPieces;
             off[i] = (uint32_t)(((int64_t)row * pitch + col0 + ((p ^ (swz(row) << 1)) * 8)) * 2);
         }
-        step = (uint32_t)(kStepK * pitch * 2);
+        step = (uint32_t)kStepK * (uint32_t)pitch * 2;  // 2^31 at the longest side
         const int li = lane & 15, g = lane >> 4;
         const int row = 8 * g + (li >> 2);  // rows + 4 and + 32 have the same swizzle
 #pragma unroll
