@@ -268,15 +268,26 @@ def _raw_stream(device):
     return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
+def _given_workspace(nbytes, device, workspace):
+    """A caller's workspace and its size: `nbytes` or more, on `device`, one after another."""
+    if not isinstance(workspace, _torch().Tensor):
+        raise ValueError("workspace must be a torch.Tensor")
+    if workspace.device != device:
+        raise ValueError("workspace must be on %s, got %s" % (device, workspace.device))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    have = workspace.numel() * workspace.element_size()
+    if have < nbytes:
+        raise ValueError("workspace holds %d bytes, %d needed" % (have, nbytes))
+    return workspace, have
+
+
 def _workspace(desc, op, device, workspace):
     n = gconv_workspace_size(desc, op)
     if n == 0:
         return None, 0
     if workspace is not None:
-        if workspace.numel() * workspace.element_size() < n:
-            raise ValueError("workspace holds %d bytes, %d needed"
-                             % (workspace.numel() * workspace.element_size(), n))
-        return workspace, workspace.numel() * workspace.element_size()
+        return _given_workspace(n, device, workspace)
     torch = _torch()
     return torch.empty(n, dtype=torch.uint8, device=device), n
 
@@ -517,13 +528,10 @@ def _last_axis(t, name):
 
 
 def _scratch(nbytes, device, workspace):
-    if workspace is not None:
-        have = workspace.numel() * workspace.element_size()
-        if have < nbytes:
-            raise ValueError("workspace holds %d bytes, %d needed" % (have, nbytes))
-        return workspace, have
     if nbytes == 0:
         return None, 0
+    if workspace is not None:
+        return _given_workspace(nbytes, device, workspace)
     torch = _torch()
     return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
 
