@@ -23,9 +23,11 @@
 // Rounding them is what the matrix pipes ask for; fp16 has 11 bits where bf16
 // has 8 and its short range is no matter: the entries of X, A and B are at
 // most 1.3, 1.5 and 2.9 (the singular values stay below 1.21), and 2^12 puts
-// everything above 2^-26 into fp16's normal range. The result is within
-// 1.5e-3 of the 64-bit one (in the 2-norm, before the bf16 output's own
-// 1.7e-3); bf16 products would be off by 9e-3. What fp16 leaves of X is kept
+// everything above 2^-26 into fp16's normal range. After five rounds a random
+// gradient of full rank is 1.5e-3 off the 64-bit result (in the 2-norm, before
+// the bf16 output's own 1.7e-3) and one of low rank 2.8e-3, where bf16 operands
+// would leave 1e-2 and 2e-2; a constant gradient, whose entries are all rounded
+// the same way, is up to 1.5e-2 off. What fp16 leaves of X is kept
 // too and joins the term a X: directions that hold next to nothing of the
 // gradient grow by a in every round, 485 times in five, and rounding noise
 // there would grow with them (a rank-one gradient came back 15% off).

@@ -398,9 +398,16 @@ int gconv_normgate_bwd(const gconv_normgate_desc* d, const void* dy, const void*
  * (of the transposed matrix where U has more rows than columns), after which
  * its singular values lie around 1. u [filters][inner] dense, of either type;
  * out [filters][inner] in bfloat16, 8-byte aligned. The iterates are rounded
- * to fp16 between products, whose sums are float32: for gradients of any rank
- * the result is within 3e-3 of the exact one in the norm, and the output's
- * rounding. A group that
+ * to fp16 between products, whose sums are float32. Relative in the norm, and
+ * besides the output's own rounding, the result is within 5e-3 of the exact one
+ * up to seven rounds and 7e-3 at eight, for gradients of any rank with sides of
+ * 64 or more whose roundings are independent (some 1.5e-3 for a random one of
+ * full rank, 3e-3 for one of low rank). At worst, for a constant gradient, all
+ * of whose entries are rounded the same way, or for a side of 2 or 3, it is
+ * 1.5e-2 after five rounds and 6e-2 after eight. Each further round enlarges the
+ * noise in the directions that a gradient of low rank does not have up to 3.4445
+ * times: rank one is 5e-2 off at ten rounds and by half at twelve, as it is when
+ * all is kept in float32. Full rank is within 3e-2 at twenty. A group that
  * holds an infinity or a NaN gives NaN, and the other groups their own
  * results. A group's matrix, its longer side padded to 64, holds up to 2^29
  * elements, and neither side is above 2^24.
