@@ -313,3 +313,62 @@ def test_graph_capture():
         torch.cuda.synchronize()
         want = call()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+# Segments of five chunks of 64 tokens (64 heads x T over 512 workgroups) whose last chunk is short, so
+# that a chunk's state, its flags and its loads meet those of several others.
+LONG = [([2500], False), ([1250, 1250], False), ([900, 1, 0, 700, 640, 259], True)]
+
+
+@pytest.mark.parametrize("type_", ["fp32", "bf16"])
+@pytest.mark.parametrize("Hk,dk,dv", [(4, 128, 128), (1, 24, 40), (2, 33, 65)])
+@pytest.mark.parametrize("lens,packed", LONG)
+def test_segments_of_many_chunks(type_, Hk, dk, dv, lens, packed):
+    """Four heads sixteen times over (the reference takes them once): the copies have the same bits."""
+    c = make(51, type_, lens, 4, Hk, dk, dv, packed)
+    q, k, v, g, kw, do, ds = on_gpu(c, "dense")
+    many = lambda t, axis: torch.cat([t] * 16, axis)  # noqa: E731
+    kw["initial_state"] = many(kw["initial_state"], 1)
+    q, k, v, do = (many(t, -2) for t in (q, k, v, do))
+    g, ds, scale = many(g, 0), many(ds, 1), dk ** -0.5
+    print("linattn many chunks", tuple(q.shape), tuple(v.shape), q.dtype, flush=True)
+    o, fin = G.gconv_linattn_fwd(q, k, v, g, scale=scale, **kw)
+    grads = G.gconv_linattn_bwd(do, q, k, v, g, scale=scale, d_final_state=ds, **kw)
+    got = dict(zip(("o", "final", "dq", "dk", "dv", "dstate"), (o, fin) + grads))
+    for name, t in got.items():
+        axis = 1 if name in ("final", "dstate") else t.dim() - 2
+        parts = t.split(t.shape[axis] // 16, axis)
+        assert all(torch.equal(parts[0], p) for p in parts), name
+        got[name] = parts[0]
+    compare("many chunks", c, got, scale, True)
+
+
+@pytest.mark.parametrize("type_", ["fp32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("spot", [70, 140, 300, 319, 330])
+def test_not_finite_in_a_segment_of_many_chunks(type_, value, spot):
+    """A value of token `spot` that is not finite: earlier tokens keep their outputs, whichever chunk of
+    a segment it lies in and whatever comes after; every later one sees it; gradients likewise."""
+    c = make(61, type_, [2500], 64, 16, 16, 16, False)
+    q, k, v, g, kw, do, ds = on_gpu(c, "dense")
+    o, fin = G.gconv_linattn_fwd(q, k, v, g, **kw)
+    mag = reference(c, 16 ** -0.5, absolute=True)["o"]
+    bad = v.clone()
+    bad[0, spot, 3, 5] = value
+    ob, fb = G.gconv_linattn_fwd(q, k, bad, g, **kw)
+    check_mag("v", ob[0, :spot], o[0, :spot].cpu().to(F64), mag[:spot], 2 * bounds(c, "o"))
+    mine = torch.zeros(64, 16, dtype=torch.bool, device="cuda")
+    mine[12:16, 5] = True  # the four heads that share it, the column that it is in
+    assert (~torch.isfinite(ob[0, spot:][:, mine])).all() and not torch.isfinite(fb[0, 12:16, :, 5]).any()
+    check_mag("v, others", ob[0, spot:][:, ~mine], o[0, spot:][:, ~mine].cpu().to(F64), mag[spot:][:, ~mine.cpu()], 2 * bounds(c, "o"))
+    dob = do.clone()
+    dob[0, spot, 12, 5] = value
+    a = G.gconv_linattn_bwd(do, q, k, v, g, d_final_state=ds, **kw)
+    b = G.gconv_linattn_bwd(dob, q, k, v, g, d_final_state=ds, **kw)
+    keep = torch.ones(2500, dtype=torch.bool, device="cuda")
+    keep[spot] = False
+    assert torch.equal(a[0][0, keep], b[0][0, keep])
+    gmag = reference(c, 16 ** -0.5, True, absolute=True)
+    for n, x, y in zip(("dk", "dv"), a[1:3], b[1:3]):
+        check_mag(n, y[0, spot + 1:], x[0, spot + 1:].cpu().to(F64), gmag[n][spot + 1:], 2 * bounds(c, n))
+        assert not torch.isfinite(y[0, :spot + 1, 3]).all(-1).any(), n
