@@ -592,8 +592,8 @@ def gconv_linattn_fwd(q, k, v, log_decay, *, scale=None, cu_seqlens=None, initia
     """Linear attention with a decay for each head: S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,
     o_t = scale q_t S_t. q [N, T, H, dk], k [N, T, Hk, dk], v [N, T, Hk, dv] (H a multiple of Hk;
     float32 or bfloat16, any strides with a contiguous last axis), or [T, heads, d] with
-    cu_seqlens (int32 [N + 1]) where sequences are packed. log_decay [H] float32; scale
-    defaults to dk^-0.5; initial_state [N, H, dk, dv] float32 or None.
+    cu_seqlens (int32 [N + 1]) where sequences are packed (tokens in none of them give 0).
+    log_decay [H] float32; scale defaults to dk^-0.5; initial_state [N, H, dk, dv] float32 or None.
     Returns o (q's type) and the final state [N, H, dk, dv] float32."""
     def make():
         d, states = _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state)

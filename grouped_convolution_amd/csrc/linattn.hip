@@ -118,6 +118,27 @@ __device__ __forceinline__ Place slot_place(const Pass& a, int slot)
     return p;
 }
 
+// Zeros a head's output in the rows of packed tensors that no sequence holds,
+// those before the first and after the last. The segment slots of the first
+// and the last sequence reach as far as them: a slot's workgroup takes the rows
+// where its segment would lie.
+template <typename T>
+__device__ __forceinline__ void clear_rows(const Pass& a, const Place& p, int h, int slot)
+{
+    auto clear = [&](int64_t from, int64_t to) {
+        for (int64_t i = threadIdx.x; i < (to - from) * a.dv; i += kThreads) {
+            const int64_t at = (from + i / a.dv) * a.out_tok + (int64_t)h * a.out_head + i % a.dv;
+            if (a.out_f32) ((float*)a.out)[at] = 0.f;
+            else ((T*)a.out)[at] = (T)0.f;
+        }
+    };
+    if (p.n == 0 && p.s <= 0) clear((int64_t)slot * a.seg, min((int64_t)(slot + 1) * a.seg, cu_at(a, 0)));
+    if (p.n == a.sequences - 1 && p.s >= 0) {
+        const int64_t at = p.start + (int64_t)p.s * a.seg;
+        clear(max(at, p.start + p.len), min(at + a.seg, a.tokens));
+    }
+}
+
 // Token `t` (in the order of the pass) of an operand's head.
 template <typename T>
 __device__ __forceinline__ const T* row_of(const Operand& o, const Pass& a, const Place& p, int h, int64_t t)
@@ -472,6 +493,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void chunk_output
     const int h = b % a.heads, slot = b / a.heads;
     const Place p = slot_place(a, slot);
     const int t0 = p.s * a.seg;
+    if (a.cu) clear_rows<T>(a, p, h, slot);
     if (p.s < 0 || t0 >= p.len) return;
     const int n = min(a.seg, p.len - t0);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;

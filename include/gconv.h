@@ -281,7 +281,9 @@ typedef enum gconv_dtype {
  * Sequences: with packed == 0, `sequences` of `tokens` each. With packed != 0
  * the tokens of all sequences follow one another, `tokens` in all, and
  * cu_seqlens (int32, device memory, sequences + 1 values from 0 to `tokens`,
- * not decreasing) says where each begins; a sequence may be empty.
+ * not decreasing) says where each begins; a sequence may be empty. Tokens
+ * before the first and after the last sequence (padding) are not read; their
+ * outputs and gradients are 0.
  * Strides are in elements: [0] between sequences (not read when packed), [1]
  * between tokens, [2] between heads; the last axis is contiguous. Outputs
  * are dense, [sequences, tokens, heads, d] or [tokens, heads, d].

@@ -372,3 +372,38 @@ def test_not_finite_in_a_segment_of_many_chunks(type_, value, spot):
     for n, x, y in zip(("dk", "dv"), a[1:3], b[1:3]):
         check_mag(n, y[0, spot + 1:], x[0, spot + 1:].cpu().to(F64), gmag[n][spot + 1:], 2 * bounds(c, n))
         assert not torch.isfinite(y[0, :spot + 1, 3]).all(-1).any(), n
+
+
+@pytest.mark.parametrize("type_", ["fp32", "bf16"])
+@pytest.mark.parametrize("H,Hk", [(4, 2), (64, 64)])
+@pytest.mark.parametrize("cu,T", [([0, 70, 70, 200], 300), ([5, 70, 140], 140), ([130, 130, 400, 1000], 1500), ([40, 40], 77),
+                                  ([0, 0], 200), ([64, 128], 192), ([700, 701, 701], 1000)])
+def test_tokens_of_no_sequence(type_, H, Hk, cu, T):
+    """Rows before the first and after the last sequence (a buffer's padding): 0, and the others as without them."""
+    lens = [b - a for a, b in zip(cu, cu[1:])]
+    c = make(71, type_, lens, H, Hk, 16, 24, True)
+    q, k, v, g, kw, do, ds = on_gpu(c, "dense")
+    scale = 0.25
+    print("linattn padding", type_, H, cu, T, flush=True)
+
+    def padded(t):
+        out = torch.full((T,) + t.shape[1:], float("nan"), dtype=t.dtype, device="cuda")
+        out[cu[0]:cu[-1]] = t
+        return out
+
+    want = G.gconv_linattn_fwd(q, k, v, g, scale=scale, **kw) + \
+        G.gconv_linattn_bwd(do, q, k, v, g, scale=scale, d_final_state=ds, **kw)
+    kw["cu_seqlens"] = torch.tensor(cu, dtype=torch.int32).cuda()
+    q, k, v, do = (padded(t) for t in (q, k, v, do))
+    dirty = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(8)]
+    del dirty  # what the allocator hands out next is not 0 by chance
+    got = G.gconv_linattn_fwd(q, k, v, g, scale=scale, **kw) + \
+        G.gconv_linattn_bwd(do, q, k, v, g, scale=scale, d_final_state=ds, **kw)
+    names = ("o", "final", "dq", "dk", "dv", "dstate")
+    mag = reference(c, scale, True, absolute=True)
+    for name, a, b in zip(names, got, want):
+        if name not in ("final", "dstate"):
+            assert not a[:cu[0]].any() and not a[cu[-1]:].any(), name
+            a = a[cu[0]:cu[-1]]
+        # the same terms, in segments that may begin elsewhere
+        check_mag(name, a, b.cpu().to(F64), mag[name], 2 * bounds(c, name), 1e-37)
