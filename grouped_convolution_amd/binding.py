@@ -556,6 +556,8 @@ def _linattn_desc(q, k, v, log_decay, scale, cu_seqlens, initial_state, do=None)
         raise ValueError("k has heads and size %s, expected %s" % (tuple(k.shape[-2:]), (Hk, dk)))
     _dense(log_decay, "log_decay", (H,), torch.float32, q.device)
     if packed:
+        if not isinstance(cu_seqlens, torch.Tensor):
+            raise ValueError("cu_seqlens must be a torch.Tensor")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [sequences + 1]")
         _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, q.device)

@@ -145,3 +145,23 @@ def test_more_workgroups_than_a_launch_takes():
     assert size(desc(sequences=1, tokens=1 << 23, heads=16, kv_heads=8, dk=128, dv=64), B.LINATTN_BWD) > 0
     # the single-token step: a workgroup a head here
     assert step(desc(tokens=0, sequences=1 << 20, heads=16, kv_heads=16, dk=1, dv=1), num=1 << 20) == 6
+
+
+def test_cu_seqlens_has_to_be_a_tensor():
+    """(Shapes and types come before the device, so host tensors that say they are on the GPU suffice.)"""
+    torch = pytest.importorskip("torch")
+
+    class OnGpu(torch.Tensor):
+        is_cuda = True
+
+    def t(*shape):
+        return torch.zeros(*shape).as_subclass(OnGpu)
+
+    q = t(4, 2, 16)
+    for bad in ([0, 4], (0, 4), 4):
+        with pytest.raises(ValueError, match="cu_seqlens must be a torch.Tensor"):
+            B.gconv_linattn_fwd(q, q, q, t(2), cu_seqlens=bad)
+        with pytest.raises(ValueError, match="cu_seqlens must be a torch.Tensor"):
+            B.gconv_linattn_bwd(q, q, q, q, t(2), cu_seqlens=bad)
+    with pytest.raises(ValueError, match=r"cu_seqlens must be \[sequences \+ 1\]"):
+        B.gconv_linattn_fwd(q, q, q, t(2), cu_seqlens=torch.zeros(2, 2, dtype=torch.int32))
