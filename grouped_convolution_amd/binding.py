@@ -263,9 +263,18 @@ def _addr(t):
     return t.data_ptr() if t is not None else None
 
 
-def _raw_stream(device):
-    """_stream as a plain number: torch's own short way to it, where a call's cost counts."""
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+def _launch(name, device, *args):
+    """Calls a C entry point on `device`'s current stream, with `device` current while it launches:
+    a stream that is another device's default one would otherwise stand for the current one's.
+    (torch's own short ways to both, as a call's cost counts.)"""
+    torch = _torch()
+    entry, index = getattr(load(), name), device.index
+    if torch._C._cuda_getDevice() == index:
+        status = entry(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = entry(*args, torch._C._cuda_getCurrentRawStream(index))
+    _check(status, name)
 
 
 def _given_workspace(nbytes, device, workspace):
@@ -605,8 +614,8 @@ def gconv_linattn_fwd(q, k, v, log_decay, *, scale=None, cu_seqlens=None, initia
     o = q.new_empty(shape)
     final = log_decay.new_empty(states)
     ws, nws = _scratch(need, q.device, workspace)
-    _check(load().gconv_linattn_fwd(d, _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens), _addr(initial_state),
-                                    _addr(o), _addr(final), _addr(ws), nws, _raw_stream(q.device)), "gconv_linattn_fwd")
+    _launch("gconv_linattn_fwd", q.device, d, _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens),
+            _addr(initial_state), _addr(o), _addr(final), _addr(ws), nws)
     return o, final
 
 
@@ -625,9 +634,8 @@ def gconv_linattn_bwd(do, q, k, v, log_decay, *, scale=None, cu_seqlens=None, in
     dq, dk, dv = (t.new_empty(t.shape) for t in (q, k, v))
     ds = log_decay.new_empty(states) if initial_state is not None else None
     ws, nws = _scratch(need, q.device, workspace)
-    _check(load().gconv_linattn_bwd(d, _addr(do), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens),
-                                    _addr(initial_state), _addr(d_final_state), _addr(dq), _addr(dk), _addr(dv), _addr(ds),
-                                    _addr(ws), nws, _raw_stream(q.device)), "gconv_linattn_bwd")
+    _launch("gconv_linattn_bwd", q.device, d, _addr(do), _addr(q), _addr(k), _addr(v), _addr(log_decay), _addr(cu_seqlens),
+            _addr(initial_state), _addr(d_final_state), _addr(dq), _addr(dk), _addr(dv), _addr(ds), _addr(ws), nws)
     return dq, dk, dv, ds
 
 
@@ -656,7 +664,7 @@ def _linattn_step_plan(q, k, v, log_decay, state, scale, slots, out):
     sq, sk, sv = q.stride(), k.stride(), v.stride()
     d = gconv_linattn_desc(_dtype_code(q), 0, B, 0, H, Hk, dk, dv, i3(sq[0], 0, sq[1]), i3(sk[0], 0, sk[1]),
                            i3(sv[0], 0, sv[1]), i3(), float(dk ** -0.5 if scale is None else scale))
-    return ctypes.byref(d), (B, H, dv), state.shape[0], load().gconv_linattn_step
+    return ctypes.byref(d), (B, H, dv), state.shape[0]
 
 
 def gconv_linattn_step(q, k, v, log_decay, state, *, scale=None, slots=None, out=None):
@@ -664,12 +672,12 @@ def gconv_linattn_step(q, k, v, log_decay, state, *, scale=None, slots=None, out
     v [B, Hk, dv] (float32 or bfloat16, any strides with a contiguous last axis), state
     [slots, H, dk, dv] float32, slots int32 [B] (different ones; one out of range gives o = 0
     and touches no state) or None for slot b. Returns o [B, H, dv]."""
-    d, shape, num, call = _plan("linattn_step", (q, k, v, log_decay, state, slots, out), (scale,),
-                                lambda: _linattn_step_plan(q, k, v, log_decay, state, scale, slots, out))
+    d, shape, num = _plan("linattn_step", (q, k, v, log_decay, state, slots, out), (scale,),
+                          lambda: _linattn_step_plan(q, k, v, log_decay, state, scale, slots, out))
     if out is None:
         out = q.new_empty(shape)
-    _check(call(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), _addr(slots), num,
-                out.data_ptr(), _raw_stream(q.device)), "gconv_linattn_step")
+    _launch("gconv_linattn_step", q.device, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+            state.data_ptr(), _addr(slots), num, out.data_ptr())
     return out
 
 
@@ -718,8 +726,8 @@ def gconv_normgate_fwd(x, b, *, w_post, gate=None, act="silu", scale=None, w_pre
               lambda: ctypes.byref(_normgate_desc(x, b, gate, act, w_post, scale, w_pre, eps)))
     y = b.new_empty(b.shape)
     h = b.new_empty(b.shape) if w_pre is not None else None
-    _check(load().gconv_normgate_fwd(d, _addr(x), b.data_ptr(), _addr(gate), w_post.data_ptr(), _addr(scale), _addr(w_pre),
-                                     y.data_ptr(), _addr(h), _raw_stream(b.device)), "gconv_normgate_fwd")
+    _launch("gconv_normgate_fwd", b.device, d, _addr(x), b.data_ptr(), _addr(gate), w_post.data_ptr(), _addr(scale),
+            _addr(w_pre), y.data_ptr(), _addr(h))
     return y, h
 
 
@@ -738,9 +746,8 @@ def gconv_normgate_bwd(dy, dh, x, b, *, w_post, gate=None, act="silu", scale=Non
     d, need = _plan("normgate_bwd", (dy, dh, x, b, gate, w_post, scale, w_pre), (act, eps), make)
     out = [t.new_empty(t.shape) if t is not None else None for t in (x, b, gate, w_post, scale, w_pre)]
     ws, nws = _scratch(need, b.device, workspace)
-    _check(load().gconv_normgate_bwd(d, _addr(dy), _addr(dh), _addr(x), _addr(b), _addr(gate), _addr(w_post), _addr(scale),
-                                     _addr(w_pre), *(_addr(t) for t in out), _addr(ws), nws, _raw_stream(b.device)),
-           "gconv_normgate_bwd")
+    _launch("gconv_normgate_bwd", b.device, d, _addr(dy), _addr(dh), _addr(x), _addr(b), _addr(gate), _addr(w_post),
+            _addr(scale), _addr(w_pre), *(_addr(t) for t in out), _addr(ws), nws)
     return tuple(out)
 
 
@@ -767,6 +774,5 @@ def gconv_orthogonalize(u, *, groups=1, steps=5, eps=1e-7, out=None, workspace=N
     if out is None:
         out = u.new_empty(u.shape, dtype=_torch().bfloat16)
     ws, nws = _scratch(need, u.device, workspace)
-    _check(load().gconv_orthogonalize(d, u.data_ptr(), out.data_ptr(), _addr(ws), nws, _raw_stream(u.device)),
-           "gconv_orthogonalize")
+    _launch("gconv_orthogonalize", u.device, d, u.data_ptr(), out.data_ptr(), _addr(ws), nws)
     return out
