@@ -529,13 +529,17 @@ void launch(Ortho a, int64_t groups, hipStream_t st)
     ortho_gemm<BQ, BP, WQ, WP, OP><<<(unsigned)(per * groups), 64 * WQ * WP, 0, st>>>(a);
 }
 
-// The tile whose whole rounds of 256 workgroups take least: its area, over the
-// rate of its kernel against the largest tile's, from products of 4096 x 9216
-// (us a round of that area, epilogues included; update: 256x256 104, 256x192
-// 130, 192x192 122, 128x128 146, 64x64 210; Gram matrix: 178, -, 258, 270,
-// 637). There the rule takes 256x192 for the update (293 us; 256x256 leaves a
-// quarter of its third round: 313) and 192x192 for the Gram matrix, whose 253
-// tiles fill the chip once (145 us; 256x256 has 136 tiles: 178).
+// The tile whose whole rounds of 256 workgroups take least: its area over a
+// rate, of which one set serves all three products, as it only has to put the
+// tiles in order. It does: with one product's tile forced, at 16 sizes from 512
+// x 512 to 4096 x 9216 and of 1 to 32 groups, no tile was quicker than the
+// rule's by more than the noise of 2%. What others cost, us of a whole update:
+//   4096 x 9216 (2585)  update 256x192; 256 +196, 192 +229, 128 +254
+//                       Gram matrix 192; 256 +180, 128 +341; square 192; 256 +76
+//   2048 x 8192 (745)   update 256; 192 +68, 128 +126; Gram 128; 192 +167, 64 +171
+//   1500 x 6000 (469)   update 192; 256 +58, 128 +87; Gram 64; 128 +6, 192 +123
+//   1024 x 2304 (169)   update 128; 64 +10, 192 +55; Gram 64; 128 +37, 192 +97
+//   8 of 512 x 512 (122), 2 of 128 x 1200 (83): all 64; 128 +3 to +20
 template <int OP>
 void product(const Ortho& a, int64_t groups, hipStream_t st)
 {
