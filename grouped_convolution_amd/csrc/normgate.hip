@@ -6,14 +6,17 @@
 //
 // A row is held in registers from its one read to its one write: TPR threads a
 // row (4 to 1024: 962626 rows of 32 took 783 us, forward and backward, by 16
-// threads each, 200 by 4 and 173 without branches), eight elements (VPT 16-byte pieces) a thread, so both norms and every
-// product cost no second pass. Workgroups walk over rows with the weights in registers. What
-// bounds it is HBM: (b, gate, x in; y, h out) forward, at the copy rate (16384
-// rows of 4096: 125 us, 5.3 TB/s), and the same with their gradients backward,
-// where the sums over rows and up to five tensors' values leave room for one or
-// three waves a SIMD (262144 rows of 128: 72 us, 4.7 TB/s; 16384 of 4096: 274
-// us, 3.9 TB/s). Tried and dropped: loading the next row ahead (forward 127 -> 147
-// us: fewer waves), reading past odd rows' ends and masking (76 -> 102 us).
+// threads each, 200 by 4 and 164 without branches), eight elements (VPT 16-byte
+// pieces) a thread, so both norms and every product cost no second pass.
+// Workgroups walk over rows with the weights in registers. What bounds it is HBM:
+// (b, gate, x in; y, h out) forward, at the copy rate (16384 rows of 4096: 125
+// us, 5.3 TB/s), and the same with their gradients backward, where the sums over
+// rows and up to five tensors' values leave few waves a SIMD (262144 rows of 128:
+// 70 us, 4.8 TB/s; 16384 of 4096: 281 us, 3.9 TB/s). Above 4096 columns 1024
+// threads leave 128 registers each and 16 to 129 values spill (4000 of 8000: 235
+// us, in which 1.0 GB pass for the 0.5 that are needed). Tried and dropped:
+// loading the next row ahead (forward 127 -> 147 us: fewer waves), reading past
+// odd rows' ends and masking (76 -> 102 us).
 //
 // Backward, with e = dh w_pre and yn = y ry:
 //   dy' = dy + ry (e - yn mean(e yn))                          dx = dy'
@@ -111,6 +114,7 @@ __device__ __forceinline__ float act_of(float z, int act)
 {
     return act == GCONV_ACT_NONE ? z : act == GCONV_ACT_SIGMOID ? sigmoid(z) : z * sigmoid(z);
 }
+
 // Sum over the TPR threads of a row, the same in all of them. `red`: one float
 // a wave; every call of a kernel alternates between two of them.
 template <int TPR>

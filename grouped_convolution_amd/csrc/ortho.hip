@@ -60,7 +60,7 @@ struct Ortho {
 // Stage of an operand whose reduction runs along its rows in memory: [R][64]
 // elements, the 16-byte pieces of row r at piece ^ (r & 7), so the 8 lanes
 // that are served together read 8 different sets of banks.
-template <int R, int NW, int FRAGS>
+template <int R, int NW>
 struct AlongRows {
     static constexpr int kLoads = R / 8 / NW;
     static constexpr int kBytes = R * 128;
@@ -154,8 +154,8 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void ortho_gemm(Ortho a)
 {
     constexpr int NW = WQ * WP;
     constexpr int FQ = BQ / WQ / 16, FP = BP / WP / 16;
-    using SQ = AlongRows<BQ, NW, FQ>;
-    using SP = std::conditional_t<OP == UPDATE, AcrossRows<BP, NW, FP>, AlongRows<BP, NW, FP>>;
+    using SQ = AlongRows<BQ, NW>;
+    using SP = std::conditional_t<OP == UPDATE, AcrossRows<BP, NW, FP>, AlongRows<BP, NW>>;
     constexpr int kBuf = SQ::kBytes + SP::kBytes;
     constexpr int kLoads = SQ::kLoads + SP::kLoads;
     // Stages that the LDS of a CU holds, 3 at most, and 4 of the smallest tile,
