@@ -1,6 +1,6 @@
 // ortho_small.hip -- the orthogonalised update of matrices of at most 96 rows,
-// or 128 rows of at most 256 columns (gfx950): few products, so what counts is the number of launches and the
-// waits between them.
+// or 128 rows of at most 256 columns (gfx950): few products, so what counts is
+// the number of launches and the waits between them.
 //
 // A workgroup of eight waves keeps a block of X's columns in LDS with the
 // m x m matrices beside it. A short X is one workgroup's and one launch does
