@@ -289,7 +289,9 @@ typedef enum gconv_dtype {
  * are dense, [sequences, tokens, heads, d] or [tokens, heads, d].
  * dk, dv from 1 to 128. log_decay [heads] float32; -infinity (no memory) and
  * values above 0 (growth) are valid. States [sequences, heads, dk, dv]
- * float32, dense.
+ * float32, dense. Up to 65536 heads, 2^30 tokens and as many sequences x heads
+ * as launches take (2^20 - 1 with dk and dv above 64, 2^22 - 1 with both up to
+ * 64, 2^24 - 1 one token at a time); GCONV_ERR_UNSUPPORTED beyond.
  */
 typedef struct gconv_linattn_desc {
     int64_t dtype;              /* gconv_dtype of q, k, v, o and their gradients */
