@@ -10,7 +10,9 @@ first call raises; there is no fallback.
 Names mirror the C entry points: gconv_fwd, gconv_bwd_data, gconv_bwd_filter,
 gconv_bwd_bias, gconv_output_dims, gconv_workspace_size, gconv_select_path,
 gconv_set_path_override; gconv_linattn_fwd, gconv_linattn_bwd,
-gconv_linattn_step, gconv_normgate_fwd, gconv_normgate_bwd, gconv_orthogonalize.
+gconv_linattn_step, gconv_normgate_fwd, gconv_normgate_bwd, gconv_orthogonalize,
+gconv_shortconv_fwd, gconv_shortconv_bwd, gconv_shortconv_step, gconv_scan_fwd,
+gconv_scan_bwd, gconv_scan_step.
 """
 from __future__ import annotations
 
@@ -30,6 +32,7 @@ EPILOGUE_NONE, EPILOGUE_RELU = 0, 1
 LAYOUT_NCHW, LAYOUT_NHWC = 0, 1
 F32, BF16 = 0, 1
 LINATTN_FWD, LINATTN_BWD = 0, 1
+SCAN_FWD, SCAN_BWD = 0, 1
 GATE_NONE, GATE_FULL, GATE_SEQUENCE = 0, 1, 2
 ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 PATH_NAMES = {PATH_AUTO: "auto", PATH_DIRECT: "direct", PATH_SMALLGROUP: "smallgroup",
@@ -41,7 +44,9 @@ EXPORTS = ("gconv_output_dims", "gconv_workspace_size", "gconv_fwd", "gconv_fwd_
            "gconv_set_path_override", "gconv_status_string", "gconv_last_error", "gconv_version",
            "gconv_linattn_workspace_size", "gconv_linattn_fwd", "gconv_linattn_bwd", "gconv_linattn_step",
            "gconv_normgate_workspace_size", "gconv_normgate_fwd", "gconv_normgate_bwd",
-           "gconv_orthogonalize_workspace_size", "gconv_orthogonalize")
+           "gconv_orthogonalize_workspace_size", "gconv_orthogonalize",
+           "gconv_shortconv_workspace_size", "gconv_shortconv_fwd", "gconv_shortconv_bwd", "gconv_shortconv_step",
+           "gconv_scan_workspace_size", "gconv_scan_fwd", "gconv_scan_bwd", "gconv_scan_step")
 
 
 class GconvError(RuntimeError):
@@ -73,6 +78,17 @@ class gconv_normgate_desc(ctypes.Structure):
 class gconv_ortho_desc(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "filters", "inner", "groups", "steps")] +
                 [("eps", ctypes.c_double)])
+
+
+class gconv_shortconv_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "packed", "sequences", "tokens", "dim", "taps", "act")] +
+                [(n, ctypes.c_int64 * 2) for n in ("x_stride", "dy_stride")])
+
+
+class gconv_scan_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "packed", "sequences", "tokens", "dim", "states", "groups", "softplus")] +
+                [(n, ctypes.c_int64 * 2) for n in ("u_stride", "dt_stride", "gate_stride")] +
+                [(n, ctypes.c_int64 * 3) for n in ("b_stride", "c_stride")] + [("dy_stride", ctypes.c_int64 * 2)])
 
 
 _lib = None
@@ -113,6 +129,14 @@ def load(path: str = LIB_PATH):
         "gconv_normgate_bwd": [ctypes.POINTER(gconv_normgate_desc)] + [P] * 15 + [S, P],
         "gconv_orthogonalize_workspace_size": [ctypes.POINTER(gconv_ortho_desc), ctypes.POINTER(S)],
         "gconv_orthogonalize": [ctypes.POINTER(gconv_ortho_desc), P, P, P, S, P],
+        "gconv_shortconv_workspace_size": [ctypes.POINTER(gconv_shortconv_desc), ctypes.POINTER(S)],
+        "gconv_shortconv_fwd": [ctypes.POINTER(gconv_shortconv_desc)] + [P] * 8,
+        "gconv_shortconv_bwd": [ctypes.POINTER(gconv_shortconv_desc)] + [P] * 12 + [S, P],
+        "gconv_shortconv_step": [ctypes.POINTER(gconv_shortconv_desc)] + [P] * 5 + [ctypes.c_int64, P, P],
+        "gconv_scan_workspace_size": [ctypes.POINTER(gconv_scan_desc), I, ctypes.POINTER(S)],
+        "gconv_scan_fwd": [ctypes.POINTER(gconv_scan_desc)] + [P] * 13 + [S, P],
+        "gconv_scan_bwd": [ctypes.POINTER(gconv_scan_desc)] + [P] * 21 + [S, P],
+        "gconv_scan_step": [ctypes.POINTER(gconv_scan_desc)] + [P] * 10 + [ctypes.c_int64, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -775,4 +799,241 @@ def gconv_orthogonalize(u, *, groups=1, steps=5, eps=1e-7, out=None, workspace=N
         out = u.new_empty(u.shape, dtype=_torch().bfloat16)
     ws, nws = _scratch(need, u.device, workspace)
     _launch("gconv_orthogonalize", u.device, d, u.data_ptr(), out.data_ptr(), _addr(ws), nws)
+    return out
+
+
+def _token_shape(x, cu_seqlens, name):
+    """(packed, sequences, tokens) of x: [N, T, ...], or [T, ...] with cu_seqlens (checked here)."""
+    torch = _torch()
+    if cu_seqlens is None:
+        return 0, x.shape[0], x.shape[1]
+    if not isinstance(cu_seqlens, torch.Tensor):
+        raise ValueError("cu_seqlens must be a torch.Tensor")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [sequences + 1]")
+    _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, x.device)
+    return 1, cu_seqlens.numel() - 1, x.shape[0]
+
+
+def _strides(t, packed, count):
+    """The first `count` strides of t as (between sequences, between tokens, ...)."""
+    if t is None:
+        return (ctypes.c_int64 * count)()
+    s = ((0,) + t.stride() if packed else t.stride())[:count]
+    return (ctypes.c_int64 * count)(*s)
+
+
+def _like(t, name, ref, shape):
+    """A tensor of ref's type and device, of one shape, with a contiguous last axis."""
+    _seq(t, name, ref.dtype, ref.device)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    _last_axis(t, name)
+    return t
+
+
+def _shortconv_desc(x, w, bias, act, cu_seqlens, initial_state, dy=None, d_final_state=None):
+    """Checks that the forward and the backward pass share; the descriptor and the states' shape."""
+    _seq(x, "x")
+    if x.dim() != (2 if cu_seqlens is not None else 3):
+        raise ValueError("x must be %s" % ("[T, D] with cu_seqlens" if cu_seqlens is not None else "[N, T, D]"))
+    _last_axis(x, "x")
+    if act not in ACTS:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(sorted(ACTS)), act))
+    dim = x.shape[-1]
+    _seq(w, "w")
+    if w.dim() != 2:
+        raise ValueError("w must be [D, taps]")
+    _dense(w, "w", (dim, w.shape[1]), x.dtype, x.device)
+    taps = w.shape[1]
+    if taps < 1:
+        raise ValueError("w must have at least one tap")
+    if bias is not None:
+        _dense(bias, "bias", (dim,), x.dtype, x.device)
+    packed, N, T = _token_shape(x, cu_seqlens, "x")
+    states = (N, taps - 1, dim)
+    for t, name in ((initial_state, "initial_state"), (d_final_state, "d_final_state")):
+        if t is not None:
+            _dense(t, name, states, x.dtype, x.device)
+    if dy is not None:
+        _like(dy, "dy", x, x.shape)
+    d = gconv_shortconv_desc(_dtype_code(x), packed, N, T, dim, taps, ACTS[act], _strides(x, packed, 2), _strides(dy, packed, 2))
+    return d, states
+
+
+def gconv_shortconv_fwd(x, w, bias=None, *, act="silu", cu_seqlens=None, initial_state=None):
+    """The short causal convolution of each channel: y_t = act(bias + sum_j w[:, j] x_{t-taps+1+j}).
+    x [N, T, D] (or [T, D] with cu_seqlens, int32 [N + 1], where sequences are packed; tokens in none
+    of them give 0), float32 or bfloat16, any strides with a contiguous last axis; w [D, taps] (up to
+    8), bias [D] or None; act "none", "sigmoid" or "silu"; initial_state [N, taps - 1, D], the inputs
+    before the first, or None for 0. Returns y and the final state [N, taps - 1, D], of x's type."""
+    def make():
+        d, states = _shortconv_desc(x, w, bias, act, cu_seqlens, initial_state)
+        return ctypes.byref(d), states
+
+    d, states = _plan("shortconv_fwd", (x, w, bias, cu_seqlens, initial_state), (act,), make)
+    y, final = x.new_empty(x.shape), x.new_empty(states)
+    _launch("gconv_shortconv_fwd", x.device, d, _addr(x), _addr(w), _addr(bias), _addr(cu_seqlens), _addr(initial_state), _addr(y),
+            _addr(final))
+    return y, final
+
+
+def gconv_shortconv_bwd(dy, x, w, bias=None, *, act="silu", cu_seqlens=None, initial_state=None, d_final_state=None, workspace=None):
+    """Gradients of gconv_shortconv_fwd for dy of y and d_final_state of the final state (None: 0).
+    Returns dx, dw, dbias (None without bias) and the gradient of initial_state (None without it)."""
+    def make():
+        d, states = _shortconv_desc(x, w, bias, act, cu_seqlens, initial_state, _seq(dy, "dy"), d_final_state)
+        n = ctypes.c_size_t()
+        _check(load().gconv_shortconv_workspace_size(ctypes.byref(d), ctypes.byref(n)), "gconv_shortconv_workspace_size")
+        return ctypes.byref(d), n.value
+
+    d, need = _plan("shortconv_bwd", (dy, x, w, bias, cu_seqlens, initial_state, d_final_state), (act,), make)
+    dx, dw, dbias, ds = (t.new_empty(t.shape) if t is not None else None for t in (x, w, bias, initial_state))
+    ws, nws = _scratch(need, x.device, workspace)
+    _launch("gconv_shortconv_bwd", x.device, d, _addr(dy), _addr(x), _addr(w), _addr(bias), _addr(cu_seqlens), _addr(initial_state),
+            _addr(d_final_state), _addr(dx), _addr(dw), _addr(dbias), _addr(ds), _addr(ws), nws)
+    return dx, dw, dbias, ds
+
+
+def _shortconv_step_plan(x, w, state, bias, act, slots, out):
+    torch = _torch()
+    _seq(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [B, D]")
+    d, _ = _shortconv_desc(x[:, None], w, bias, act, None, None)
+    B, dim = x.shape
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("state must be [slots, taps - 1, D]")
+    _dense(state, "state", (state.shape[0], w.shape[1] - 1, dim), x.dtype, x.device)
+    if slots is not None:
+        _dense(slots, "slots", (B,), torch.int32, x.device)
+    if out is not None:
+        _dense(out, "out", (B, dim), x.dtype, x.device)
+    d.tokens = 0
+    return ctypes.byref(d), state.shape[0]
+
+
+def gconv_shortconv_step(x, w, state, bias=None, *, act="silu", slots=None, out=None):
+    """One token x [B, D] of each of B sequences, in place on `state` [slots, taps - 1, D] (x's type);
+    slots int32 [B] (different ones; one out of range gives y = 0 and touches no state) or None for
+    slot b. Returns y [B, D]."""
+    d, num = _plan("shortconv_step", (x, w, state, bias, slots, out), (act,),
+                   lambda: _shortconv_step_plan(x, w, state, bias, act, slots, out))
+    if out is None:
+        out = x.new_empty(x.shape)
+    _launch("gconv_shortconv_step", x.device, d, x.data_ptr(), w.data_ptr(), _addr(bias), state.data_ptr(), _addr(slots), num,
+            out.data_ptr())
+    return out
+
+
+def _scan_desc(u, dt, a, b, c, skip, gate, dt_bias, softplus, cu_seqlens, initial_state, dy=None, d_final_state=None):
+    """Checks that the forward and the backward pass share; the descriptor and the states' shape."""
+    torch = _torch()
+    _seq(u, "u")
+    lead = 1 if cu_seqlens is not None else 2
+    if u.dim() != lead + 1:
+        raise ValueError("u must be %s" % ("[T, D] with cu_seqlens" if lead == 1 else "[N, T, D]"))
+    _last_axis(u, "u")
+    dim = u.shape[-1]
+    _like(dt, "dt", u, u.shape)
+    _seq(b, "b", u.dtype, u.device)
+    if b.dim() != lead + 2 or b.shape[:lead] != u.shape[:lead]:
+        raise ValueError("b must be %s" % ("[T, groups, states]" if lead == 1 else "[N, T, groups, states]"))
+    _last_axis(b, "b")
+    _like(c, "c", u, b.shape)
+    groups, n = b.shape[-2:]
+    _dense(a, "a", (dim, n), torch.float32, u.device)
+    for t, name in ((skip, "skip"), (dt_bias, "dt_bias")):
+        if t is not None:
+            _dense(t, name, (dim,), torch.float32, u.device)
+    for t, name in ((gate, "gate"), (dy, "dy")):
+        if t is not None:
+            _like(t, name, u, u.shape)
+    packed, N, T = _token_shape(u, cu_seqlens, "u")
+    states = (N, dim, n)
+    for t, name in ((initial_state, "initial_state"), (d_final_state, "d_final_state")):
+        if t is not None:
+            _dense(t, name, states, torch.float32, u.device)
+    d = gconv_scan_desc(_dtype_code(u), packed, N, T, dim, n, groups, int(bool(softplus)), _strides(u, packed, 2),
+                        _strides(dt, packed, 2), _strides(gate, packed, 2), _strides(b, packed, 3), _strides(c, packed, 3),
+                        _strides(dy, packed, 2))
+    return d, states
+
+
+def gconv_scan_workspace_size(desc: gconv_scan_desc, op: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gconv_scan_workspace_size(ctypes.byref(desc), int(op), ctypes.byref(n)), "gconv_scan_workspace_size")
+    return n.value
+
+
+def gconv_scan_fwd(u, dt, a, b, c, *, skip=None, gate=None, dt_bias=None, softplus=True, cu_seqlens=None, initial_state=None,
+                   workspace=None):
+    """The selective state space scan: with s_t = softplus(dt_t + dt_bias) (or without the softplus),
+    h_t = exp(s_t a) h_{t-1} + s_t u_t b_t and y_t = (c_t . h_t + skip u_t) silu(gate_t), for each channel.
+    u, dt, gate (None: no gate) [N, T, D], b, c [N, T, G, S] (D a multiple of G, S up to 64), or [T, D] and
+    [T, G, S] with cu_seqlens (int32 [N + 1]) where sequences are packed (tokens in none of them give 0);
+    float32 or bfloat16, any strides with a contiguous last axis. a [D, S], skip and dt_bias [D] (or None)
+    float32; initial_state [N, D, S] float32 or None. Returns y and the final state [N, D, S] float32."""
+    def make():
+        d, states = _scan_desc(u, dt, a, b, c, skip, gate, dt_bias, softplus, cu_seqlens, initial_state)
+        return ctypes.byref(d), states, gconv_scan_workspace_size(d, SCAN_FWD)
+
+    d, states, need = _plan("scan_fwd", (u, dt, a, b, c, skip, gate, dt_bias, cu_seqlens, initial_state), (int(bool(softplus)),), make)
+    y, final = u.new_empty(u.shape), a.new_empty(states)
+    ws, nws = _scratch(need, u.device, workspace)
+    _launch("gconv_scan_fwd", u.device, d, _addr(u), _addr(dt), _addr(a), _addr(b), _addr(c), _addr(skip), _addr(gate), _addr(dt_bias),
+            _addr(cu_seqlens), _addr(initial_state), _addr(y), _addr(final), _addr(ws), nws)
+    return y, final
+
+
+def gconv_scan_bwd(dy, u, dt, a, b, c, *, skip=None, gate=None, dt_bias=None, softplus=True, cu_seqlens=None, initial_state=None,
+                   d_final_state=None, workspace=None):
+    """Gradients of gconv_scan_fwd for dy of y and d_final_state of the final state (None: 0). Returns du,
+    ddt, da, db, dc, dskip, dgate, ddt_bias and the gradient of initial_state, of the inputs' shapes and
+    types (None for those that are None)."""
+    def make():
+        d, _ = _scan_desc(u, dt, a, b, c, skip, gate, dt_bias, softplus, cu_seqlens, initial_state, _seq(dy, "dy"), d_final_state)
+        return ctypes.byref(d), gconv_scan_workspace_size(d, SCAN_BWD)
+
+    d, need = _plan("scan_bwd", (dy, u, dt, a, b, c, skip, gate, dt_bias, cu_seqlens, initial_state, d_final_state),
+                    (int(bool(softplus)),), make)
+    out = [t.new_empty(t.shape) if t is not None else None for t in (u, dt, a, b, c, skip, gate, dt_bias, initial_state)]
+    ws, nws = _scratch(need, u.device, workspace)
+    _launch("gconv_scan_bwd", u.device, d, _addr(dy), _addr(u), _addr(dt), _addr(a), _addr(b), _addr(c), _addr(skip), _addr(gate),
+            _addr(dt_bias), _addr(cu_seqlens), _addr(initial_state), _addr(d_final_state), *(_addr(t) for t in out), _addr(ws), nws)
+    return tuple(out)
+
+
+def _scan_step_plan(u, dt, a, b, c, state, skip, gate, dt_bias, softplus, slots, out):
+    torch = _torch()
+    for t, name in ((u, "u"), (dt, "dt"), (gate, "gate")):
+        if t is not None and _seq(t, name).dim() != 2:
+            raise ValueError("%s must be [B, D]" % name)
+    for t, name in ((b, "b"), (c, "c")):
+        if _seq(t, name).dim() != 3:
+            raise ValueError("%s must be [B, groups, states]" % name)
+    one = [t[:, None] if t is not None else None for t in (u, dt, b, c, gate)]
+    d, _ = _scan_desc(one[0], one[1], a, one[2], one[3], skip, one[4], dt_bias, softplus, None, None)
+    B, dim = u.shape
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("state must be [slots, D, states]")
+    _dense(state, "state", (state.shape[0],) + tuple(a.shape), torch.float32, u.device)
+    if slots is not None:
+        _dense(slots, "slots", (B,), torch.int32, u.device)
+    if out is not None:
+        _dense(out, "out", (B, dim), u.dtype, u.device)
+    d.tokens = 0
+    return ctypes.byref(d), state.shape[0]
+
+
+def gconv_scan_step(u, dt, a, b, c, state, *, skip=None, gate=None, dt_bias=None, softplus=True, slots=None, out=None):
+    """One token of each of B sequences, in place on `state` [slots, D, S] float32: u, dt, gate [B, D],
+    b, c [B, G, S]; slots int32 [B] (different ones; one out of range gives y = 0 and touches no state)
+    or None for slot b. Returns y [B, D]."""
+    d, num = _plan("scan_step", (u, dt, a, b, c, state, skip, gate, dt_bias, slots, out), (int(bool(softplus)),),
+                   lambda: _scan_step_plan(u, dt, a, b, c, state, skip, gate, dt_bias, softplus, slots, out))
+    if out is None:
+        out = u.new_empty(u.shape)
+    _launch("gconv_scan_step", u.device, d, u.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(skip),
+            _addr(gate), _addr(dt_bias), state.data_ptr(), _addr(slots), num, out.data_ptr())
     return out

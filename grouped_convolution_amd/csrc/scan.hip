@@ -1,0 +1,1209 @@
+// scan.hip -- the selective state space scan: a recurrence whose decay and
+// inputs depend on the token (gfx950).
+//
+//   dt_t = softplus(raw_t + dt_bias)           (or raw_t + dt_bias)
+//   h_t  = exp(dt_t a) h_{t-1} + dt_t u_t b_t  for each channel and state
+//   y_t  = (c_t . h_t + skip u_t) silu(gate_t)
+//
+// and backward, with dy' = dy silu(gate) and the adjoint state g:
+//
+//   g_t = c_t dy'_t + exp(dt_{t+1} a) g_{t+1}      m_t = exp(dt_t a) h_{t-1} g_t
+//   dc_t = sum over channels of dy'_t h_t           db_t = sum over channels of dt_t u_t g_t
+//   da = sum_t dt_t m_t         s_t = sum over states of b_t g_t
+//   du_t = dt_t s_t + skip dy'_t         ddt_t = u_t s_t + sum over states of a m_t
+//
+// The decays differ for every (token, channel, state), so there is no product of
+// matrices in it: what bounds it is the vector pipes, one exponential (a quarter
+// of the rate) and four operations for each of them forward.
+//
+// A workgroup takes 64 channels, a lane each, and NW waves, each with four of the
+// states in registers: b_t and c_t are then the same for a whole wave and come
+// from scalar memory as operands. What depends on (token, channel) alone (softplus,
+// gate, sums over the waves) is done once for a tile of tokens by all threads and
+// passed through LDS.
+//
+// Long sequences are cut into chunks: a first kernel runs each chunk from a zero
+// state, a second carries the states over the chunks, and the last starts each
+// chunk from its true state. The decay over a chunk is exp(a sum dt), so a chunk
+// passes on one number a channel for it. Backward, the same first kernel also
+// makes what the chunk adds to the adjoint before it, sum_t (decay from the
+// chunk's start to t) c_t dy'_t, running forward.
+//
+// Tokens carry marks (first or last of a sequence, or of none), made beforehand
+// with b and c in float32, four states of one wave side by side.
+#include "seq_host.h"
+#include "seq_tokens.h"
+
+namespace gconv {
+namespace {
+
+constexpr int kLanes = 64;   // channels of a workgroup
+constexpr int kSpw = 4;      // states of a wave
+constexpr int kTile = 16;    // tokens passed through LDS at once
+constexpr int kBack = 8;     // the same, of the backward pass
+constexpr float kLog2e = 1.44269504088896340736f;
+
+enum { FIRST = 1, LAST = 2 };  // marks of a token; the sequence's number is above them, a token of none is -1
+
+struct Scan {
+    const void *u, *dt, *b, *c, *gate, *dy;
+    const float *a, *skip, *dt_bias, *init, *dfinal;
+    void *y, *du, *ddt, *dgate;
+    float *final_, *dinit;
+    Sequences seq;
+    int64_t u_s[2], dt_s[2], gate_s[2], dy_s[2], b_s[3], c_s[3];
+    float* bc;          // [rows][groups][NW][8]: four of b, four of c
+    int32_t* mark;      // [rows]
+    float* ends;        // [chunks][blocks][NW][4][64]: states; later those before each chunk
+    float* adds;        // the same of the adjoint; later that after each chunk
+    float* sums;        // [chunks][blocks][64]: sum of dt
+    int32_t* breaks;    // [chunks]: whether a sequence begins in it
+    float* part_a;      // [chunks][blocks][NW][4][64]: of da
+    float* part_d;      // [chunks][2][dim]: of dskip and ddt_bias
+    float* part_bc;     // [blocks of a group][rows][groups][NW][8]: of db and dc
+    int64_t rows;       // tokens of all sequences
+    int64_t per, chunks;  // chunks of a stretch (a sequence, or all packed tokens), of all
+    int chunk;          // tokens
+    int dim, states, groups;
+    int gdim, gblocks;  // channels of a group, workgroups along them
+    int blocks;         // groups * gblocks
+    int softplus;
+};
+
+// What a workgroup works at.
+struct Where {
+    int g, gb, block;      // group, workgroup along its channels, workgroup along all
+    int c0, left;          // first channel, channels
+    int64_t chunk, outer;
+    int64_t t0;            // first token, in its stretch
+    int n;                 // tokens
+    int64_t row0;          // first token, of all
+};
+
+__device__ __forceinline__ Where where(const Scan& a)
+{
+    Where w;
+    w.block = (int)(blockIdx.x % (unsigned)a.blocks);
+    w.chunk = blockIdx.x / (unsigned)a.blocks;
+    w.g = w.block / a.gblocks;
+    w.gb = w.block - w.g * a.gblocks;
+    w.c0 = w.g * a.gdim + w.gb * kLanes;
+    w.left = min(kLanes, a.gdim - w.gb * kLanes);
+    w.outer = w.chunk / a.per;
+    w.t0 = (w.chunk - w.outer * a.per) * a.chunk;
+    w.n = (int)min((int64_t)a.chunk, a.seq.tokens - w.t0);
+    w.row0 = w.outer * a.seq.tokens + w.t0;
+    return w;
+}
+
+// softplus(x) = max(x, 0) + log(1 + w), w = exp(-|x|). The logarithm of 1 + w as
+// it was rounded, times w over what was added: right to the last bits however
+// small w is.
+__device__ __forceinline__ float softplus_of(float x)
+{
+    const float w = __expf(-fabsf(x)), v = 1.f + w, d = v - 1.f;
+    const float l = d == 0.f ? w : __logf(v) * (w * __builtin_amdgcn_rcpf(d));
+    return fmaxf(x, 0.f) + l;
+}
+
+template <typename T>
+struct Quad {
+    float v[4];
+    __device__ __forceinline__ Quad() {}
+    __device__ __forceinline__ explicit Quad(const Packed<T, 4>& p)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)p.e[e];
+    }
+};
+
+// ---- marks, b and c -------------------------------------------------------------
+
+// A thread: the marks of a token and four states of one group.
+template <typename T>
+__global__ __launch_bounds__(256) void scan_prep(Scan a, int nw)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int per = a.groups * nw;
+    const int64_t row = id / per;
+    if (row >= a.rows) return;
+    const int k = (int)(id - row * per), g = k / nw, w = k - g * nw;
+    int n, mark = 0;
+    int64_t outer = 0, t = row;
+    if (!a.seq.cu) {
+        outer = row / a.seq.tokens;
+        t = row - outer * a.seq.tokens;
+        n = (int)outer;
+        mark = (t == 0 ? FIRST : 0) | (t == a.seq.tokens - 1 ? LAST : 0);
+    } else {
+        n = a.seq.find(row);
+        if (n < 0 || n >= a.seq.count) n = -1;
+        else mark = (row == a.seq.bound(n) ? FIRST : 0) | (row == a.seq.bound(n + 1) - 1 ? LAST : 0);
+    }
+    if (k == 0) a.mark[row] = n < 0 ? -1 : n * 4 + mark;
+    f4 b = {0, 0, 0, 0}, c = {0, 0, 0, 0};
+    if (n >= 0) {
+        const T* pb = (const T*)a.b + outer * a.b_s[0] + t * a.b_s[1] + g * a.b_s[2];
+        const T* pc = (const T*)a.c + outer * a.c_s[0] + t * a.c_s[1] + g * a.c_s[2];
+#pragma unroll
+        for (int s = 0; s < kSpw; ++s) {
+            if (w * kSpw + s >= a.states) break;
+            b[s] = (float)pb[w * kSpw + s];
+            c[s] = (float)pc[w * kSpw + s];
+        }
+    }
+    f4* o = (f4*)(a.bc + id * 8);
+    o[0] = b;
+    o[1] = c;
+}
+
+// Sequences without tokens: the state after them is the one before, and the
+// gradients likewise.
+__global__ __launch_bounds__(256) void scan_empty(Sequences seq, const float* from, float* to, int64_t size)
+{
+    const int n = blockIdx.x;
+    if (seq.cu ? seq.bound(n + 1) > seq.bound(n) : seq.tokens > 0) return;
+    for (int64_t i = threadIdx.x; i < size; i += 256) to[n * size + i] = from ? from[n * size + i] : 0.f;
+}
+
+// ---- parts that the kernels share -------------------------------------------------
+
+// The states of lane's channel that its wave holds.
+struct Mine {
+    int lane, wave;
+    int ch;         // channel, clamped to one that exists
+    bool live;
+    int64_t at;     // element of [dim][states]
+    int have;       // states that exist, of kSpw
+    template <int NW>
+    __device__ __forceinline__ static Mine of(const Scan& a, const Where& w)
+    {
+        Mine m;
+        m.lane = threadIdx.x & 63;
+        m.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        m.live = m.lane < w.left;
+        m.ch = w.c0 + (m.live ? m.lane : 0);
+        m.at = (int64_t)m.ch * a.states + m.wave * kSpw;
+        m.have = m.live ? max(0, min(kSpw, a.states - m.wave * kSpw)) : 0;
+        return m;
+    }
+    // p[n][dim][states] of sequence n, or 0
+    __device__ __forceinline__ f4 get(const Scan& a, const float* p, int64_t n) const
+    {
+        f4 v = {0, 0, 0, 0};
+        if (p) {
+            const float* q = p + n * a.dim * a.states + at;
+#pragma unroll
+            for (int s = 0; s < kSpw; ++s)
+                if (s < have) v[s] = q[s];
+        }
+        return v;
+    }
+    __device__ __forceinline__ void put(const Scan& a, float* p, int64_t n, f4 v) const
+    {
+        float* q = p + n * a.dim * a.states + at;
+#pragma unroll
+        for (int s = 0; s < kSpw; ++s)
+            if (s < have) q[s] = v[s];
+    }
+    // index into `ends` and its like, of state s
+    __device__ __forceinline__ int64_t slot(const Scan& a, int64_t chunk, int block, int nw, int s) const
+    {
+        return ((((chunk * a.blocks + block) * nw + wave) * kSpw + s) * kLanes) + lane;
+    }
+};
+
+// A thread's quads of a tile: quad q is token q / 16, channels 4 (q % 16).
+template <typename T, int NW, int TILE>
+struct Quads {
+    static constexpr int kCount = TILE * 16, kThreads = NW * 64;
+    static constexpr int kPer = (kCount + kThreads - 1) / kThreads;
+    static __device__ __forceinline__ int of(int i) { return i * kThreads + (int)threadIdx.x; }
+};
+
+template <typename T>
+__device__ __forceinline__ Packed<T, 4> load_quad(const void* p, const int64_t* stride, const Where& w, int64_t t, int quad)
+{
+    return load_piece<T, 4>((const T*)p + w.outer * stride[0] + t * stride[1] + w.c0, quad * 4, w.left);
+}
+
+// dt and dt u of a quad of channels; 0 for a token of no sequence.
+template <typename T>
+__device__ __forceinline__ void step_sizes(const Scan& a, const f4& bias, const Packed<T, 4>& raw, const Packed<T, 4>& u, bool real, f4* dt,
+                                           f4* dtu)
+{
+    const Quad<T> r(raw), uu(u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float v = r.v[e] + bias[e];
+        if (a.softplus) v = softplus_of(v);
+        (*dt)[e] = real ? v : 0.f;
+        (*dtu)[e] = real ? v * uu.v[e] : 0.f;
+    }
+}
+
+__device__ __forceinline__ f4 channel_quad(const float* p, const Where& w, int quad)
+{
+    f4 v = {0, 0, 0, 0};
+    if (p) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (quad * 4 + e < w.left) v[e] = p[w.c0 + quad * 4 + e];
+    }
+    return v;
+}
+
+__device__ __forceinline__ float silu_of(float z) { return z * sigmoid_of(z); }
+
+// dy' of a quad of channels; 0 for a token of no sequence.
+template <typename T>
+__device__ __forceinline__ f4 gated(const Scan& a, const Packed<T, 4>& dy, const Packed<T, 4>& gate, bool real)
+{
+    const Quad<T> d(dy);
+    f4 v = {d.v[0], d.v[1], d.v[2], d.v[3]};
+    if (a.gate) {
+        const Quad<T> z(gate);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= silu_of(z.v[e]);
+    }
+    return real ? v : f4{0, 0, 0, 0};
+}
+
+// ---- forward ----------------------------------------------------------------------
+
+// OUT: the outputs, from the state before each chunk; else each chunk's own
+// contribution to the state after it (and, ADJ, to the adjoint before it).
+template <typename T, int NW, bool OUT, bool ADJ>
+__global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
+{
+    using Q = Quads<T, NW, kTile>;
+    constexpr int kW = ADJ ? 3 : 2;
+    __shared__ float sd[2][kTile][kW][kLanes];            // dt, dt u (, dy')
+    __shared__ float yp[OUT ? 2 : 1][OUT ? NW : 1][OUT ? kTile : 1][kLanes];
+    const Where w = where(a);
+    const Mine m = Mine::of<NW>(a, w);
+    const int quad = threadIdx.x & 15;
+    const f4 bias = channel_quad(a.dt_bias, w, quad), skip = channel_quad(a.skip, w, quad);
+
+    f4 a2 = m.get(a, a.a, 0) * kLog2e;
+    f4 h = {0, 0, 0, 0}, p = {1, 1, 1, 1}, r = {0, 0, 0, 0};
+    float total = 0.f;
+    int broken = 0;
+    if (OUT && a.per > 1) {
+#pragma unroll
+        for (int s = 0; s < kSpw; ++s) h[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
+    }
+    struct Raw {
+        Packed<T, 4> u, dt, z, dy;
+    } raw[Q::kPer];
+    Packed<T, 4> cur_u[Q::kPer], cur_z[Q::kPer], old_u[Q::kPer], old_z[Q::kPer];  // of this tile and the one before
+    auto fetch = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < Q::kPer; ++i) {
+            const int q = Q::of(i), tok = min(tile * kTile + q / 16, w.n - 1);
+            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+            raw[i].u = load_quad<T>(a.u, a.u_s, w, w.t0 + tok, quad);
+            raw[i].dt = load_quad<T>(a.dt, a.dt_s, w, w.t0 + tok, quad);
+            if ((OUT || ADJ) && a.gate) raw[i].z = load_quad<T>(a.gate, a.gate_s, w, w.t0 + tok, quad);
+            if (ADJ) raw[i].dy = load_quad<T>(a.dy, a.dy_s, w, w.t0 + tok, quad);
+        }
+    };
+    auto stage = [&](int tile) {  // of what was fetched
+#pragma unroll
+        for (int i = 0; i < Q::kPer; ++i) {
+            const int q = Q::of(i), tok = tile * kTile + q / 16;
+            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+            const bool real = tok < w.n && a.mark[w.row0 + min(tok, w.n - 1)] >= 0;
+            f4 dt, dtu;
+            step_sizes<T>(a, bias, raw[i].dt, raw[i].u, real, &dt, &dtu);
+            float(*row)[kLanes] = sd[tile & 1][q / 16];
+            *(f4*)&row[0][quad * 4] = dt;
+            *(f4*)&row[1][quad * 4] = dtu;
+            if constexpr (ADJ) *(f4*)&row[kW - 1][quad * 4] = gated<T>(a, raw[i].dy, raw[i].z, real);
+            if (OUT) {
+                old_u[i] = cur_u[i];
+                old_z[i] = cur_z[i];
+                cur_u[i] = raw[i].u;
+                cur_z[i] = raw[i].z;
+            }
+        }
+    };
+    const int tiles = (w.n + kTile - 1) / kTile;
+    const float* bc = a.bc + ((w.row0 * a.groups + w.g) * NW + m.wave) * 8;
+    const int64_t bc_step = (int64_t)a.groups * NW * 8;
+    fetch(0);
+    stage(0);
+    __syncthreads();
+    // One barrier a tile: while the waves run over a tile, its outputs go to one
+    // buffer, those of the tile before are read from the other, and the next
+    // tile's inputs are put beside this one's.
+    for (int tile = 0; tile < tiles + (OUT ? 1 : 0); ++tile) {
+        if (tile + 1 < tiles) fetch(tile + 1);
+        if (tile < tiles) {
+            // marks of the tile, a token a lane
+            const int tok = tile * kTile + (m.lane & (kTile - 1));
+            const int mk = tok < w.n ? a.mark[w.row0 + tok] : -1;
+            const uint32_t firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kTile) - 1);
+            const uint32_t lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kTile) - 1);
+            const int here = min(kTile, w.n - tile * kTile);
+            auto token = [&](int i, bool marks) {
+                if (marks && (firsts >> i & 1)) {
+                    h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
+                    p = f4{0, 0, 0, 0};
+                    broken = 1;
+                }
+                const float dt = sd[tile & 1][i][0][m.lane], dtu = sd[tile & 1][i][1][m.lane];
+                const float* o = bc + (int64_t)(tile * kTile + i) * bc_step;
+                float y = 0.f, dy = 0.f;
+                if (ADJ) dy = sd[tile & 1][i][kW - 1][m.lane];
+                if (!OUT) total += dt;
+#pragma unroll
+                for (int s = 0; s < kSpw; ++s) {
+                    const float e = __builtin_amdgcn_exp2f(dt * a2[s]);
+                    h[s] = fmaf(e, h[s], dtu * o[s]);
+                    if (OUT) y = fmaf(o[4 + s], h[s], y);
+                    if (ADJ) {
+                        p[s] *= e;
+                        r[s] = fmaf(p[s], o[4 + s] * dy, r[s]);
+                    }
+                }
+                if (OUT) yp[tile & 1][OUT ? m.wave : 0][OUT ? i : 0][m.lane] = y;
+                if (marks && (lasts >> i & 1)) {
+                    const int n = __builtin_amdgcn_readlane(mk, i) >> 2;
+                    if (OUT && a.final_) m.put(a, a.final_, n, h);
+                    if (ADJ && a.dfinal) r += p * m.get(a, a.dfinal, n);
+                    h = f4{0, 0, 0, 0};
+                }
+            };
+            if (here == kTile && (firsts | lasts) == 0) {
+#pragma unroll 4
+                for (int i = 0; i < kTile; ++i) token(i, false);
+            } else {
+                for (int i = 0; i < here; ++i) token(i, true);
+            }
+        }
+        if (OUT && tile > 0) {
+            const bool last = tile == tiles;  // nothing has been staged since
+#pragma unroll
+            for (int i = 0; i < Q::kPer; ++i) {
+                const int q = Q::of(i), tok = (tile - 1) * kTile + q / 16;
+                if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+                if (tok >= w.n) continue;
+                const Quad<T> u(last ? cur_u[i] : old_u[i]);
+                f4 v = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < NW; ++k) v += *(const f4*)&yp[OUT ? (tile - 1) & 1 : 0][OUT ? k : 0][OUT ? q / 16 : 0][quad * 4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fmaf(skip[e], u.v[e], v[e]);
+                if (a.gate) {
+                    const Quad<T> z(last ? cur_z[i] : old_z[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] *= silu_of(z.v[e]);
+                }
+                const bool real = a.mark[w.row0 + tok] >= 0;
+                float o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = real ? v[e] : 0.f;
+                store_piece<T, 4>((T*)a.y + (w.row0 + tok) * a.dim + w.c0, quad * 4, w.left, o);
+            }
+        }
+        if (tile + 1 < tiles) stage(tile + 1);
+        __syncthreads();
+    }
+    if (!OUT) {
+#pragma unroll
+        for (int s = 0; s < kSpw; ++s) {
+            a.ends[m.slot(a, w.chunk, w.block, NW, s)] = h[s];
+            if (ADJ) a.adds[m.slot(a, w.chunk, w.block, NW, s)] = r[s];
+        }
+        if (m.wave == 0) a.sums[(w.chunk * a.blocks + w.block) * kLanes + m.lane] = total;
+        if (w.block == 0 && threadIdx.x == 0) a.breaks[w.chunk] = broken;
+    }
+}
+
+// Carries states over the chunks of a stretch: what `ends` holds becomes the
+// state before each chunk, and (backward) what `adds` holds the adjoint after it.
+// A thread: one state of one channel. Where a sequence begins in a chunk, nothing
+// from before it comes through.
+__global__ __launch_bounds__(256) void scan_carry(Scan a, int nw, int64_t outers)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, size = (int64_t)a.blocks * nw * kSpw * kLanes;
+    const int64_t outer = id / size, at = id - outer * size;
+    if (outer >= outers) return;
+    const int lane = (int)(at % kLanes), state = (int)(at / kLanes % (nw * kSpw)), block = (int)(at / kLanes / (nw * kSpw));
+    const int g = block / a.gblocks, in = (block - g * a.gblocks) * kLanes + lane;
+    const bool have = in < a.gdim && state < a.states;
+    const float a2 = have ? a.a[(int64_t)(g * a.gdim + in) * a.states + state] * kLog2e : 0.f;
+    const int64_t c0 = outer * a.per;
+    const float* sums = a.sums + block * kLanes + lane;
+    const bool back = blockIdx.y != 0;
+    float* v = (back ? a.adds : a.ends) + at;
+    constexpr int U = 8;
+    float h = 0.f;
+    for (int64_t c = 0; c < a.per; c += U) {
+        float e[U], s[U];
+        int b[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t k = min(c + i, a.per - 1), n = c0 + (back ? a.per - 1 - k : k);
+            e[i] = v[n * size];
+            s[i] = sums[n * a.blocks * kLanes];
+            b[i] = a.breaks[n];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (c + i >= a.per) break;
+            const int64_t k = c + i, n = c0 + (back ? a.per - 1 - k : k);
+            v[n * size] = h;
+            h = b[i] ? e[i] : fmaf(__builtin_amdgcn_exp2f(s[i] * a2), h, e[i]);
+        }
+    }
+}
+
+// ---- backward ---------------------------------------------------------------------
+
+// Sum over the 16 lanes of a row, in all of them.
+__device__ __forceinline__ float row16_sum(float v)
+{
+    auto add = [](float x, auto ctrl) {
+        return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    v = add(v, std::integral_constant<int, 0x128>{});  // row_ror 8, 4, 2, 1
+    v = add(v, std::integral_constant<int, 0x124>{});
+    v = add(v, std::integral_constant<int, 0x122>{});
+    return add(v, std::integral_constant<int, 0x121>{});
+}
+
+// Tokens of a chunk of the backward pass: its states at every kBack tokens stay in LDS.
+template <int NW>
+constexpr int back_chunk()
+{
+    return NW <= 4 ? 64 : 256 / NW;
+}
+
+// A chunk's gradients. Forward once over the chunk, keeping the state at each
+// tile; then tile by tile from the last, forward again with the states and decays
+// of its tokens in registers, and back over them.
+//
+// The sums over channels (dc, db) go through the matrix pipe, which is idle
+// otherwise: a product with a matrix that has ones in one row adds the 64 lanes'
+// values in fours into that row, exactly as float32 sums; what is left, 16 lanes,
+// takes four shifted additions for 16 such rows at once.
+template <typename T, int NW>
+__global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
+{
+    using Q = Quads<T, NW, kBack>;
+    constexpr int kTiles = back_chunk<NW>() / kBack;
+    __shared__ float sd[kBack][3][kLanes];            // dt, dt u, dy'
+    __shared__ float part[3][NW][kBack][kLanes];      // of s, the sum of a m, and y
+    __shared__ f4 held[kTiles][NW * 64];
+    const Where w = where(a);
+    const Mine m = Mine::of<NW>(a, w);
+    const int quad = threadIdx.x & 15;
+    const f4 bias = channel_quad(a.dt_bias, w, quad), skip = channel_quad(a.skip, w, quad);
+    const f4 av = m.get(a, a.a, 0), a2 = av * kLog2e;
+    f4 h = {0, 0, 0, 0}, g = {0, 0, 0, 0}, da = {0, 0, 0, 0};
+    if (a.per > 1) {
+#pragma unroll
+        for (int s = 0; s < kSpw; ++s) {
+            h[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
+            g[s] = a.adds[m.slot(a, w.chunk, w.block, NW, s)];
+        }
+    }
+    f4 s_skip = {0, 0, 0, 0}, s_bias = {0, 0, 0, 0};
+    struct Raw {
+        Packed<T, 4> u, dt, z, dy;
+        int mark;
+    } raw[Q::kPer];
+    auto fetch = [&](int tile, bool all) {
+#pragma unroll
+        for (int i = 0; i < Q::kPer; ++i) {
+            const int q = Q::of(i), tok = min(tile * kBack + q / 16, w.n - 1);
+            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+            raw[i].mark = a.mark[w.row0 + tok];
+            raw[i].u = load_quad<T>(a.u, a.u_s, w, w.t0 + tok, quad);
+            raw[i].dt = load_quad<T>(a.dt, a.dt_s, w, w.t0 + tok, quad);
+            if (!all) continue;
+            if (a.gate) raw[i].z = load_quad<T>(a.gate, a.gate_s, w, w.t0 + tok, quad);
+            raw[i].dy = load_quad<T>(a.dy, a.dy_s, w, w.t0 + tok, quad);
+        }
+    };
+    auto stage = [&](int tile, bool all) {
+#pragma unroll
+        for (int i = 0; i < Q::kPer; ++i) {
+            const int q = Q::of(i), tok = tile * kBack + q / 16;
+            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+            const bool real = tok < w.n && raw[i].mark >= 0;
+            f4 dt, dtu;
+            step_sizes<T>(a, bias, raw[i].dt, raw[i].u, real, &dt, &dtu);
+            float(*row)[kLanes] = sd[q / 16];
+            *(f4*)&row[0][quad * 4] = dt;
+            *(f4*)&row[1][quad * 4] = dtu;
+            if (all) *(f4*)&row[2][quad * 4] = gated<T>(a, raw[i].dy, raw[i].z, real);
+        }
+    };
+    const int tiles = (w.n + kBack - 1) / kBack;
+    const float* bc = a.bc + ((w.row0 * a.groups + w.g) * NW + m.wave) * 8;
+    const int64_t bc_step = (int64_t)a.groups * NW * 8;
+    float* out_bc = a.part_bc + (((int64_t)w.gb * a.rows + w.row0) * a.groups + w.g) * NW * 8 + m.wave * 8;
+
+    int mk = -1, here = 0;
+    uint32_t firsts = 0, lasts = 0;
+    auto marks = [&](int tile) {
+        const int tok = tile * kBack + (m.lane & (kBack - 1));
+        mk = tok < w.n ? a.mark[w.row0 + tok] : -1;
+        firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kBack) - 1);
+        lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kBack) - 1);
+        here = min(kBack, w.n - tile * kBack);
+    };
+    fetch(0, tiles == 1);
+    for (int tile = 0; tile + 1 < tiles; ++tile) {
+        held[tile][threadIdx.x] = h;
+        stage(tile, false);
+        __syncthreads();
+        fetch(tile + 1, tile + 2 == tiles);
+        marks(tile);
+#pragma unroll
+        for (int i = 0; i < kBack; ++i) {
+            if (firsts >> i & 1) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
+            const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane];
+            const float* o = bc + (int64_t)(tile * kBack + i) * bc_step;
+#pragma unroll
+            for (int s = 0; s < kSpw; ++s) h[s] = fmaf(__builtin_amdgcn_exp2f(dt * a2[s]), h[s], dtu * o[s]);
+            if (lasts >> i & 1) h = f4{0, 0, 0, 0};
+        }
+        __syncthreads();
+    }
+    held[tiles - 1][threadIdx.x] = h;
+    for (int tile = tiles - 1; tile >= 0; --tile) {
+        stage(tile, true);
+        __syncthreads();
+        marks(tile);
+        h = held[tile][threadIdx.x];
+        f4 before[kBack], e[kBack];
+        f4 sum_c[kBack / 4], sum_b[kBack / 4];
+#pragma unroll
+        for (int i = 0; i < kBack / 4; ++i) sum_c[i] = sum_b[i] = f4{0, 0, 0, 0};
+        // adds the 64 lanes' v into row 4 (i % 4) + s of a group of four tokens
+        auto gather = [&](f4& acc, int i, int s, float v) {
+            const float one = (m.lane & 15) == (i & 3) * 4 + s ? 1.f : 0.f;
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(one, v, acc, 0, 0, 0);
+        };
+#pragma unroll
+        for (int i = 0; i < kBack; ++i) {
+            before[i] = e[i] = f4{0, 0, 0, 0};
+            if (i >= here) continue;
+            if (firsts >> i & 1) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
+            const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
+            const float* o = bc + (int64_t)(tile * kBack + i) * bc_step;
+            before[i] = h;
+            float y = 0.f;
+#pragma unroll
+            for (int s = 0; s < kSpw; ++s) {
+                e[i][s] = __builtin_amdgcn_exp2f(dt * a2[s]);
+                h[s] = fmaf(e[i][s], h[s], dtu * o[s]);
+                y = fmaf(o[4 + s], h[s], y);
+                gather(sum_c[i / 4], i, s, dy * h[s]);
+            }
+            part[2][m.wave][i][m.lane] = y;
+            if (lasts >> i & 1) h = f4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = kBack - 1; i >= 0; --i) {
+            if (i >= here) continue;
+            if (lasts >> i & 1) g = m.get(a, a.dfinal, __builtin_amdgcn_readlane(mk, i) >> 2);
+            const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
+            const float* o = bc + (int64_t)(tile * kBack + i) * bc_step;
+            float fed = 0.f, moved = 0.f;
+#pragma unroll
+            for (int s = 0; s < kSpw; ++s) {
+                g[s] = fmaf(o[4 + s], dy, g[s]);
+                gather(sum_b[i / 4], i, s, g[s] * dtu);
+                fed = fmaf(g[s], o[s], fed);
+                g[s] *= e[i][s];
+                const float q = g[s] * before[i][s];
+                da[s] = fmaf(q, dt, da[s]);
+                moved = fmaf(q, av[s], moved);
+            }
+            part[0][m.wave][i][m.lane] = fed;
+            part[1][m.wave][i][m.lane] = moved;
+            if (firsts >> i & 1) {
+                if (a.dinit) m.put(a, a.dinit, __builtin_amdgcn_readlane(mk, i) >> 2, g);
+                g = f4{0, 0, 0, 0};
+            }
+        }
+        // the first lane of 16 has db of its token, the second dc
+#pragma unroll
+        for (int i = 0; i < kBack / 4; ++i) {
+            f4 vb, vc;
+#pragma unroll
+            for (int s = 0; s < kSpw; ++s) {
+                vb[s] = row16_sum(sum_b[i][s]);
+                vc[s] = row16_sum(sum_c[i][s]);
+            }
+            const int tok = i * 4 + (m.lane >> 4), which = m.lane & 15;
+            if (which < 2 && tok < here)
+                *(f4*)(out_bc + (int64_t)(tile * kBack + tok) * bc_step + which * 4) = which ? vc : vb;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < Q::kPer; ++i) {
+            const int q = Q::of(i), in = q / 16, tok = tile * kBack + in;
+            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+            if (tok >= w.n) continue;
+            const bool real = raw[i].mark >= 0;
+            const Quad<T> u(raw[i].u), r(raw[i].dt);
+            const f4 dt = *(const f4*)&sd[in][0][quad * 4], dy = *(const f4*)&sd[in][2][quad * 4];
+            f4 fed = {0, 0, 0, 0}, moved = fed, y = fed;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                fed += *(const f4*)&part[0][k][in][quad * 4];
+                moved += *(const f4*)&part[1][k][in][quad * 4];
+                if (a.gate) y += *(const f4*)&part[2][k][in][quad * 4];
+            }
+            const int64_t row = (w.row0 + tok) * a.dim + w.c0;
+            float du[4], dd[4], dz[4];
+#pragma unroll
+            for (int e2 = 0; e2 < 4; ++e2) {
+                du[e2] = real ? fmaf(dt[e2], fed[e2], skip[e2] * dy[e2]) : 0.f;
+                float v = fmaf(u.v[e2], fed[e2], moved[e2]);
+                if (a.softplus) {
+                    const float x = r.v[e2] + bias[e2];
+                    v *= sigmoid_of(x);
+                }
+                dd[e2] = real ? v : 0.f;
+                s_bias[e2] += dd[e2];
+                s_skip[e2] = real ? fmaf(dy[e2], u.v[e2], s_skip[e2]) : s_skip[e2];
+            }
+            store_piece<T, 4>((T*)a.du + row, quad * 4, w.left, du);
+            store_piece<T, 4>((T*)a.ddt + row, quad * 4, w.left, dd);
+            if (a.gate) {
+                const Quad<T> z(raw[i].z), d(raw[i].dy);
+#pragma unroll
+                for (int e2 = 0; e2 < 4; ++e2) {
+                    const float sg = sigmoid_of(z.v[e2]);
+                    dz[e2] = real ? d.v[e2] * fmaf(skip[e2], u.v[e2], y[e2]) * (sg * fmaf(z.v[e2], 1.f - sg, 1.f)) : 0.f;
+                }
+                store_piece<T, 4>((T*)a.dgate + row, quad * 4, w.left, dz);
+            }
+        }
+        if (tile > 0) fetch(tile - 1, true);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int s = 0; s < kSpw; ++s) a.part_a[m.slot(a, w.chunk, w.block, NW, s)] = da[s];
+    // the channels' sums over the threads that had them, in order
+    constexpr int kHave = Q::kCount < Q::kThreads ? Q::kCount : Q::kThreads;
+    float* red = &part[0][0][0][0];
+    static_assert(sizeof(part) >= kHave * 8 * sizeof(float), "room for the sums");
+    if ((int)threadIdx.x < kHave) {
+        *(f4*)(red + threadIdx.x * 8) = s_skip;
+        *(f4*)(red + threadIdx.x * 8 + 4) = s_bias;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * kLanes; i += NW * 64) {
+        const int which = i / kLanes, ch = i % kLanes;
+        float v = 0.f;
+        for (int k = 0; k < kHave / 16; ++k) v += red[(k * 16 + ch / 4) * 8 + which * 4 + ch % 4];
+        if (ch < w.left) a.part_d[(w.chunk * 2 + which) * a.dim + w.c0 + ch] = v;
+    }
+}
+
+// Sums over chunks: of da (blockIdx.y 0, a column for each state of each
+// workgroup's lanes), dskip and ddt_bias. 64 columns a workgroup, 16 slices of
+// the chunks, then the slices.
+__global__ __launch_bounds__(1024) void scan_fold(Scan a, int nw, float* da, float* dskip, float* dbias)
+{
+    __shared__ float red[16][65];
+    const int c = threadIdx.x & 63, slice = threadIdx.x >> 6, which = blockIdx.y;
+    const int64_t size = (int64_t)a.blocks * nw * kSpw * kLanes, col = (int64_t)blockIdx.x * 64 + c;
+    float* out = which == 0 ? da : which == 1 ? dskip : dbias;
+    const int64_t columns = which == 0 ? size : a.dim, pitch = which == 0 ? size : 2 * (int64_t)a.dim;
+    if (!out || (int64_t)blockIdx.x * 64 >= columns) return;
+    const float* p = which == 0 ? a.part_a + col : a.part_d + (int64_t)(which - 1) * a.dim + col;
+    float s = 0.f;
+    if (col < columns) {
+        int64_t i = slice;
+        for (; i + 48 < a.chunks; i += 64) {
+            const float v0 = p[i * pitch], v1 = p[(i + 16) * pitch], v2 = p[(i + 32) * pitch], v3 = p[(i + 48) * pitch];
+            s += v0; s += v1; s += v2; s += v3;
+        }
+        for (; i < a.chunks; i += 16) s += p[i * pitch];
+    }
+    red[slice][c] = s;
+    __syncthreads();
+    if (slice != 0 || col >= columns) return;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += red[k][c];
+    if (which) {
+        out[col] = v;
+        return;
+    }
+    const int state = (int)(col / kLanes % (nw * kSpw)), block = (int)(col / kLanes / (nw * kSpw));
+    const int g = block / a.gblocks, in = (block - g * a.gblocks) * kLanes + c;
+    if (in < a.gdim && state < a.states) out[(int64_t)(g * a.gdim + in) * a.states + state] = v;
+}
+
+// db and dc: the sums over a group's workgroups. A thread: four states of a token
+// and group, of both.
+template <typename T>
+__global__ __launch_bounds__(256) void scan_fold_bc(Scan a, int nw, T* db, T* dc)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, size = a.rows * a.groups * nw;
+    if (id >= size) return;
+    f4 b = {0, 0, 0, 0}, c = b;
+    const float* p = a.part_bc + id * 8;
+    constexpr int U = 4;
+    for (int k = 0; k < a.gblocks; k += U) {
+        f4 vb[U], vc[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const f4* q = (const f4*)(p + (int64_t)min(k + i, a.gblocks - 1) * size * 8);
+            vb[i] = q[0];
+            vc[i] = q[1];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (k + i < a.gblocks) {
+                b += vb[i];
+                c += vc[i];
+            }
+    }
+    const int w = (int)(id % nw);
+    const int64_t at = id / nw * a.states + w * kSpw;
+    const bool real = a.mark[id / nw / a.groups] >= 0;
+#pragma unroll
+    for (int s = 0; s < kSpw; ++s)
+        if (w * kSpw + s < a.states) {
+            db[at + s] = (T)(real ? b[s] : 0.f);
+            dc[at + s] = (T)(real ? c[s] : 0.f);
+        }
+}
+
+// ---- one token --------------------------------------------------------------------
+
+struct Step {
+    const void *u, *dt, *b, *c, *gate;
+    const float *a, *skip, *dt_bias;
+    float* state;
+    const int32_t* slots;
+    void* y;
+    int64_t u_s, dt_s, gate_s, b_s[2], c_s[2];
+    int64_t batch, num_slots;
+    int dim, states, gdim, softplus;
+    int per;       // lanes of a channel: a power of two, four states each
+    int along;     // sequences a workgroup takes, one after another
+};
+
+// A thread: four states of a channel, for a few sequences. Bound by the states'
+// traffic.
+template <typename T>
+__global__ __launch_bounds__(256) void scan_step(Step a)
+{
+    const int lane = threadIdx.x % a.per;
+    const int blocks = (int)(((int64_t)a.dim * a.per + 255) / 256);
+    const int64_t first = (int64_t)(blockIdx.x / (unsigned)blocks) * a.along;
+    const int64_t id = (int64_t)(blockIdx.x % (unsigned)blocks) * 256 + threadIdx.x;
+    const int ch = (int)(id / a.per), s0 = lane * kSpw, g = min(ch, a.dim - 1) / a.gdim;
+    const bool live = ch < a.dim;
+    const int64_t at = (int64_t)ch * a.states + s0;
+    const int have = live ? min(kSpw, a.states - s0) : 0;
+    f4 a2 = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < kSpw; ++s)
+        if (s < have) a2[s] = a.a[at + s] * kLog2e;
+    const float skip = live && a.skip ? a.skip[ch] : 0.f, bias = live && a.dt_bias ? a.dt_bias[ch] : 0.f;
+    for (int64_t i = first; i < min(first + a.along, a.batch); ++i) {
+        const int64_t slot = a.slots ? a.slots[i] : i;
+        const bool known = slot >= 0 && slot < a.num_slots;
+        T* y = (T*)a.y + i * a.dim;
+        if (!known) {
+            if (live && lane == 0) y[ch] = (T)0.f;
+            continue;
+        }
+        float sum = 0.f, u = 0.f, z = 0.f;
+        if (have > 0) {
+            u = (float)((const T*)a.u)[i * a.u_s + ch];
+            float dt = (float)((const T*)a.dt)[i * a.dt_s + ch] + bias;
+            if (a.gate) z = (float)((const T*)a.gate)[i * a.gate_s + ch];
+            float* h = a.state + slot * a.dim * a.states + at;
+            const Packed<float, 4> old = load_piece<float, 4>(h, 0, have);
+            const Packed<T, 4> b = load_piece<T, 4>((const T*)a.b + i * a.b_s[0] + g * a.b_s[1], s0, a.states);
+            const Packed<T, 4> c = load_piece<T, 4>((const T*)a.c + i * a.c_s[0] + g * a.c_s[1], s0, a.states);
+            if (a.softplus) dt = softplus_of(dt);
+            float now[4];
+#pragma unroll
+            for (int s = 0; s < kSpw; ++s) {
+                now[s] = fmaf(__builtin_amdgcn_exp2f(dt * a2[s]), old.e[s], dt * u * (float)b.e[s]);
+                sum = s < have ? fmaf((float)c.e[s], now[s], sum) : sum;
+            }
+            store_piece<float, 4>(h, 0, have, now);
+        }
+        for (int k = a.per / 2; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
+        if (live && lane == 0) {
+            float v = fmaf(skip, u, sum);
+            if (a.gate) v *= silu_of(z);
+            y[ch] = (T)v;
+        }
+    }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+constexpr int kMaxStates = 64;
+constexpr int64_t kMaxDim = (int64_t)1 << 20;
+constexpr int64_t kMaxRows = (int64_t)1 << 31;
+
+int check_desc(const gconv_scan_desc* d)
+{
+    if (!d) return fail(GCONV_ERR_NULL, "descriptor is NULL");
+    if (d->dtype != GCONV_F32 && d->dtype != GCONV_BF16) return fail(GCONV_ERR_ARG, "unknown dtype %lld", (long long)d->dtype);
+    if (d->sequences < 0 || d->tokens < 0 || d->dim < 1 || d->states < 1 || d->groups < 1)
+        return fail(GCONV_ERR_SHAPE, "need sequences, tokens >= 0 and dim, states, groups >= 1 (got %lld, %lld, %lld, %lld, %lld)",
+                    (long long)d->sequences, (long long)d->tokens, (long long)d->dim, (long long)d->states, (long long)d->groups);
+    if (d->dim % d->groups) return fail(GCONV_ERR_GROUPS, "dim=%lld not divisible by groups=%lld", (long long)d->dim, (long long)d->groups);
+    if (d->packed && d->tokens > 0 && d->sequences == 0) return fail(GCONV_ERR_SHAPE, "tokens of no sequence");
+    if (d->states > kMaxStates) return fail(GCONV_ERR_UNSUPPORTED, "states=%lld above %d", (long long)d->states, kMaxStates);
+    if (d->dim > kMaxDim) return fail(GCONV_ERR_UNSUPPORTED, "dim=%lld above %lld", (long long)d->dim, (long long)kMaxDim);
+    if (d->sequences > ((int64_t)1 << 28) || d->tokens > ((int64_t)1 << 30) ||
+        (!d->packed && d->tokens > 0 && d->sequences > kMaxRows / d->tokens))
+        return fail(GCONV_ERR_UNSUPPORTED, "too many rows");
+    return GCONV_OK;
+}
+
+int waves_of(int64_t states)
+{
+    int nw = 1;
+    while (nw * kSpw < states) nw *= 2;
+    return nw;
+}
+
+int64_t outer_of(const gconv_scan_desc* d) { return d->packed ? 1 : d->sequences; }
+int64_t rows_of(const gconv_scan_desc* d) { return outer_of(d) * d->tokens; }
+
+struct Layout {
+    int nw;
+    size_t bc, mark, ends, adds, sums, breaks, part_a, part_d, part_bc, bytes;
+};
+
+// Workgroups of the forward pass that leave no CU without work. A sequence is
+// cut only as far as it takes to have them: each chunk is run over twice.
+constexpr int64_t kForwardBlocks = 512;
+
+void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
+{
+    l->nw = waves_of(d->states);
+    a->rows = rows_of(d);
+    a->dim = (int)d->dim;
+    a->states = (int)d->states;
+    a->groups = (int)d->groups;
+    a->gdim = a->dim / a->groups;
+    a->gblocks = (a->gdim + kLanes - 1) / kLanes;
+    a->blocks = a->groups * a->gblocks;
+    a->softplus = d->softplus != 0;
+    a->seq.tokens = d->tokens;
+    a->seq.count = (int)d->sequences;
+    int64_t chunk;
+    if (back) {
+        chunk = l->nw <= 4 ? 64 : 256 / l->nw;
+    } else {
+        const int64_t have = std::max<int64_t>(1, outer_of(d) * a->blocks);
+        const int64_t per = have * 2 > kForwardBlocks ? 1 : (kForwardBlocks + have - 1) / have;
+        chunk = std::max<int64_t>(4 * kTile, ((d->tokens + per - 1) / per + kTile - 1) / kTile * kTile);
+        chunk = std::min<int64_t>(chunk, (int64_t)1 << 30);
+    }
+    a->chunk = (int)chunk;
+    a->per = std::max<int64_t>(1, (d->tokens + chunk - 1) / chunk);
+    a->chunks = d->tokens > 0 ? outer_of(d) * a->per : 0;
+    const int64_t states = a->chunks * a->blocks * l->nw * kSpw * kLanes * 4;
+    Cut cut;
+    l->bc = cut.take(a->rows * a->groups * l->nw * 8 * 4);
+    l->mark = cut.take(a->rows * 4);
+    const bool cuts = a->per > 1;
+    l->ends = cut.take(cuts ? states : 0);
+    l->sums = cut.take(cuts ? a->chunks * a->blocks * kLanes * 4 : 0);
+    l->breaks = cut.take(cuts ? a->chunks * 4 : 0);
+    l->adds = cut.take(back && cuts ? states : 0);
+    l->part_a = cut.take(back ? states : 0);
+    l->part_d = cut.take(back ? a->chunks * 2 * a->dim * 4 : 0);
+    l->part_bc = cut.take(back ? a->rows * a->groups * l->nw * 8 * 4 * a->gblocks : 0);
+    l->bytes = cut.bytes;
+}
+
+void place(const Layout& l, void* workspace, Scan* a)
+{
+    char* w = (char*)workspace;
+    a->bc = (float*)(w + l.bc);
+    a->mark = (int32_t*)(w + l.mark);
+    a->ends = (float*)(w + l.ends);
+    a->sums = (float*)(w + l.sums);
+    a->breaks = (int32_t*)(w + l.breaks);
+    a->adds = (float*)(w + l.adds);
+    a->part_a = (float*)(w + l.part_a);
+    a->part_d = (float*)(w + l.part_d);
+    a->part_bc = (float*)(w + l.part_bc);
+}
+
+int check_blocks(const Scan& a, int nw)
+{
+    if (a.chunks > max_blocks(nw * 64) / a.blocks || a.rows * a.groups * nw / 256 >= max_blocks(256) ||
+        a.chunks / a.per * a.blocks * nw >= max_blocks(256))
+        return fail(GCONV_ERR_UNSUPPORTED, "too many rows");
+    return GCONV_OK;
+}
+
+void strides(const gconv_scan_desc* d, Scan* a)
+{
+    auto two = [&](const int64_t* s, int64_t* o) {
+        o[0] = d->packed ? 0 : s[0];
+        o[1] = s[1];
+    };
+    two(d->u_stride, a->u_s);
+    two(d->dt_stride, a->dt_s);
+    two(d->gate_stride, a->gate_s);
+    two(d->dy_stride, a->dy_s);
+    two(d->b_stride, a->b_s);
+    two(d->c_stride, a->c_s);
+    a->b_s[2] = d->b_stride[2];
+    a->c_s[2] = d->c_stride[2];
+}
+
+template <typename F>
+void by_waves(int nw, F f)
+{
+    switch (nw) {
+        case 1: f(std::integral_constant<int, 1>{}); break;
+        case 2: f(std::integral_constant<int, 2>{}); break;
+        case 4: f(std::integral_constant<int, 4>{}); break;
+        case 8: f(std::integral_constant<int, 8>{}); break;
+        default: f(std::integral_constant<int, 16>{}); break;
+    }
+}
+
+template <typename F>
+void by_type(int64_t dtype, F f)
+{
+    if (dtype == GCONV_BF16) f((__bf16)0.f);
+    else f(0.f);
+}
+
+unsigned blocks_of(int64_t threads, int per) { return (unsigned)((threads + per - 1) / per); }
+
+}  // namespace
+}  // namespace gconv
+
+using namespace gconv;
+
+extern "C" {
+
+int gconv_scan_workspace_size(const gconv_scan_desc* d, int op, size_t* bytes)
+{
+    const int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    if (op != GCONV_SCAN_FWD && op != GCONV_SCAN_BWD) return fail(GCONV_ERR_ARG, "unknown op %d", op);
+    if (!bytes) return fail(GCONV_ERR_NULL, "bytes pointer is NULL");
+    Scan a{};
+    Layout l{};
+    plan(d, op == GCONV_SCAN_BWD, &a, &l);
+    *bytes = l.bytes;
+    return GCONV_OK;
+}
+
+int gconv_scan_fwd(const gconv_scan_desc* d, const void* u, const void* dt, const float* a_, const void* b, const void* c, const float* skip,
+                   const void* gate, const float* dt_bias, const int32_t* cu_seqlens, const float* initial_state, void* y,
+                   float* final_state, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    const int64_t rows = rows_of(d), es = d->dtype == GCONV_BF16 ? 2 : 4, held = d->sequences * d->dim * d->states * 4;
+    if (!a_ || (rows > 0 && (!u || !dt || !b || !c || !y))) return fail(GCONV_ERR_NULL, "u, dt, a, b, c and y must be non-NULL");
+    if ((d->packed != 0) != (cu_seqlens != nullptr)) return fail(GCONV_ERR_NULL, "cu_seqlens must be given with packed sequences, and only then");
+    const int64_t o = outer_of(d);
+    const Span in[] = {strided_span(u, es, o, d->u_stride[0], d->tokens, d->u_stride[1], 1, 0, d->dim),
+                       strided_span(dt, es, o, d->dt_stride[0], d->tokens, d->dt_stride[1], 1, 0, d->dim),
+                       strided_span(gate, es, o, d->gate_stride[0], d->tokens, d->gate_stride[1], 1, 0, d->dim),
+                       strided_span(b, es, o, d->b_stride[0], d->tokens, d->b_stride[1], d->groups, d->b_stride[2], d->states),
+                       strided_span(c, es, o, d->c_stride[0], d->tokens, d->c_stride[1], d->groups, d->c_stride[2], d->states),
+                       {a_, d->dim * d->states * 4}, {skip, d->dim * 4}, {dt_bias, d->dim * 4}, {cu_seqlens, (d->sequences + 1) * 4},
+                       {initial_state, held}};
+    const Span out[] = {{y, rows * d->dim * es}, {final_state, held}};
+    st = check_overlap(in, out);
+    if (st != GCONV_OK) return st;
+    Scan a{};
+    Layout l{};
+    plan(d, false, &a, &l);
+    st = check_blocks(a, l.nw);
+    if (st != GCONV_OK) return st;
+    st = check_workspace(workspace, workspace_bytes, l.bytes);
+    if (st != GCONV_OK) return st;
+    place(l, workspace, &a);
+    strides(d, &a);
+    a.u = u;
+    a.dt = dt;
+    a.a = a_;
+    a.b = b;
+    a.c = c;
+    a.skip = skip;
+    a.gate = gate;
+    a.dt_bias = dt_bias;
+    a.init = initial_state;
+    a.y = y;
+    a.final_ = final_state;
+    a.seq.cu = cu_seqlens;
+    hipStream_t hs = (hipStream_t)stream;
+    (void)hipGetLastError();
+    if (final_state && d->sequences > 0 && (d->packed || d->tokens == 0))
+        scan_empty<<<(unsigned)d->sequences, 256, 0, hs>>>(a.seq, initial_state, final_state, d->dim * d->states);
+    if (rows == 0) return finish();
+    by_type(d->dtype, [&](auto t) {
+        using T = decltype(t);
+        scan_prep<T><<<blocks_of(a.rows * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw);
+        by_waves(l.nw, [&](auto n) {
+            constexpr int NW = decltype(n)::value;
+            const unsigned blocks = (unsigned)(a.chunks * a.blocks);
+            if (a.per > 1) {
+                scan_run<T, NW, false, false><<<blocks, NW * 64, 0, hs>>>(a);
+                scan_carry<<<blocks_of(a.chunks / a.per * a.blocks * NW * kSpw * kLanes, 256), 256, 0, hs>>>(a, NW, a.chunks / a.per);
+            }
+            scan_run<T, NW, true, false><<<blocks, NW * 64, 0, hs>>>(a);
+        });
+    });
+    return finish();
+}
+
+int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, const void* dt, const float* a_, const void* b, const void* c,
+                   const float* skip, const void* gate, const float* dt_bias, const int32_t* cu_seqlens, const float* initial_state,
+                   const float* d_final_state, void* du, void* ddt, float* da, void* db, void* dc, float* dskip, void* dgate,
+                   float* ddt_bias, float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    const int64_t rows = rows_of(d), es = d->dtype == GCONV_BF16 ? 2 : 4, held = d->sequences * d->dim * d->states * 4;
+    if (!a_ || !da || (rows > 0 && (!dy || !u || !dt || !b || !c || !du || !ddt || !db || !dc)))
+        return fail(GCONV_ERR_NULL, "dy, u, dt, a, b, c and their gradients must be non-NULL");
+    if ((skip != nullptr) != (dskip != nullptr)) return fail(GCONV_ERR_NULL, "skip and dskip go together");
+    if ((dt_bias != nullptr) != (ddt_bias != nullptr)) return fail(GCONV_ERR_NULL, "dt_bias and ddt_bias go together");
+    if ((gate != nullptr) != (dgate != nullptr) && rows > 0) return fail(GCONV_ERR_NULL, "gate and dgate go together");
+    if ((d->packed != 0) != (cu_seqlens != nullptr)) return fail(GCONV_ERR_NULL, "cu_seqlens must be given with packed sequences, and only then");
+    const int64_t o = outer_of(d), wide = rows * d->dim * es, narrow = rows * d->groups * d->states * es;
+    const Span in[] = {strided_span(u, es, o, d->u_stride[0], d->tokens, d->u_stride[1], 1, 0, d->dim),
+                       strided_span(dt, es, o, d->dt_stride[0], d->tokens, d->dt_stride[1], 1, 0, d->dim),
+                       strided_span(gate, es, o, d->gate_stride[0], d->tokens, d->gate_stride[1], 1, 0, d->dim),
+                       strided_span(dy, es, o, d->dy_stride[0], d->tokens, d->dy_stride[1], 1, 0, d->dim),
+                       strided_span(b, es, o, d->b_stride[0], d->tokens, d->b_stride[1], d->groups, d->b_stride[2], d->states),
+                       strided_span(c, es, o, d->c_stride[0], d->tokens, d->c_stride[1], d->groups, d->c_stride[2], d->states),
+                       {a_, d->dim * d->states * 4}, {skip, d->dim * 4}, {dt_bias, d->dim * 4}, {cu_seqlens, (d->sequences + 1) * 4},
+                       {initial_state, held}, {d_final_state, held}};
+    const Span out[] = {{du, wide}, {ddt, wide}, {dgate, wide}, {db, narrow}, {dc, narrow}, {da, d->dim * d->states * 4},
+                        {dskip, d->dim * 4}, {ddt_bias, d->dim * 4}, {d_initial_state, held}};
+    st = check_overlap(in, out);
+    if (st != GCONV_OK) return st;
+    Scan a{};
+    Layout l{};
+    plan(d, true, &a, &l);
+    st = check_blocks(a, l.nw);
+    if (st != GCONV_OK) return st;
+    st = check_workspace(workspace, workspace_bytes, l.bytes);
+    if (st != GCONV_OK) return st;
+    place(l, workspace, &a);
+    strides(d, &a);
+    a.u = u;
+    a.dt = dt;
+    a.a = a_;
+    a.b = b;
+    a.c = c;
+    a.skip = skip;
+    a.gate = gate;
+    a.dy = dy;
+    a.dt_bias = dt_bias;
+    a.init = initial_state;
+    a.dfinal = d_final_state;
+    a.du = du;
+    a.ddt = ddt;
+    a.dgate = dgate;
+    a.dinit = d_initial_state;
+    a.seq.cu = cu_seqlens;
+    hipStream_t hs = (hipStream_t)stream;
+    (void)hipGetLastError();
+    if (d_initial_state && d->sequences > 0 && (d->packed || d->tokens == 0))
+        scan_empty<<<(unsigned)d->sequences, 256, 0, hs>>>(a.seq, d_final_state, d_initial_state, d->dim * d->states);
+    by_type(d->dtype, [&](auto t) {
+        using T = decltype(t);
+        if (rows > 0) {
+            scan_prep<T><<<blocks_of(a.rows * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw);
+            by_waves(l.nw, [&](auto n) {
+                constexpr int NW = decltype(n)::value;
+                const unsigned blocks = (unsigned)(a.chunks * a.blocks);
+                if (a.per > 1) {
+                    scan_run<T, NW, false, true><<<blocks, NW * 64, 0, hs>>>(a);
+                    scan_carry<<<dim3(blocks_of(a.chunks / a.per * a.blocks * NW * kSpw * kLanes, 256), 2), 256, 0, hs>>>(a, NW, a.chunks / a.per);
+                }
+                scan_back<T, NW><<<blocks, NW * 64, 0, hs>>>(a);
+            });
+            scan_fold_bc<T><<<blocks_of(a.rows * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw, (T*)db, (T*)dc);
+        }
+    });
+    const int64_t columns = std::max<int64_t>((int64_t)a.blocks * l.nw * kSpw * kLanes, d->dim);
+    scan_fold<<<dim3(blocks_of(columns, 64), 3), 1024, 0, hs>>>(a, l.nw, da, dskip, ddt_bias);
+    return finish();
+}
+
+int gconv_scan_step(const gconv_scan_desc* d, const void* u, const void* dt, const float* a_, const void* b, const void* c,
+                    const float* skip, const void* gate, const float* dt_bias, float* state, const int32_t* slots, int64_t num_slots,
+                    void* y, void* stream)
+{
+    int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    if (d->packed || d->tokens) return fail(GCONV_ERR_ARG, "a step takes one token of each sequence: packed and tokens must be 0");
+    if (num_slots < 0) return fail(GCONV_ERR_SHAPE, "num_slots must be >= 0");
+    const int64_t es = d->dtype == GCONV_BF16 ? 2 : 4, n = d->sequences;
+    if (!a_ || (n > 0 && (!u || !dt || !b || !c || !y || (num_slots > 0 && !state))))
+        return fail(GCONV_ERR_NULL, "u, dt, a, b, c, state and y must be non-NULL");
+    if (!slots && num_slots < n) return fail(GCONV_ERR_SHAPE, "%lld sequences, %lld states", (long long)n, (long long)num_slots);
+    if (num_slots > kMaxRows) return fail(GCONV_ERR_UNSUPPORTED, "too many states");
+    const Span in[] = {strided_span(u, es, n, d->u_stride[0], 1, 0, 1, 0, d->dim), strided_span(dt, es, n, d->dt_stride[0], 1, 0, 1, 0, d->dim),
+                       strided_span(gate, es, n, d->gate_stride[0], 1, 0, 1, 0, d->dim),
+                       strided_span(b, es, n, d->b_stride[0], 1, 0, d->groups, d->b_stride[2], d->states),
+                       strided_span(c, es, n, d->c_stride[0], 1, 0, d->groups, d->c_stride[2], d->states),
+                       {a_, d->dim * d->states * 4}, {skip, d->dim * 4}, {dt_bias, d->dim * 4}, {slots, n * 4}};
+    const Span out[] = {{state, num_slots * d->dim * d->states * 4}, {y, n * d->dim * es}};
+    st = check_overlap(in, out);
+    if (st != GCONV_OK) return st;
+    (void)hipGetLastError();
+    if (n == 0) return finish();
+    Step a{};
+    a.u = u;
+    a.dt = dt;
+    a.b = b;
+    a.c = c;
+    a.gate = gate;
+    a.a = a_;
+    a.skip = skip;
+    a.dt_bias = dt_bias;
+    a.state = state;
+    a.slots = slots;
+    a.y = y;
+    a.u_s = d->u_stride[0];
+    a.dt_s = d->dt_stride[0];
+    a.gate_s = d->gate_stride[0];
+    a.b_s[0] = d->b_stride[0];
+    a.b_s[1] = d->b_stride[2];
+    a.c_s[0] = d->c_stride[0];
+    a.c_s[1] = d->c_stride[2];
+    a.batch = n;
+    a.num_slots = num_slots;
+    a.dim = (int)d->dim;
+    a.states = (int)d->states;
+    a.gdim = a.dim / (int)d->groups;
+    a.softplus = d->softplus != 0;
+    a.per = waves_of(d->states);
+    const int64_t blocks = (d->dim * a.per + 255) / 256;
+    a.along = (int)std::max<int64_t>(1, std::min<int64_t>(8, n * blocks / 2048));
+    const int64_t all = (n + a.along - 1) / a.along;
+    if (all > max_blocks(256) / blocks) return fail(GCONV_ERR_UNSUPPORTED, "too many rows");
+    by_type(d->dtype, [&](auto t) { scan_step<decltype(t)><<<(unsigned)(all * blocks), 256, 0, (hipStream_t)stream>>>(a); });
+    return finish();
+}
+
+}  // extern "C"

@@ -1,0 +1,652 @@
+// shortconv.hip -- the short causal convolution of each channel over its last
+// tokens, with its activation and the inputs that it carries on (gfx950).
+//
+//   p_t = bias + sum_j w[j] x_{t-K+1+j}       y_t = act(p_t)
+//   dp_t = dy_t act'(p_t)    dx_s = sum_i w[K-1-i] dp_{s+i}
+//   dw[j] = sum_t dp_t x_{t-K+1+j}            dbias = sum_t dp_t
+//
+// Bound by HBM: x in and y out (forward), x and dy in and dx out (backward). A
+// thread holds 16 bytes of channels and walks over a chunk of tokens with the
+// window of K inputs in registers, so each input is read once but for the K - 1
+// tokens before (and, backward, after) a chunk, which the neighbour's reads leave
+// in the cache. The backward pass computes p again rather than keep it. The
+// weights' sums are float32 in registers over a chunk, over the workgroup's
+// chunks in LDS, and over workgroups in a second kernel, each in a fixed order.
+#include "seq_host.h"
+#include "seq_tokens.h"
+
+namespace gconv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTaps = 8;
+constexpr int kAhead = 4;  // tokens whose loads are under way together
+
+struct Conv {
+    const void *x, *w, *bias, *dy, *init, *dfinal;
+    void *y, *final_, *dx, *dinit;
+    float* part;          // [blocks of chunks][taps + 1][dim]
+    Sequences seq;
+    int64_t x_seq, x_tok, dy_seq, dy_tok;
+    int64_t per;          // chunks of a stretch: one sequence, or all packed tokens
+    int64_t chunks;
+    int64_t chunk_blocks, state_blocks;
+    int chunk;            // tokens
+    int dim, act;
+    int px;               // pieces (threads) along the channels in a workgroup
+    int nx;               // workgroups along the channels
+};
+
+__device__ __forceinline__ float act_of(float p, int act)
+{
+    return act == GCONV_ACT_NONE ? p : act == GCONV_ACT_SIGMOID ? sigmoid_of(p) : p * sigmoid_of(p);
+}
+
+__device__ __forceinline__ float act_grad(float p, int act)
+{
+    if (act == GCONV_ACT_NONE) return 1.f;
+    const float s = sigmoid_of(p);
+    return act == GCONV_ACT_SIGMOID ? s * (1.f - s) : s * fmaf(p, 1.f - s, 1.f);
+}
+
+// Where a workgroup's thread works: its piece of channels and its slice.
+struct Place {
+    int col;       // first channel, >= dim: none
+    int64_t slice; // chunk, or (past chunk_blocks) sequence
+    bool state;
+};
+
+__device__ __forceinline__ Place place_of(const Conv& a, int ve)
+{
+    const int cy = kThreads / a.px, tx = threadIdx.x % a.px, ty = threadIdx.x / a.px;
+    const int64_t by = blockIdx.x / a.nx;
+    Place p;
+    p.col = ((int)(blockIdx.x % a.nx) * a.px + tx) * ve;
+    p.state = by >= a.chunk_blocks;
+    p.slice = (p.state ? by - a.chunk_blocks : by) * cy + ty;
+    return p;
+}
+
+template <typename T, int K, int V>
+struct Window {
+    float v[K > 1 ? K - 1 : 1][V];
+    // the K - 1 inputs before place `at` of sequence n, whose tokens begin at row x
+    __device__ __forceinline__ void load(const T* x, int64_t tok, int64_t at, const T* init, int col, int dim)
+    {
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) {
+            const int64_t from = at - (K - 1) + i;
+            Packed<T, V> p;
+            if (from >= 0) {
+                p = load_piece<T, V>(x + from * tok, col, dim);
+            } else if (init) {
+                p = load_piece<T, V>(init + (from + K - 1) * dim, col, dim);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) p.e[e] = (T)0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[i][e] = (float)p.e[e];
+        }
+    }
+    __device__ __forceinline__ void push(const float (&x)[V])
+    {
+#pragma unroll
+        for (int i = 0; i + 2 < K; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[i][e] = v[i + 1][e];
+        if constexpr (K > 1) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[K - 2][e] = x[e];
+        }
+    }
+};
+
+template <typename T, int K, int V>
+struct Taps {
+    float w[K][V], bias[V];
+    __device__ __forceinline__ void load(const Conv& a, int col)
+    {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const bool in = col + e < a.dim;
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j][e] = in ? (float)((const T*)a.w)[(int64_t)(col + e) * K + j] : 0.f;
+            bias[e] = in && a.bias ? (float)((const T*)a.bias)[col + e] : 0.f;
+        }
+    }
+    __device__ __forceinline__ float at(const Window<T, K, V>& win, const float (&x)[V], int e) const
+    {
+        float p = bias[e];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) p = fmaf(w[j][e], win.v[j][e], p);
+        return fmaf(w[K - 1][e], x[e], p);
+    }
+};
+
+// Calls seg(n, s0, s1, a, b) for each stretch [a, b) of the chunk's tokens that
+// lies in sequence n, whose tokens are [s0, s1), and gap(a, b) for those in none.
+// Tokens are counted from the stretch that the chunk belongs to.
+template <typename S, typename G>
+__device__ __forceinline__ void walk(const Conv& a, int64_t chunk, S seg, G gap)
+{
+    const int64_t outer = chunk / a.per, t0 = (chunk - outer * a.per) * a.chunk;
+    const int64_t t1 = min(t0 + a.chunk, a.seq.tokens);
+    if (!a.seq.cu) {
+        seg((int)outer, (int64_t)0, a.seq.tokens, t0, t1);
+        return;
+    }
+    int n = a.seq.find(t0);
+    int64_t t = t0;
+    while (t < t1) {
+        if (n < 0 || n >= a.seq.count) {
+            const int64_t e = n < 0 ? min(t1, a.seq.bound(0)) : t1;
+            if (e > t) gap(t, e);
+            t = max(t, e);
+            ++n;
+            continue;
+        }
+        const int64_t s0 = min(a.seq.bound(n), t), s1 = a.seq.bound(n + 1);
+        if (s1 <= t) {
+            ++n;
+            continue;
+        }
+        const int64_t e = min(t1, s1);
+        seg(n, s0, s1, t, e);
+        t = e;
+        ++n;
+    }
+}
+
+// Sequence n's first row and its tokens.
+template <typename T>
+__device__ __forceinline__ const T* sequence(const Conv& a, int64_t n, int64_t* len)
+{
+    if (!a.seq.cu) {
+        *len = a.seq.tokens;
+        return (const T*)a.x + n * a.x_seq;
+    }
+    const int64_t s0 = a.seq.bound((int)n), s1 = a.seq.bound((int)n + 1);
+    *len = max(s1 - s0, (int64_t)0);
+    return (const T*)a.x + s0 * a.x_tok;
+}
+
+template <typename T, int K, int V>
+__global__ __launch_bounds__(kThreads) void conv_fwd(Conv a)
+{
+    const Place p = place_of(a, V);
+    if (p.col >= a.dim) return;
+    const int64_t held = (int64_t)(K - 1) * a.dim;
+    if (p.state) {
+        // what the sequence leaves behind: its last K - 1 inputs, of the initial ones where it is shorter
+        if (p.slice >= a.seq.count) return;
+        int64_t len;
+        const T* x = sequence<T>(a, p.slice, &len);
+        Window<T, K, V> win;
+        win.load(x, a.x_tok, len, a.init ? (const T*)a.init + p.slice * held : nullptr, p.col, a.dim);
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) store_piece<T, V>((T*)a.final_ + p.slice * held + (int64_t)i * a.dim, p.col, a.dim, win.v[i]);
+        return;
+    }
+    if (p.slice >= a.chunks) return;
+    Taps<T, K, V> taps;
+    taps.load(a, p.col);
+    const int64_t outer = p.slice / a.per;
+    const T* x = (const T*)a.x + outer * a.x_seq;
+    T* y = (T*)a.y + outer * a.seq.tokens * a.dim;
+    walk(a, p.slice,
+         [&](int n, int64_t s0, int64_t, int64_t t0, int64_t t1) {
+             Window<T, K, V> win;
+             win.load(x + s0 * a.x_tok, a.x_tok, t0 - s0, a.init ? (const T*)a.init + n * held : nullptr, p.col, a.dim);
+             for (int64_t t = t0; t < t1; t += kAhead) {
+                 Packed<T, V> raw[kAhead];
+#pragma unroll
+                 for (int i = 0; i < kAhead; ++i)
+                     raw[i] = load_piece<T, V>(x + min(t + i, t1 - 1) * a.x_tok, p.col, a.dim);
+#pragma unroll
+                 for (int i = 0; i < kAhead; ++i) {
+                     if (t + i >= t1) break;
+                     float in[V], out[V];
+#pragma unroll
+                     for (int e = 0; e < V; ++e) in[e] = (float)raw[i].e[e];
+#pragma unroll
+                     for (int e = 0; e < V; ++e) out[e] = act_of(taps.at(win, in, e), a.act);
+                     store_piece<T, V>(y + (t + i) * a.dim, p.col, a.dim, out);
+                     win.push(in);
+                 }
+             }
+         },
+         [&](int64_t t0, int64_t t1) {
+             const float zero[V] = {};
+             for (int64_t t = t0; t < t1; ++t) store_piece<T, V>(y + t * a.dim, p.col, a.dim, zero);
+         });
+}
+
+template <typename T, int K, int V>
+__global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
+{
+    __shared__ float red[kThreads * V];
+    const Place p = place_of(a, V);
+    const bool live = p.col < a.dim;
+    const int64_t held = (int64_t)(K - 1) * a.dim;
+    Taps<T, K, V> taps;
+    taps.load(a, p.col);
+    if (p.state) {
+        // the initial inputs' gradient: what the first K - 1 tokens read of them, and of a short sequence what it leaves behind
+        if (!live || p.slice >= a.seq.count) return;
+        int64_t len;
+        const T* x = sequence<T>(a, p.slice, &len);
+        const T* dy = (const T*)a.dy + (a.seq.cu ? a.seq.bound((int)p.slice) * a.dy_tok : p.slice * a.dy_seq);
+        const T* init = a.init ? (const T*)a.init + p.slice * held : nullptr;
+        float g[K > 1 ? K - 1 : 1][V] = {};
+        Window<T, K, V> win;
+        win.load(x, a.x_tok, 0, init, p.col, a.dim);
+#pragma unroll
+        for (int t = 0; t < K - 1; ++t) {
+            if (t >= len) break;
+            const Packed<T, V> rx = load_piece<T, V>(x + t * a.x_tok, p.col, a.dim), rd = load_piece<T, V>(dy + t * a.dy_tok, p.col, a.dim);
+            float in[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) in[e] = (float)rx.e[e];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float dp = (float)rd.e[e] * act_grad(taps.at(win, in, e), a.act);
+#pragma unroll
+                for (int i = 0; i < K - 1; ++i)
+                    if (i >= t) g[i][e] = fmaf(taps.w[i >= t ? i - t : 0][e], dp, g[i][e]);
+            }
+            win.push(in);
+        }
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) {
+            if (i >= len && a.dfinal) {
+                const Packed<T, V> r = load_piece<T, V>((const T*)a.dfinal + p.slice * held + (i - len) * a.dim, p.col, a.dim);
+#pragma unroll
+                for (int e = 0; e < V; ++e) g[i][e] += (float)r.e[e];
+            }
+            store_piece<T, V>((T*)a.dinit + p.slice * held + (int64_t)i * a.dim, p.col, a.dim, g[i]);
+        }
+        return;
+    }
+    float dw[K][V] = {}, db[V] = {};
+    if (live && p.slice < a.chunks) {
+        const int64_t outer = p.slice / a.per;
+        const T* x = (const T*)a.x + outer * a.x_seq;
+        const T* dy = (const T*)a.dy + outer * a.dy_seq;
+        T* dx = (T*)a.dx + outer * a.seq.tokens * a.dim;
+        walk(a, p.slice,
+             [&](int n, int64_t s0, int64_t s1, int64_t t0, int64_t t1) {
+                 Window<T, K, V> win;
+                 win.load(x + s0 * a.x_tok, a.x_tok, t0 - s0, a.init ? (const T*)a.init + n * held : nullptr, p.col, a.dim);
+                 float acc[K][V] = {};  // [i]: the gradient of token t - i so far
+                 const int64_t last = min(t1 + K - 1, s1);
+                 for (int64_t t = t0; t < last; t += kAhead) {
+                     Packed<T, V> rx[kAhead], rd[kAhead];
+#pragma unroll
+                     for (int i = 0; i < kAhead; ++i) {
+                         rx[i] = load_piece<T, V>(x + min(t + i, last - 1) * a.x_tok, p.col, a.dim);
+                         rd[i] = load_piece<T, V>(dy + min(t + i, last - 1) * a.dy_tok, p.col, a.dim);
+                     }
+#pragma unroll
+                     for (int i = 0; i < kAhead; ++i) {
+                         if (t + i >= last) break;
+                         const bool mine = t + i < t1;
+                         float in[V];
+#pragma unroll
+                         for (int e = 0; e < V; ++e) in[e] = (float)rx[i].e[e];
+#pragma unroll
+                         for (int e = 0; e < V; ++e) {
+                             const float dp = (float)rd[i].e[e] * act_grad(taps.at(win, in, e), a.act);
+#pragma unroll
+                             for (int j = 0; j < K; ++j) acc[j][e] = fmaf(taps.w[K - 1 - j][e], dp, acc[j][e]);
+                             if (mine) {
+#pragma unroll
+                                 for (int j = 0; j < K - 1; ++j) dw[j][e] = fmaf(dp, win.v[j][e], dw[j][e]);
+                                 dw[K - 1][e] = fmaf(dp, in[e], dw[K - 1][e]);
+                                 db[e] += dp;
+                             }
+                         }
+                         if (t + i - (K - 1) >= t0) store_piece<T, V>(dx + (t + i - (K - 1)) * a.dim, p.col, a.dim, acc[K - 1]);
+#pragma unroll
+                         for (int j = K - 1; j > 0; --j)
+#pragma unroll
+                             for (int e = 0; e < V; ++e) acc[j][e] = acc[j - 1][e];
+#pragma unroll
+                         for (int e = 0; e < V; ++e) acc[0][e] = 0.f;
+                         win.push(in);
+                     }
+                 }
+                 // the sequence's last tokens, which fewer read and which it leaves behind
+                 if (last == s1) {
+#pragma unroll
+                     for (int i = K - 1; i > 0; --i) {
+                         const int64_t t = last - i;
+                         if (t < t0 || t >= t1) continue;
+                         if (a.dfinal) {
+                             const Packed<T, V> r = load_piece<T, V>((const T*)a.dfinal + n * held + (int64_t)(K - 1 - i) * a.dim, p.col, a.dim);
+#pragma unroll
+                             for (int e = 0; e < V; ++e) acc[i][e] += (float)r.e[e];
+                         }
+                         store_piece<T, V>(dx + t * a.dim, p.col, a.dim, acc[i]);
+                     }
+                 }
+             },
+             [&](int64_t t0, int64_t t1) {
+                 const float zero[V] = {};
+                 for (int64_t t = t0; t < t1; ++t) store_piece<T, V>(dx + t * a.dim, p.col, a.dim, zero);
+             });
+    }
+    // the workgroup's chunks, in order
+    const int cy = kThreads / a.px, tx = threadIdx.x % a.px, ty = threadIdx.x / a.px;
+    float* part = a.part + (int64_t)(blockIdx.x / a.nx) * (K + 1) * a.dim;
+    auto columns = [&](const float (&v)[V], int row) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < V; ++e) red[(ty * a.px + tx) * V + e] = v[e];
+        __syncthreads();
+        if (ty == 0 && live) {
+            float s[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[e] = red[tx * V + e];
+            for (int q = 1; q < cy; ++q)
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[e] += red[(q * a.px + tx) * V + e];
+            store_piece<float, V>(part + (int64_t)row * a.dim, p.col, a.dim, s);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < K; ++j) columns(dw[j], j);
+    if (a.bias) columns(db, K);
+}
+
+// dw[col][row] (or dbias[col], row == taps) = sum over `count` partial rows: 64
+// columns a workgroup, 16 slices of the rows, then the slices.
+template <typename T>
+__global__ __launch_bounds__(1024) void conv_fold(const float* part, int64_t count, int taps, int dim, T* dw, T* dbias)
+{
+    __shared__ float red[16][65];
+    const int c = threadIdx.x & 63, slice = threadIdx.x >> 6;
+    const int col = blockIdx.x * 64 + c, row = blockIdx.y;
+    const int64_t pitch = (int64_t)(taps + 1) * dim;
+    const float* p = part + (int64_t)row * dim + col;
+    float s = 0.f;
+    if (col < dim) {
+        int64_t i = slice;
+        for (; i + 48 < count; i += 64) {
+            const float v0 = p[i * pitch], v1 = p[(i + 16) * pitch], v2 = p[(i + 32) * pitch], v3 = p[(i + 48) * pitch];
+            s += v0; s += v1; s += v2; s += v3;
+        }
+        for (; i < count; i += 16) s += p[i * pitch];
+    }
+    red[slice][c] = s;
+    __syncthreads();
+    if (slice == 0 && col < dim) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v += red[k][c];
+        if (row < taps) dw[(int64_t)col * taps + row] = (T)v;
+        else dbias[col] = (T)v;
+    }
+}
+
+struct Step {
+    const void *x, *w, *bias;
+    void *state, *y;
+    const int32_t* slots;
+    int64_t x_stride, num_slots, batch;
+    int dim, act;
+};
+
+// One token of each sequence: the state moves up by one input, in place.
+template <typename T, int K, int V>
+__global__ __launch_bounds__(kThreads) void conv_step(Step a)
+{
+    const int pieces = (a.dim + V - 1) / V;
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x, i = id / pieces;
+    if (i >= a.batch) return;
+    const int col = (int)(id - i * pieces) * V;
+    T* y = (T*)a.y + i * a.dim;
+    const int64_t slot = a.slots ? a.slots[i] : i;
+    if (slot < 0 || slot >= a.num_slots) {
+        const float zero[V] = {};
+        store_piece<T, V>(y, col, a.dim, zero);
+        return;
+    }
+    Conv c{};
+    c.w = a.w;
+    c.bias = a.bias;
+    c.dim = a.dim;
+    T* state = (T*)a.state + slot * (K - 1) * a.dim;
+    Window<T, K, V> win;
+    win.load(state, a.dim, K - 1, nullptr, col, a.dim);
+    const Packed<T, V> raw = load_piece<T, V>((const T*)a.x + i * a.x_stride, col, a.dim);
+    Taps<T, K, V> taps;
+    taps.load(c, col);
+    float in[V], out[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) in[e] = (float)raw.e[e];
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = act_of(taps.at(win, in, e), a.act);
+    store_piece<T, V>(y, col, a.dim, out);
+    win.push(in);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) store_piece<T, V>(state + (int64_t)j * a.dim, col, a.dim, win.v[j]);
+}
+
+// ---- host ------------------------------------------------------------------------
+
+constexpr int64_t kMaxDim = (int64_t)1 << 24;
+constexpr int64_t kMaxRows = (int64_t)1 << 40;
+
+int check_desc(const gconv_shortconv_desc* d)
+{
+    if (!d) return fail(GCONV_ERR_NULL, "descriptor is NULL");
+    if (d->dtype != GCONV_F32 && d->dtype != GCONV_BF16) return fail(GCONV_ERR_ARG, "unknown dtype %lld", (long long)d->dtype);
+    if (d->act < GCONV_ACT_NONE || d->act > GCONV_ACT_SILU) return fail(GCONV_ERR_ARG, "unknown activation %lld", (long long)d->act);
+    if (d->sequences < 0 || d->tokens < 0 || d->dim < 1 || d->taps < 1)
+        return fail(GCONV_ERR_SHAPE, "need sequences, tokens >= 0 and dim, taps >= 1 (got %lld, %lld, %lld, %lld)",
+                    (long long)d->sequences, (long long)d->tokens, (long long)d->dim, (long long)d->taps);
+    if (d->packed && d->tokens > 0 && d->sequences == 0) return fail(GCONV_ERR_SHAPE, "tokens of no sequence");
+    if (d->taps > kMaxTaps) return fail(GCONV_ERR_UNSUPPORTED, "taps=%lld above %d", (long long)d->taps, kMaxTaps);
+    if (d->dim > kMaxDim) return fail(GCONV_ERR_UNSUPPORTED, "dim=%lld above %lld", (long long)d->dim, (long long)kMaxDim);
+    if (d->sequences > ((int64_t)1 << 30) || d->tokens > ((int64_t)1 << 30) ||
+        (!d->packed && d->tokens > 0 && d->sequences > kMaxRows / d->tokens))
+        return fail(GCONV_ERR_UNSUPPORTED, "too many rows");
+    return GCONV_OK;
+}
+
+int64_t outer_of(const gconv_shortconv_desc* d) { return d->packed ? 1 : d->sequences; }
+int64_t rows_of(const gconv_shortconv_desc* d) { return outer_of(d) * d->tokens; }
+
+// Channels a thread holds: 16 bytes, half of that where more than four taps of bf16 would not fit the registers.
+int piece_of(const gconv_shortconv_desc* d) { return d->dtype == GCONV_BF16 && d->taps <= 4 ? 8 : 4; }
+
+// The launch: as long chunks as leave enough threads (a chunk's first K - 1
+// tokens are read by two).
+void plan(const gconv_shortconv_desc* d, bool states, int longest, Conv* a)
+{
+    const int64_t pieces = (d->dim + piece_of(d) - 1) / piece_of(d);
+    int px = 1;
+    while (px < 64 && px < pieces) px *= 2;
+    a->px = px;
+    a->nx = (int)((pieces + px - 1) / px);
+    int chunk = longest;
+    while (chunk > 4 && pieces * outer_of(d) * ((d->tokens + chunk - 1) / chunk) < (int64_t)1 << 17) chunk /= 2;
+    a->chunk = chunk;
+    a->per = std::max<int64_t>(1, (d->tokens + chunk - 1) / chunk);
+    a->chunks = d->tokens > 0 ? outer_of(d) * a->per : 0;
+    const int cy = kThreads / px;
+    a->chunk_blocks = (a->chunks + cy - 1) / cy;
+    a->state_blocks = states ? (d->sequences + cy - 1) / cy : 0;
+    a->dim = (int)d->dim;
+    a->act = (int)d->act;
+    a->seq.tokens = d->tokens;
+    a->seq.count = (int)d->sequences;
+    a->x_seq = d->packed ? 0 : d->x_stride[0];
+    a->x_tok = d->x_stride[1];
+    a->dy_seq = d->packed ? 0 : d->dy_stride[0];
+    a->dy_tok = d->dy_stride[1];
+}
+
+constexpr int kFwdChunk = 64, kBwdChunk = 64;
+
+int check_blocks(const Conv& a)
+{
+    const int64_t blocks = (a.chunk_blocks + a.state_blocks) * a.nx;
+    return blocks > max_blocks(kThreads) ? fail(GCONV_ERR_UNSUPPORTED, "too many rows") : GCONV_OK;
+}
+
+template <typename T, int V, typename F>
+void by_taps(int taps, F f)
+{
+    switch (taps) {
+        case 1: f(std::integral_constant<int, 1>{}); break;
+        case 2: f(std::integral_constant<int, 2>{}); break;
+        case 3: f(std::integral_constant<int, 3>{}); break;
+        case 4: f(std::integral_constant<int, 4>{}); break;
+        case 5: f(std::integral_constant<int, 5>{}); break;
+        case 6: f(std::integral_constant<int, 6>{}); break;
+        case 7: f(std::integral_constant<int, 7>{}); break;
+        default: f(std::integral_constant<int, 8>{}); break;
+    }
+}
+
+// f(type, taps, channels a thread) for the descriptor's.
+template <typename F>
+void by_kind(const gconv_shortconv_desc* d, F f)
+{
+    if (d->dtype == GCONV_F32) by_taps<float, 4>((int)d->taps, [&](auto k) { f(0.f, k, std::integral_constant<int, 4>{}); });
+    else
+        by_taps<__bf16, 8>((int)d->taps, [&](auto k) {
+            f((__bf16)0.f, k, std::integral_constant<int, (decltype(k)::value <= 4 ? 8 : 4)>{});
+        });
+}
+
+}  // namespace
+}  // namespace gconv
+
+using namespace gconv;
+
+extern "C" {
+
+int gconv_shortconv_workspace_size(const gconv_shortconv_desc* d, size_t* bytes)
+{
+    const int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    if (!bytes) return fail(GCONV_ERR_NULL, "bytes pointer is NULL");
+    Conv a{};
+    plan(d, true, kBwdChunk, &a);
+    *bytes = (size_t)a.chunk_blocks * (d->taps + 1) * d->dim * 4;
+    return GCONV_OK;
+}
+
+int gconv_shortconv_fwd(const gconv_shortconv_desc* d, const void* x, const void* w, const void* bias, const int32_t* cu_seqlens,
+                        const void* initial_state, void* y, void* final_state, void* stream)
+{
+    int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    const int64_t rows = rows_of(d), es = d->dtype == GCONV_BF16 ? 2 : 4, held = d->sequences * (d->taps - 1) * d->dim * es;
+    if (!w || (rows > 0 && (!x || !y))) return fail(GCONV_ERR_NULL, "x, w and y must be non-NULL");
+    if ((d->packed != 0) != (cu_seqlens != nullptr)) return fail(GCONV_ERR_NULL, "cu_seqlens must be given with packed sequences, and only then");
+    const Span in[] = {strided_span(x, es, outer_of(d), d->x_stride[0], d->tokens, d->x_stride[1], 1, 0, d->dim), {w, d->dim * d->taps * es},
+                       {bias, d->dim * es}, {cu_seqlens, (d->sequences + 1) * 4}, {initial_state, held}};
+    const Span out[] = {{y, rows * d->dim * es}, {final_state, held}};
+    st = check_overlap(in, out);
+    if (st != GCONV_OK) return st;
+    Conv a{};
+    plan(d, final_state && d->taps > 1, kFwdChunk, &a);
+    st = check_blocks(a);
+    if (st != GCONV_OK) return st;
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.init = initial_state;
+    a.y = y;
+    a.final_ = final_state;
+    a.seq.cu = cu_seqlens;
+    (void)hipGetLastError();
+    const int64_t blocks = (a.chunk_blocks + a.state_blocks) * a.nx;
+    if (blocks > 0)
+        by_kind(d, [&](auto t, auto k, auto v) {
+            conv_fwd<decltype(t), decltype(k)::value, decltype(v)::value><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a);
+        });
+    return finish();
+}
+
+int gconv_shortconv_bwd(const gconv_shortconv_desc* d, const void* dy, const void* x, const void* w, const void* bias,
+                        const int32_t* cu_seqlens, const void* initial_state, const void* d_final_state, void* dx, void* dw, void* dbias,
+                        void* d_initial_state, void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    const int64_t rows = rows_of(d), es = d->dtype == GCONV_BF16 ? 2 : 4, held = d->sequences * (d->taps - 1) * d->dim * es;
+    if (!w || !dw || (rows > 0 && (!dy || !x || !dx))) return fail(GCONV_ERR_NULL, "dy, x, w, dx and dw must be non-NULL");
+    if ((bias != nullptr) != (dbias != nullptr)) return fail(GCONV_ERR_NULL, "bias and dbias go together");
+    if ((d->packed != 0) != (cu_seqlens != nullptr)) return fail(GCONV_ERR_NULL, "cu_seqlens must be given with packed sequences, and only then");
+    const Span in[] = {strided_span(x, es, outer_of(d), d->x_stride[0], d->tokens, d->x_stride[1], 1, 0, d->dim),
+                       strided_span(dy, es, outer_of(d), d->dy_stride[0], d->tokens, d->dy_stride[1], 1, 0, d->dim),
+                       {w, d->dim * d->taps * es}, {bias, d->dim * es}, {cu_seqlens, (d->sequences + 1) * 4}, {initial_state, held},
+                       {d_final_state, held}};
+    const Span out[] = {{dx, rows * d->dim * es}, {dw, d->dim * d->taps * es}, {dbias, d->dim * es}, {d_initial_state, held}};
+    st = check_overlap(in, out);
+    if (st != GCONV_OK) return st;
+    Conv a{};
+    plan(d, d_initial_state && d->taps > 1, kBwdChunk, &a);
+    st = check_blocks(a);
+    if (st != GCONV_OK) return st;
+    st = check_workspace(workspace, workspace_bytes, (size_t)a.chunk_blocks * (d->taps + 1) * d->dim * 4);
+    if (st != GCONV_OK) return st;
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.dy = dy;
+    a.init = initial_state;
+    a.dfinal = d_final_state;
+    a.dx = dx;
+    a.dinit = d_initial_state;
+    a.part = (float*)workspace;
+    a.seq.cu = cu_seqlens;
+    (void)hipGetLastError();
+    hipStream_t hs = (hipStream_t)stream;
+    const int64_t blocks = (a.chunk_blocks + a.state_blocks) * a.nx;
+    if (blocks > 0)
+        by_kind(d, [&](auto t, auto k, auto v) {
+            conv_bwd<decltype(t), decltype(k)::value, decltype(v)::value><<<(unsigned)blocks, kThreads, 0, hs>>>(a);
+        });
+    const dim3 grid((unsigned)((d->dim + 63) / 64), (unsigned)d->taps + (bias ? 1 : 0));
+    if (d->dtype == GCONV_BF16) conv_fold<__bf16><<<grid, 1024, 0, hs>>>(a.part, a.chunk_blocks, (int)d->taps, a.dim, (__bf16*)dw, (__bf16*)dbias);
+    else conv_fold<float><<<grid, 1024, 0, hs>>>(a.part, a.chunk_blocks, (int)d->taps, a.dim, (float*)dw, (float*)dbias);
+    return finish();
+}
+
+int gconv_shortconv_step(const gconv_shortconv_desc* d, const void* x, const void* w, const void* bias, void* state, const int32_t* slots,
+                         int64_t num_slots, void* y, void* stream)
+{
+    int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    if (d->packed || d->tokens) return fail(GCONV_ERR_ARG, "a step takes one token of each sequence: packed and tokens must be 0");
+    if (num_slots < 0) return fail(GCONV_ERR_SHAPE, "num_slots must be >= 0");
+    const int64_t es = d->dtype == GCONV_BF16 ? 2 : 4;
+    const bool held = d->taps > 1 && num_slots > 0;
+    if (!w || (d->sequences > 0 && (!x || !y || (held && !state)))) return fail(GCONV_ERR_NULL, "x, w, state and y must be non-NULL");
+    if (!slots && num_slots < d->sequences) return fail(GCONV_ERR_SHAPE, "%lld sequences, %lld states", (long long)d->sequences, (long long)num_slots);
+    if (num_slots > kMaxRows) return fail(GCONV_ERR_UNSUPPORTED, "too many states");
+    const Span in[] = {strided_span(x, es, d->sequences, d->x_stride[0], 1, 0, 1, 0, d->dim), {w, d->dim * d->taps * es}, {bias, d->dim * es},
+                       {slots, d->sequences * 4}};
+    const Span out[] = {{state, num_slots * (d->taps - 1) * d->dim * es}, {y, d->sequences * d->dim * es}};
+    st = check_overlap(in, out);
+    if (st != GCONV_OK) return st;
+    const int v = piece_of(d);
+    const int64_t threads = d->sequences * ((d->dim + v - 1) / v), blocks = (threads + kThreads - 1) / kThreads;
+    if (blocks > max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many rows");
+    (void)hipGetLastError();
+    if (blocks > 0) {
+        const Step a{x, w, bias, state, y, slots, d->x_stride[0], num_slots, d->sequences, (int)d->dim, (int)d->act};
+        by_kind(d, [&](auto t, auto k, auto vv) {
+            conv_step<decltype(t), decltype(k)::value, decltype(vv)::value><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a);
+        });
+    }
+    return finish();
+}
+
+}  // extern "C"

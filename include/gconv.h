@@ -430,6 +430,112 @@ int gconv_orthogonalize_workspace_size(const gconv_ortho_desc* d, size_t* bytes)
 int gconv_orthogonalize(const gconv_ortho_desc* d, const void* u, void* out, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/*
+ * The short causal convolution of each channel over its last `taps` tokens:
+ *
+ *   y_t = act(bias + sum_j w[.][j] x_{t-taps+1+j})
+ *
+ * x, y [sequences, tokens, dim] (x with strides in elements, [0] between
+ * sequences, [1] between tokens, the last axis contiguous; y dense), w
+ * [dim, taps], bias [dim] or NULL, all of one type. The taps - 1 inputs before
+ * a sequence's first are initial_state [sequences, taps - 1, dim] (NULL: 0),
+ * the oldest first; final_state (may be NULL) is the last taps - 1 inputs of
+ * initial_state and sequence together. Packed sequences as in linear
+ * attention. taps 1 to 8, dim up to 2^24.
+ */
+typedef struct gconv_shortconv_desc {
+    int64_t dtype;              /* gconv_dtype of every tensor, weight and state */
+    int64_t packed;
+    int64_t sequences, tokens;
+    int64_t dim, taps;
+    int64_t act;                /* gconv_act */
+    int64_t x_stride[2];
+    int64_t dy_stride[2];       /* read by gconv_shortconv_bwd only */
+} gconv_shortconv_desc;
+
+/* Bytes of workspace gconv_shortconv_bwd needs, 16-byte aligned (the forward pass needs none). */
+int gconv_shortconv_workspace_size(const gconv_shortconv_desc* d, size_t* bytes);
+
+int gconv_shortconv_fwd(const gconv_shortconv_desc* d, const void* x, const void* w, const void* bias, const int32_t* cu_seqlens,
+                        const void* initial_state, void* y, void* final_state, void* stream);
+
+/*
+ * Gradients for dy of y and d_final_state of the final state (NULL: 0): dx
+ * (dense), dw, dbias (given exactly when bias is) and d_initial_state (may be
+ * NULL). The weights' are summed over all tokens in float32 and rounded once.
+ */
+int gconv_shortconv_bwd(const gconv_shortconv_desc* d, const void* dy, const void* x, const void* w, const void* bias,
+                        const int32_t* cu_seqlens, const void* initial_state, const void* d_final_state, void* dx, void* dw, void* dbias,
+                        void* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token x [sequences, dim] of each sequence (packed and tokens are 0), in
+ * place on a pool of states [num_slots, taps - 1, dim]; slots as in
+ * gconv_linattn_step. Strides [1] are not read.
+ */
+int gconv_shortconv_step(const gconv_shortconv_desc* d, const void* x, const void* w, const void* bias, void* state, const int32_t* slots,
+                         int64_t num_slots, void* y, void* stream);
+
+/*
+ * The selective state space scan: a recurrence of `states` numbers for each
+ * channel, whose decay and inputs depend on the token.
+ *
+ *   s_t = softplus(dt_t + dt_bias)      (s_t = dt_t + dt_bias without softplus)
+ *   h_t = exp(s_t a) h_{t-1} + s_t u_t b_t
+ *   y_t = (c_t . h_t + skip u_t) silu(gate_t)
+ *
+ * u, dt, gate, y [sequences, tokens, dim]; b, c [sequences, tokens, groups,
+ * states], shared by the dim / groups channels of a group; strides in elements
+ * ([0] between sequences, [1] between tokens, [2] between groups, the last
+ * axis contiguous), outputs dense. a [dim, states], skip, dt_bias [dim]
+ * float32. gate, skip and dt_bias may be NULL (1, 0 and 0 in their place).
+ * States [sequences, dim, states] float32, dense; initial_state (NULL: 0) and
+ * final_state may be NULL. Packed sequences as in linear attention. states up
+ * to 64, dim up to 2^20, 2^31 tokens of all sequences together (2^30 of one).
+ */
+typedef struct gconv_scan_desc {
+    int64_t dtype;              /* gconv_dtype of u, dt, b, c, gate, y and their gradients */
+    int64_t packed;
+    int64_t sequences, tokens;
+    int64_t dim, states, groups;
+    int64_t softplus;
+    int64_t u_stride[2], dt_stride[2], gate_stride[2];
+    int64_t b_stride[3], c_stride[3];
+    int64_t dy_stride[2];       /* read by gconv_scan_bwd only */
+} gconv_scan_desc;
+
+typedef enum gconv_scan_op {
+    GCONV_SCAN_FWD = 0,
+    GCONV_SCAN_BWD = 1
+} gconv_scan_op;
+
+/* Bytes of workspace `op` (a gconv_scan_op) needs, 16-byte aligned. */
+int gconv_scan_workspace_size(const gconv_scan_desc* d, int op, size_t* bytes);
+
+int gconv_scan_fwd(const gconv_scan_desc* d, const void* u, const void* dt, const float* a, const void* b, const void* c, const float* skip,
+                   const void* gate, const float* dt_bias, const int32_t* cu_seqlens, const float* initial_state, void* y,
+                   float* final_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients for dy of y and d_final_state of the final state (NULL: 0): du,
+ * ddt, db, dc, dgate of the inputs' type, dense; da, dskip, ddt_bias summed
+ * over all tokens in float32; d_initial_state may be NULL. dskip, dgate and
+ * ddt_bias are given exactly when their inputs are.
+ */
+int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, const void* dt, const float* a, const void* b, const void* c,
+                   const float* skip, const void* gate, const float* dt_bias, const int32_t* cu_seqlens, const float* initial_state,
+                   const float* d_final_state, void* du, void* ddt, float* da, void* db, void* dc, float* dskip, void* dgate,
+                   float* ddt_bias, float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of each sequence (packed and tokens are 0), in place on a pool of
+ * states [num_slots, dim, states]; slots as in gconv_linattn_step. Strides [1]
+ * are not read.
+ */
+int gconv_scan_step(const gconv_scan_desc* d, const void* u, const void* dt, const float* a, const void* b, const void* c,
+                    const float* skip, const void* gate, const float* dt_bias, float* state, const int32_t* slots, int64_t num_slots,
+                    void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
