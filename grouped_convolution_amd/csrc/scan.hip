@@ -31,6 +31,7 @@
 //
 // Tokens carry marks (first or last of a sequence, or of none), made beforehand
 // with b and c in float32, four states of one wave side by side.
+#include "device_util.h"
 #include "seq_host.h"
 #include "seq_tokens.h"
 
@@ -52,16 +53,17 @@ struct Scan {
     float *final_, *dinit;
     Sequences seq;
     int64_t u_s[2], dt_s[2], gate_s[2], dy_s[2], b_s[3], c_s[3];
-    float* bc;          // [rows][groups][NW][8]: four of b, four of c
-    int32_t* mark;      // [rows]
+    float* bc;          // [groups][NW][places][8]: four of b, four of c
+    int32_t* mark;      // [places]
     float* ends;        // [chunks][blocks][NW][4][64]: states; later those before each chunk
     float* adds;        // the same of the adjoint; later that after each chunk
     float* sums;        // [chunks][blocks][64]: sum of dt
     int32_t* breaks;    // [chunks]: whether a sequence begins in it
     float* part_a;      // [chunks][blocks][NW][4][64]: of da
     float* part_d;      // [chunks][2][dim]: of dskip and ddt_bias
-    float* part_bc;     // [blocks of a group][rows][groups][NW][8]: of db and dc
+    float* part_bc;     // [blocks of a group][groups][NW][places][8]: of db and dc
     int64_t rows;       // tokens of all sequences
+    int64_t pad, places;  // of a stretch and of all: its tokens up to a whole tile, those past its end like tokens of none
     int64_t per, chunks;  // chunks of a stretch (a sequence, or all packed tokens), of all
     int chunk;          // tokens
     int dim, states, groups;
@@ -78,6 +80,7 @@ struct Where {
     int64_t t0;            // first token, in its stretch
     int n;                 // tokens
     int64_t row0;          // first token, of all
+    int64_t place0;        // its place in the workspace
 };
 
 __device__ __forceinline__ Where where(const Scan& a)
@@ -93,6 +96,7 @@ __device__ __forceinline__ Where where(const Scan& a)
     w.t0 = (w.chunk - w.outer * a.per) * a.chunk;
     w.n = (int)min((int64_t)a.chunk, a.seq.tokens - w.t0);
     w.row0 = w.outer * a.seq.tokens + w.t0;
+    w.place0 = w.outer * a.pad + w.t0;
     return w;
 }
 
@@ -124,23 +128,21 @@ template <typename T>
 __global__ __launch_bounds__(256) void scan_prep(Scan a, int nw)
 {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int per = a.groups * nw;
-    const int64_t row = id / per;
-    if (row >= a.rows) return;
-    const int k = (int)(id - row * per), g = k / nw, w = k - g * nw;
-    int n, mark = 0;
-    int64_t outer = 0, t = row;
-    if (!a.seq.cu) {
-        outer = row / a.seq.tokens;
-        t = row - outer * a.seq.tokens;
-        n = (int)outer;
+    const int64_t k = id / a.places, place = id - k * a.places;
+    const int g = (int)k / nw, w = (int)k - g * nw;
+    if (g >= a.groups) return;
+    const int64_t outer = place / a.pad, t = place - outer * a.pad;
+    int n = (int)outer, mark = 0;
+    if (t >= a.seq.tokens) {
+        n = -1;
+    } else if (!a.seq.cu) {
         mark = (t == 0 ? FIRST : 0) | (t == a.seq.tokens - 1 ? LAST : 0);
     } else {
-        n = a.seq.find(row);
+        n = a.seq.find(t);
         if (n < 0 || n >= a.seq.count) n = -1;
-        else mark = (row == a.seq.bound(n) ? FIRST : 0) | (row == a.seq.bound(n + 1) - 1 ? LAST : 0);
+        else mark = (t == a.seq.bound(n) ? FIRST : 0) | (t == a.seq.bound(n + 1) - 1 ? LAST : 0);
     }
-    if (k == 0) a.mark[row] = n < 0 ? -1 : n * 4 + mark;
+    if (k == 0) a.mark[place] = n < 0 ? -1 : n * 4 + mark;
     f4 b = {0, 0, 0, 0}, c = {0, 0, 0, 0};
     if (n >= 0) {
         const T* pb = (const T*)a.b + outer * a.b_s[0] + t * a.b_s[1] + g * a.b_s[2];
@@ -161,19 +163,22 @@ __global__ __launch_bounds__(256) void scan_prep(Scan a, int nw)
 // gradients likewise.
 __global__ __launch_bounds__(256) void scan_empty(Sequences seq, const float* from, float* to, int64_t size)
 {
-    const int n = blockIdx.x;
-    if (seq.cu ? seq.bound(n + 1) > seq.bound(n) : seq.tokens > 0) return;
-    for (int64_t i = threadIdx.x; i < size; i += 256) to[n * size + i] = from ? from[n * size + i] : 0.f;
+    const int64_t n = blockIdx.x;
+    if (seq.cu ? seq.bound((int)n + 1) > seq.bound((int)n) : seq.tokens > 0) return;
+    for (int64_t i = blockIdx.y * 256 + threadIdx.x; i < size; i += gridDim.y * 256) to[n * size + i] = from ? from[n * size + i] : 0.f;
 }
 
 // ---- parts that the kernels share -------------------------------------------------
+
+// Read-only while the kernel runs, at an address that is the same for a wave: scalar loads.
+typedef const __attribute__((address_space(4))) float* scalar_floats;
 
 // The states of lane's channel that its wave holds.
 struct Mine {
     int lane, wave;
     int ch;         // channel, clamped to one that exists
     bool live;
-    int64_t at;     // element of [dim][states]
+    int at;         // element of [dim][states]
     int have;       // states that exist, of kSpw
     template <int NW>
     __device__ __forceinline__ static Mine of(const Scan& a, const Where& w)
@@ -183,28 +188,28 @@ struct Mine {
         m.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         m.live = m.lane < w.left;
         m.ch = w.c0 + (m.live ? m.lane : 0);
-        m.at = (int64_t)m.ch * a.states + m.wave * kSpw;
+        m.at = m.ch * a.states + m.wave * kSpw;
         m.have = m.live ? max(0, min(kSpw, a.states - m.wave * kSpw)) : 0;
         return m;
     }
-    // p[n][dim][states] of sequence n, or 0
+    // p[n][dim][states] of sequence n, or 0: no branches, a state that does not
+    // exist is read (and written) past the resource's end
+    __device__ __forceinline__ uint32_t offset(int s) const { return s < have ? (uint32_t)(at + s) * 4 : kOOB; }
     __device__ __forceinline__ f4 get(const Scan& a, const float* p, int64_t n) const
     {
-        f4 v = {0, 0, 0, 0};
-        if (p) {
-            const float* q = p + n * a.dim * a.states + at;
+        const int64_t size = (int64_t)a.dim * a.states;
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(p + (p ? n * size : 0), p ? (uint32_t)size * 4 : 0);
+        f4 v;
 #pragma unroll
-            for (int s = 0; s < kSpw; ++s)
-                if (s < have) v[s] = q[s];
-        }
+        for (int s = 0; s < kSpw; ++s) v[s] = load_f32(r, offset(s));
         return v;
     }
     __device__ __forceinline__ void put(const Scan& a, float* p, int64_t n, f4 v) const
     {
-        float* q = p + n * a.dim * a.states + at;
+        const int64_t size = (int64_t)a.dim * a.states;
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(p + (p ? n * size : 0), p ? (uint32_t)size * 4 : 0);
 #pragma unroll
-        for (int s = 0; s < kSpw; ++s)
-            if (s < have) q[s] = v[s];
+        for (int s = 0; s < kSpw; ++s) store_f32(r, offset(s), v[s]);
     }
     // index into `ends` and its like, of state s
     __device__ __forceinline__ int64_t slot(const Scan& a, int64_t chunk, int block, int nw, int s) const
@@ -224,7 +229,19 @@ struct Quads {
 template <typename T>
 __device__ __forceinline__ Packed<T, 4> load_quad(const void* p, const int64_t* stride, const Where& w, int64_t t, int quad)
 {
-    return load_piece<T, 4>((const T*)p + w.outer * stride[0] + t * stride[1] + w.c0, quad * 4, w.left);
+    const T* row = (const T*)p + w.outer * stride[0] + t * stride[1] + w.c0;
+    if (w.left == kLanes) return *(const Packed<T, 4>*)(row + quad * 4);  // (the same for the whole workgroup)
+    return load_piece<T, 4>(row, quad * 4, w.left);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_quad(const Where& w, T* row, int quad, const float (&v)[4])
+{
+    if (w.left == kLanes) {
+        *(Packed<T, 4>*)(row + quad * 4) = Packed<T, 4>{{(T)v[0], (T)v[1], (T)v[2], (T)v[3]}};
+        return;
+    }
+    store_piece<T, 4>(row, quad * 4, w.left, v);
 }
 
 // dt and dt u of a quad of channels; 0 for a token of no sequence.
@@ -313,7 +330,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         for (int i = 0; i < Q::kPer; ++i) {
             const int q = Q::of(i), tok = tile * kTile + q / 16;
             if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
-            const bool real = tok < w.n && a.mark[w.row0 + min(tok, w.n - 1)] >= 0;
+            const bool real = a.mark[w.place0 + tok] >= 0;
             f4 dt, dtu;
             step_sizes<T>(a, bias, raw[i].dt, raw[i].u, real, &dt, &dtu);
             float(*row)[kLanes] = sd[tile & 1][q / 16];
@@ -329,8 +346,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         }
     };
     const int tiles = (w.n + kTile - 1) / kTile;
-    const float* bc = a.bc + ((w.row0 * a.groups + w.g) * NW + m.wave) * 8;
-    const int64_t bc_step = (int64_t)a.groups * NW * 8;
+    const scalar_floats bc = (scalar_floats)(a.bc + ((w.g * NW + m.wave) * a.places + w.place0) * 8);
     fetch(0);
     stage(0);
     __syncthreads();
@@ -342,18 +358,17 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         if (tile < tiles) {
             // marks of the tile, a token a lane
             const int tok = tile * kTile + (m.lane & (kTile - 1));
-            const int mk = tok < w.n ? a.mark[w.row0 + tok] : -1;
+            const int mk = a.mark[w.place0 + tok];
             const uint32_t firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kTile) - 1);
             const uint32_t lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kTile) - 1);
-            const int here = min(kTile, w.n - tile * kTile);
-            auto token = [&](int i, bool marks) {
-                if (marks && (firsts >> i & 1)) {
+            auto token = [&](int i, auto marked) {
+                if (decltype(marked)::value && (firsts >> i & 1)) {
                     h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
                     p = f4{0, 0, 0, 0};
                     broken = 1;
                 }
                 const float dt = sd[tile & 1][i][0][m.lane], dtu = sd[tile & 1][i][1][m.lane];
-                const float* o = bc + (int64_t)(tile * kTile + i) * bc_step;
+                const scalar_floats o = bc + (tile * kTile + i) * 8;
                 float y = 0.f, dy = 0.f;
                 if (ADJ) dy = sd[tile & 1][i][kW - 1][m.lane];
                 if (!OUT) total += dt;
@@ -368,18 +383,20 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
                     }
                 }
                 if (OUT) yp[tile & 1][OUT ? m.wave : 0][OUT ? i : 0][m.lane] = y;
-                if (marks && (lasts >> i & 1)) {
+                if (decltype(marked)::value && (lasts >> i & 1)) {
                     const int n = __builtin_amdgcn_readlane(mk, i) >> 2;
                     if (OUT && a.final_) m.put(a, a.final_, n, h);
                     if (ADJ && a.dfinal) r += p * m.get(a, a.dfinal, n);
                     h = f4{0, 0, 0, 0};
                 }
             };
-            if (here == kTile && (firsts | lasts) == 0) {
-#pragma unroll 4
-                for (int i = 0; i < kTile; ++i) token(i, false);
+            // (without marks the tokens are one stretch of code, whose loads are all under way early)
+            if ((firsts | lasts) == 0) {
+#pragma unroll
+                for (int i = 0; i < kTile; ++i) token(i, std::false_type{});
             } else {
-                for (int i = 0; i < here; ++i) token(i, true);
+#pragma unroll 1
+                for (int i = 0; i < kTile; ++i) token(i, std::true_type{});
             }
         }
         if (OUT && tile > 0) {
@@ -400,11 +417,11 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] *= silu_of(z.v[e]);
                 }
-                const bool real = a.mark[w.row0 + tok] >= 0;
+                const bool real = a.mark[w.place0 + tok] >= 0;
                 float o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = real ? v[e] : 0.f;
-                store_piece<T, 4>((T*)a.y + (w.row0 + tok) * a.dim + w.c0, quad * 4, w.left, o);
+                store_quad<T>(w, (T*)a.y + (w.row0 + tok) * a.dim + w.c0, quad, o);
             }
         }
         if (tile + 1 < tiles) stage(tile + 1);
@@ -520,7 +537,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         for (int i = 0; i < Q::kPer; ++i) {
             const int q = Q::of(i), tok = min(tile * kBack + q / 16, w.n - 1);
             if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
-            raw[i].mark = a.mark[w.row0 + tok];
+            raw[i].mark = a.mark[w.place0 + tile * kBack + q / 16];
             raw[i].u = load_quad<T>(a.u, a.u_s, w, w.t0 + tok, quad);
             raw[i].dt = load_quad<T>(a.dt, a.dt_s, w, w.t0 + tok, quad);
             if (!all) continue;
@@ -531,9 +548,9 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
     auto stage = [&](int tile, bool all) {
 #pragma unroll
         for (int i = 0; i < Q::kPer; ++i) {
-            const int q = Q::of(i), tok = tile * kBack + q / 16;
+            const int q = Q::of(i);
             if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
-            const bool real = tok < w.n && raw[i].mark >= 0;
+            const bool real = raw[i].mark >= 0;
             f4 dt, dtu;
             step_sizes<T>(a, bias, raw[i].dt, raw[i].u, real, &dt, &dtu);
             float(*row)[kLanes] = sd[q / 16];
@@ -543,18 +560,23 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         }
     };
     const int tiles = (w.n + kBack - 1) / kBack;
-    const float* bc = a.bc + ((w.row0 * a.groups + w.g) * NW + m.wave) * 8;
-    const int64_t bc_step = (int64_t)a.groups * NW * 8;
-    float* out_bc = a.part_bc + (((int64_t)w.gb * a.rows + w.row0) * a.groups + w.g) * NW * 8 + m.wave * 8;
+    const scalar_floats bc = (scalar_floats)(a.bc + ((w.g * NW + m.wave) * a.places + w.place0) * 8);
+    float* out_bc = a.part_bc + ((((int64_t)w.gb * a.groups + w.g) * NW + m.wave) * a.places + w.place0) * 8;
 
-    int mk = -1, here = 0;
+    // [r]: a matrix with ones in row r; kept as values (as conditions they take twice the scalar registers there are)
+    float ones[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        ones[r] = (m.lane & 15) == r ? 1.f : 0.f;
+        asm volatile("" : "+v"(ones[r]));
+    }
+    int mk = -1;
     uint32_t firsts = 0, lasts = 0;
     auto marks = [&](int tile) {
         const int tok = tile * kBack + (m.lane & (kBack - 1));
-        mk = tok < w.n ? a.mark[w.row0 + tok] : -1;
+        mk = a.mark[w.place0 + tok];
         firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kBack) - 1);
         lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kBack) - 1);
-        here = min(kBack, w.n - tile * kBack);
     };
     fetch(0, tiles == 1);
     for (int tile = 0; tile + 1 < tiles; ++tile) {
@@ -563,14 +585,20 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         __syncthreads();
         fetch(tile + 1, tile + 2 == tiles);
         marks(tile);
-#pragma unroll
-        for (int i = 0; i < kBack; ++i) {
-            if (firsts >> i & 1) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
+        auto token = [&](int i, auto marked) {
+            if (decltype(marked)::value && (firsts >> i & 1)) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
             const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane];
-            const float* o = bc + (int64_t)(tile * kBack + i) * bc_step;
+            const scalar_floats o = bc + (tile * kBack + i) * 8;
 #pragma unroll
             for (int s = 0; s < kSpw; ++s) h[s] = fmaf(__builtin_amdgcn_exp2f(dt * a2[s]), h[s], dtu * o[s]);
-            if (lasts >> i & 1) h = f4{0, 0, 0, 0};
+            if (decltype(marked)::value && (lasts >> i & 1)) h = f4{0, 0, 0, 0};
+        };
+        if ((firsts | lasts) == 0) {
+#pragma unroll
+            for (int i = 0; i < kBack; ++i) token(i, std::false_type{});
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < kBack; ++i) token(i, std::true_type{});
         }
         __syncthreads();
     }
@@ -580,58 +608,58 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         __syncthreads();
         marks(tile);
         h = held[tile][threadIdx.x];
-        f4 before[kBack], e[kBack];
         f4 sum_c[kBack / 4], sum_b[kBack / 4];
 #pragma unroll
         for (int i = 0; i < kBack / 4; ++i) sum_c[i] = sum_b[i] = f4{0, 0, 0, 0};
         // adds the 64 lanes' v into row 4 (i % 4) + s of a group of four tokens
         auto gather = [&](f4& acc, int i, int s, float v) {
-            const float one = (m.lane & 15) == (i & 3) * 4 + s ? 1.f : 0.f;
-            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(one, v, acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(ones[(i & 3) * 4 + s], v, acc, 0, 0, 0);
         };
+        auto tokens = [&](auto marked) {
+            f4 before[kBack], e[kBack];
 #pragma unroll
-        for (int i = 0; i < kBack; ++i) {
-            before[i] = e[i] = f4{0, 0, 0, 0};
-            if (i >= here) continue;
-            if (firsts >> i & 1) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
-            const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
-            const float* o = bc + (int64_t)(tile * kBack + i) * bc_step;
-            before[i] = h;
-            float y = 0.f;
+            for (int i = 0; i < kBack; ++i) {
+                if (decltype(marked)::value && (firsts >> i & 1)) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
+                const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
+                const scalar_floats o = bc + (tile * kBack + i) * 8;
+                before[i] = h;
+                float y = 0.f;
 #pragma unroll
-            for (int s = 0; s < kSpw; ++s) {
-                e[i][s] = __builtin_amdgcn_exp2f(dt * a2[s]);
-                h[s] = fmaf(e[i][s], h[s], dtu * o[s]);
-                y = fmaf(o[4 + s], h[s], y);
-                gather(sum_c[i / 4], i, s, dy * h[s]);
+                for (int s = 0; s < kSpw; ++s) {
+                    e[i][s] = __builtin_amdgcn_exp2f(dt * a2[s]);
+                    h[s] = fmaf(e[i][s], h[s], dtu * o[s]);
+                    y = fmaf(o[4 + s], h[s], y);
+                    gather(sum_c[i / 4], i, s, dy * h[s]);
+                }
+                part[2][m.wave][i][m.lane] = y;
+                if (decltype(marked)::value && (lasts >> i & 1)) h = f4{0, 0, 0, 0};
             }
-            part[2][m.wave][i][m.lane] = y;
-            if (lasts >> i & 1) h = f4{0, 0, 0, 0};
-        }
 #pragma unroll
-        for (int i = kBack - 1; i >= 0; --i) {
-            if (i >= here) continue;
-            if (lasts >> i & 1) g = m.get(a, a.dfinal, __builtin_amdgcn_readlane(mk, i) >> 2);
-            const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
-            const float* o = bc + (int64_t)(tile * kBack + i) * bc_step;
-            float fed = 0.f, moved = 0.f;
+            for (int i = kBack - 1; i >= 0; --i) {
+                if (decltype(marked)::value && (lasts >> i & 1)) g = m.get(a, a.dfinal, __builtin_amdgcn_readlane(mk, i) >> 2);
+                const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
+                const scalar_floats o = bc + (tile * kBack + i) * 8;
+                float fed = 0.f, moved = 0.f;
 #pragma unroll
-            for (int s = 0; s < kSpw; ++s) {
-                g[s] = fmaf(o[4 + s], dy, g[s]);
-                gather(sum_b[i / 4], i, s, g[s] * dtu);
-                fed = fmaf(g[s], o[s], fed);
-                g[s] *= e[i][s];
-                const float q = g[s] * before[i][s];
-                da[s] = fmaf(q, dt, da[s]);
-                moved = fmaf(q, av[s], moved);
+                for (int s = 0; s < kSpw; ++s) {
+                    g[s] = fmaf(o[4 + s], dy, g[s]);
+                    gather(sum_b[i / 4], i, s, g[s] * dtu);
+                    fed = fmaf(g[s], o[s], fed);
+                    g[s] *= e[i][s];
+                    const float q = g[s] * before[i][s];
+                    da[s] = fmaf(q, dt, da[s]);
+                    moved = fmaf(q, av[s], moved);
+                }
+                part[0][m.wave][i][m.lane] = fed;
+                part[1][m.wave][i][m.lane] = moved;
+                if (decltype(marked)::value && (firsts >> i & 1)) {
+                    if (a.dinit) m.put(a, a.dinit, __builtin_amdgcn_readlane(mk, i) >> 2, g);
+                    g = f4{0, 0, 0, 0};
+                }
             }
-            part[0][m.wave][i][m.lane] = fed;
-            part[1][m.wave][i][m.lane] = moved;
-            if (firsts >> i & 1) {
-                if (a.dinit) m.put(a, a.dinit, __builtin_amdgcn_readlane(mk, i) >> 2, g);
-                g = f4{0, 0, 0, 0};
-            }
-        }
+        };
+        if ((firsts | lasts) == 0) tokens(std::false_type{});
+        else tokens(std::true_type{});
         // the first lane of 16 has db of its token, the second dc
 #pragma unroll
         for (int i = 0; i < kBack / 4; ++i) {
@@ -641,9 +669,8 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                 vb[s] = row16_sum(sum_b[i][s]);
                 vc[s] = row16_sum(sum_c[i][s]);
             }
-            const int tok = i * 4 + (m.lane >> 4), which = m.lane & 15;
-            if (which < 2 && tok < here)
-                *(f4*)(out_bc + (int64_t)(tile * kBack + tok) * bc_step + which * 4) = which ? vc : vb;
+            const int tok = tile * kBack + i * 4 + (m.lane >> 4), which = m.lane & 15;
+            if (which < 2) *(f4*)(out_bc + tok * 8 + which * 4) = which ? vc : vb;
         }
         __syncthreads();
 #pragma unroll
@@ -675,8 +702,8 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                 s_bias[e2] += dd[e2];
                 s_skip[e2] = real ? fmaf(dy[e2], u.v[e2], s_skip[e2]) : s_skip[e2];
             }
-            store_piece<T, 4>((T*)a.du + row, quad * 4, w.left, du);
-            store_piece<T, 4>((T*)a.ddt + row, quad * 4, w.left, dd);
+            store_quad<T>(w, (T*)a.du + row, quad, du);
+            store_quad<T>(w, (T*)a.ddt + row, quad, dd);
             if (a.gate) {
                 const Quad<T> z(raw[i].z), d(raw[i].dy);
 #pragma unroll
@@ -684,7 +711,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                     const float sg = sigmoid_of(z.v[e2]);
                     dz[e2] = real ? d.v[e2] * fmaf(skip[e2], u.v[e2], y[e2]) * (sg * fmaf(z.v[e2], 1.f - sg, 1.f)) : 0.f;
                 }
-                store_piece<T, 4>((T*)a.dgate + row, quad * 4, w.left, dz);
+                store_quad<T>(w, (T*)a.dgate + row, quad, dz);
             }
         }
         if (tile > 0) fetch(tile - 1, true);
@@ -750,29 +777,30 @@ __global__ __launch_bounds__(1024) void scan_fold(Scan a, int nw, float* da, flo
 template <typename T>
 __global__ __launch_bounds__(256) void scan_fold_bc(Scan a, int nw, T* db, T* dc)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, size = a.rows * a.groups * nw;
-    if (id >= size) return;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, size = a.places * a.groups * nw;
+    const int64_t k = id / a.places, place = id - k * a.places, outer = place / a.pad, t = place - outer * a.pad;
+    if (id >= size || t >= a.seq.tokens) return;
+    const int w = (int)k % nw;
     f4 b = {0, 0, 0, 0}, c = b;
     const float* p = a.part_bc + id * 8;
     constexpr int U = 4;
-    for (int k = 0; k < a.gblocks; k += U) {
+    for (int i0 = 0; i0 < a.gblocks; i0 += U) {
         f4 vb[U], vc[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const f4* q = (const f4*)(p + (int64_t)min(k + i, a.gblocks - 1) * size * 8);
+            const f4* q = (const f4*)(p + (int64_t)min(i0 + i, a.gblocks - 1) * size * 8);
             vb[i] = q[0];
             vc[i] = q[1];
         }
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (k + i < a.gblocks) {
+            if (i0 + i < a.gblocks) {
                 b += vb[i];
                 c += vc[i];
             }
     }
-    const int w = (int)(id % nw);
-    const int64_t at = id / nw * a.states + w * kSpw;
-    const bool real = a.mark[id / nw / a.groups] >= 0;
+    const int64_t at = ((outer * a.seq.tokens + t) * a.groups + k / nw) * a.states + w * kSpw;
+    const bool real = a.mark[place] >= 0;
 #pragma unroll
     for (int s = 0; s < kSpw; ++s)
         if (w * kSpw + s < a.states) {
@@ -852,7 +880,7 @@ __global__ __launch_bounds__(256) void scan_step(Step a)
 // ---- host ------------------------------------------------------------------------
 
 constexpr int kMaxStates = 64;
-constexpr int64_t kMaxDim = (int64_t)1 << 20;
+constexpr int64_t kMaxDim = (int64_t)1 << 20;  // (times 64 states of 4 bytes: a sequence's states stay below 2^31 bytes)
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
 
 int check_desc(const gconv_scan_desc* d)
@@ -916,10 +944,12 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
     a->chunk = (int)chunk;
     a->per = std::max<int64_t>(1, (d->tokens + chunk - 1) / chunk);
     a->chunks = d->tokens > 0 ? outer_of(d) * a->per : 0;
+    a->pad = (d->tokens + kTile - 1) / kTile * kTile;
+    a->places = outer_of(d) * a->pad;
     const int64_t states = a->chunks * a->blocks * l->nw * kSpw * kLanes * 4;
     Cut cut;
-    l->bc = cut.take(a->rows * a->groups * l->nw * 8 * 4);
-    l->mark = cut.take(a->rows * 4);
+    l->bc = cut.take(a->places * a->groups * l->nw * 8 * 4);
+    l->mark = cut.take(a->places * 4);
     const bool cuts = a->per > 1;
     l->ends = cut.take(cuts ? states : 0);
     l->sums = cut.take(cuts ? a->chunks * a->blocks * kLanes * 4 : 0);
@@ -927,7 +957,7 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
     l->adds = cut.take(back && cuts ? states : 0);
     l->part_a = cut.take(back ? states : 0);
     l->part_d = cut.take(back ? a->chunks * 2 * a->dim * 4 : 0);
-    l->part_bc = cut.take(back ? a->rows * a->groups * l->nw * 8 * 4 * a->gblocks : 0);
+    l->part_bc = cut.take(back ? a->places * a->groups * l->nw * 8 * 4 * a->gblocks : 0);
     l->bytes = cut.bytes;
 }
 
@@ -947,7 +977,7 @@ void place(const Layout& l, void* workspace, Scan* a)
 
 int check_blocks(const Scan& a, int nw)
 {
-    if (a.chunks > max_blocks(nw * 64) / a.blocks || a.rows * a.groups * nw / 256 >= max_blocks(256) ||
+    if (a.chunks > max_blocks(nw * 64) / a.blocks || a.places > max_blocks(256) / (a.groups * nw) * 256 ||
         a.chunks / a.per * a.blocks * nw >= max_blocks(256))
         return fail(GCONV_ERR_UNSUPPORTED, "too many rows");
     return GCONV_OK;
@@ -1054,11 +1084,11 @@ int gconv_scan_fwd(const gconv_scan_desc* d, const void* u, const void* dt, cons
     hipStream_t hs = (hipStream_t)stream;
     (void)hipGetLastError();
     if (final_state && d->sequences > 0 && (d->packed || d->tokens == 0))
-        scan_empty<<<(unsigned)d->sequences, 256, 0, hs>>>(a.seq, initial_state, final_state, d->dim * d->states);
+        scan_empty<<<dim3((unsigned)d->sequences, (unsigned)std::min<int64_t>(64, (d->dim * d->states + 255) / 256)), 256, 0, hs>>>(a.seq, initial_state, final_state, d->dim * d->states);
     if (rows == 0) return finish();
     by_type(d->dtype, [&](auto t) {
         using T = decltype(t);
-        scan_prep<T><<<blocks_of(a.rows * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw);
+        scan_prep<T><<<blocks_of(a.places * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw);
         by_waves(l.nw, [&](auto n) {
             constexpr int NW = decltype(n)::value;
             const unsigned blocks = (unsigned)(a.chunks * a.blocks);
@@ -1127,11 +1157,11 @@ int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, cons
     hipStream_t hs = (hipStream_t)stream;
     (void)hipGetLastError();
     if (d_initial_state && d->sequences > 0 && (d->packed || d->tokens == 0))
-        scan_empty<<<(unsigned)d->sequences, 256, 0, hs>>>(a.seq, d_final_state, d_initial_state, d->dim * d->states);
+        scan_empty<<<dim3((unsigned)d->sequences, (unsigned)std::min<int64_t>(64, (d->dim * d->states + 255) / 256)), 256, 0, hs>>>(a.seq, d_final_state, d_initial_state, d->dim * d->states);
     by_type(d->dtype, [&](auto t) {
         using T = decltype(t);
         if (rows > 0) {
-            scan_prep<T><<<blocks_of(a.rows * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw);
+            scan_prep<T><<<blocks_of(a.places * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw);
             by_waves(l.nw, [&](auto n) {
                 constexpr int NW = decltype(n)::value;
                 const unsigned blocks = (unsigned)(a.chunks * a.blocks);
@@ -1141,7 +1171,7 @@ int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, cons
                 }
                 scan_back<T, NW><<<blocks, NW * 64, 0, hs>>>(a);
             });
-            scan_fold_bc<T><<<blocks_of(a.rows * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw, (T*)db, (T*)dc);
+            scan_fold_bc<T><<<blocks_of(a.places * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw, (T*)db, (T*)dc);
         }
     });
     const int64_t columns = std::max<int64_t>((int64_t)a.blocks * l.nw * kSpw * kLanes, d->dim);
