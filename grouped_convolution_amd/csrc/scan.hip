@@ -42,7 +42,7 @@ constexpr int kLanes = 64;   // channels of a workgroup
 constexpr int kSpw = 4;      // states of a wave
 constexpr int kTile = 16;    // tokens passed through LDS at once
 constexpr int kBack = 8;     // the same, of the backward pass
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 enum { FIRST = 1, LAST = 2 };  // marks of a token; the sequence's number is above them, a token of none is -1
 
@@ -105,8 +105,8 @@ __device__ __forceinline__ Where where(const Scan& a)
 // small w is.
 __device__ __forceinline__ float softplus_of(float x)
 {
-    const float w = __expf(-fabsf(x)), v = 1.f + w, d = v - 1.f;
-    const float l = d == 0.f ? w : __logf(v) * (w * __builtin_amdgcn_rcpf(d));
+    const float w = __builtin_amdgcn_exp2f(fabsf(x) * -kLog2e), v = 1.f + w, d = v - 1.f;
+    const float l = d == 0.f ? w : __builtin_amdgcn_logf(v) * (kLn2 * w) * __builtin_amdgcn_rcpf(d);
     return fmaxf(x, 0.f) + l;
 }
 
@@ -270,7 +270,9 @@ __device__ __forceinline__ f4 channel_quad(const float* p, const Where& w, int q
     return v;
 }
 
-__device__ __forceinline__ float silu_of(float z) { return z * sigmoid_of(z); }
+// (arguments so large that the exponential leaves float32's range give 0 or 1)
+__device__ __forceinline__ float sigm(float z) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -kLog2e)); }
+__device__ __forceinline__ float silu_of(float z) { return z * sigm(z); }
 
 // dy' of a quad of channels; 0 for a token of no sequence.
 template <typename T>
@@ -509,15 +511,27 @@ constexpr int back_chunk()
 template <typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
 {
-    using Q = Quads<T, NW, kBack>;
-    constexpr int kTiles = back_chunk<NW>() / kBack;
+    constexpr int kTiles = back_chunk<NW>() / kBack, kThreads = NW * 64;
+    // A thread's pieces of a tile: V channels of a token.
+    constexpr int V = NW <= 2 ? 4 : NW == 4 ? 2 : 1, kRow = kLanes / V, kPieces = kBack * kRow;
+    constexpr int kPer = (kPieces + kThreads - 1) / kThreads;
     __shared__ float sd[kBack][3][kLanes];            // dt, dt u, dy'
     __shared__ float part[3][NW][kBack][kLanes];      // of s, the sum of a m, and y
     __shared__ f4 held[kTiles][NW * 64];
+    typedef float fv __attribute__((ext_vector_type(V)));
     const Where w = where(a);
     const Mine m = Mine::of<NW>(a, w);
-    const int quad = threadIdx.x & 15;
-    const f4 bias = channel_quad(a.dt_bias, w, quad), skip = channel_quad(a.skip, w, quad);
+    const int col = (threadIdx.x % kRow) * V;          // channel of the workgroup's
+    const int in0 = threadIdx.x / kRow;                // token of the tile, of the thread's first piece
+    const bool works = (int)threadIdx.x < kPieces, whole = w.left == kLanes;
+    fv bias, skip, s_skip, s_bias;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const bool in = col + e < w.left;
+        bias[e] = in && a.dt_bias ? a.dt_bias[w.c0 + col + e] : 0.f;
+        skip[e] = in && a.skip ? a.skip[w.c0 + col + e] : 0.f;
+        s_skip[e] = s_bias[e] = 0.f;
+    }
     const f4 av = m.get(a, a.a, 0), a2 = av * kLog2e;
     f4 h = {0, 0, 0, 0}, g = {0, 0, 0, 0}, da = {0, 0, 0, 0};
     if (a.per > 1) {
@@ -527,36 +541,57 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
             g[s] = a.adds[m.slot(a, w.chunk, w.block, NW, s)];
         }
     }
-    f4 s_skip = {0, 0, 0, 0}, s_bias = {0, 0, 0, 0};
     struct Raw {
-        Packed<T, 4> u, dt, z, dy;
+        Packed<T, V> u, dt, z, dy;
         int mark;
-    } raw[Q::kPer];
-    auto fetch = [&](int tile, bool all) {
+    };
+    Raw raw[kPer], next[kPer];
+    // Rows of the thread's first piece; the workgroup's are as far on for every tile.
+    auto first = [&](const void* p, const int64_t* stride) {
+        return (const T*)p + w.outer * stride[0] + (w.t0 + in0) * stride[1] + w.c0 + col;
+    };
+    const T *pu = first(a.u, a.u_s), *pdt = first(a.dt, a.dt_s), *pz = a.gate ? first(a.gate, a.gate_s) : nullptr, *pdy = first(a.dy, a.dy_s);
+    auto load = [&](const T* p, int64_t step, int tok) {
+        const T* q = p + (tok - in0) * step;
+        if (whole) return *(const Packed<T, V>*)q;
+        return load_piece<T, V>(q - col, col, w.left);
+    };
+    auto fetch = [&](Raw (&to)[kPer], int tile, bool all) {
 #pragma unroll
-        for (int i = 0; i < Q::kPer; ++i) {
-            const int q = Q::of(i), tok = min(tile * kBack + q / 16, w.n - 1);
-            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
-            raw[i].mark = a.mark[w.place0 + tile * kBack + q / 16];
-            raw[i].u = load_quad<T>(a.u, a.u_s, w, w.t0 + tok, quad);
-            raw[i].dt = load_quad<T>(a.dt, a.dt_s, w, w.t0 + tok, quad);
+        for (int i = 0; i < kPer; ++i) {
+            const int in = in0 + i * (kThreads / kRow), tok = tile * kBack + in;
+            to[i].mark = -1;
+            if (!works || tok >= w.n) continue;
+            to[i].mark = a.mark[w.place0 + tok];
+            to[i].u = load(pu, a.u_s[1], tok);
+            to[i].dt = load(pdt, a.dt_s[1], tok);
             if (!all) continue;
-            if (a.gate) raw[i].z = load_quad<T>(a.gate, a.gate_s, w, w.t0 + tok, quad);
-            raw[i].dy = load_quad<T>(a.dy, a.dy_s, w, w.t0 + tok, quad);
+            if (a.gate) to[i].z = load(pz, a.gate_s[1], tok);
+            to[i].dy = load(pdy, a.dy_s[1], tok);
         }
     };
-    auto stage = [&](int tile, bool all) {
+    auto stage = [&](bool all) {
+        if (!works) return;
 #pragma unroll
-        for (int i = 0; i < Q::kPer; ++i) {
-            const int q = Q::of(i);
-            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+        for (int i = 0; i < kPer; ++i) {
             const bool real = raw[i].mark >= 0;
-            f4 dt, dtu;
-            step_sizes<T>(a, bias, raw[i].dt, raw[i].u, real, &dt, &dtu);
-            float(*row)[kLanes] = sd[q / 16];
-            *(f4*)&row[0][quad * 4] = dt;
-            *(f4*)&row[1][quad * 4] = dtu;
-            if (all) *(f4*)&row[2][quad * 4] = gated<T>(a, raw[i].dy, raw[i].z, real);
+            float(*row)[kLanes] = sd[in0 + i * (kThreads / kRow)];
+            fv dt, dtu, dy;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float v = (float)raw[i].dt.e[e] + bias[e];
+                if (a.softplus) v = softplus_of(v);
+                dt[e] = real ? v : 0.f;
+                dtu[e] = real ? v * (float)raw[i].u.e[e] : 0.f;
+                if (all) {
+                    float y = (float)raw[i].dy.e[e];
+                    if (a.gate) y *= silu_of((float)raw[i].z.e[e]);
+                    dy[e] = real ? y : 0.f;
+                }
+            }
+            *(fv*)&row[0][col] = dt;
+            *(fv*)&row[1][col] = dtu;
+            if (all) *(fv*)&row[2][col] = dy;
         }
     };
     const int tiles = (w.n + kBack - 1) / kBack;
@@ -578,12 +613,12 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kBack) - 1);
         lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kBack) - 1);
     };
-    fetch(0, tiles == 1);
+    fetch(raw, 0, tiles == 1);
     for (int tile = 0; tile + 1 < tiles; ++tile) {
         held[tile][threadIdx.x] = h;
-        stage(tile, false);
+        stage(false);
         __syncthreads();
-        fetch(tile + 1, tile + 2 == tiles);
+        fetch(raw, tile + 1, tile + 2 == tiles);
         marks(tile);
         auto token = [&](int i, auto marked) {
             if (decltype(marked)::value && (firsts >> i & 1)) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
@@ -604,8 +639,9 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
     }
     held[tiles - 1][threadIdx.x] = h;
     for (int tile = tiles - 1; tile >= 0; --tile) {
-        stage(tile, true);
+        stage(true);
         __syncthreads();
+        if (tile > 0) fetch(next, tile - 1, true);
         marks(tile);
         h = held[tile][threadIdx.x];
         f4 sum_c[kBack / 4], sum_b[kBack / 4];
@@ -673,65 +709,75 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
             if (which < 2) *(f4*)(out_bc + tok * 8 + which * 4) = which ? vc : vb;
         }
         __syncthreads();
+        if (works) {
 #pragma unroll
-        for (int i = 0; i < Q::kPer; ++i) {
-            const int q = Q::of(i), in = q / 16, tok = tile * kBack + in;
-            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
-            if (tok >= w.n) continue;
-            const bool real = raw[i].mark >= 0;
-            const Quad<T> u(raw[i].u), r(raw[i].dt);
-            const f4 dt = *(const f4*)&sd[in][0][quad * 4], dy = *(const f4*)&sd[in][2][quad * 4];
-            f4 fed = {0, 0, 0, 0}, moved = fed, y = fed;
+            for (int i = 0; i < kPer; ++i) {
+                const int in = in0 + i * (kThreads / kRow), tok = tile * kBack + in;
+                if (tok >= w.n) continue;
+                const bool real = raw[i].mark >= 0;
+                const fv dt = *(const fv*)&sd[in][0][col], dy = *(const fv*)&sd[in][2][col];
+                fv fed = *(const fv*)&part[0][0][in][col], moved = *(const fv*)&part[1][0][in][col], y = {};
 #pragma unroll
-            for (int k = 0; k < NW; ++k) {
-                fed += *(const f4*)&part[0][k][in][quad * 4];
-                moved += *(const f4*)&part[1][k][in][quad * 4];
-                if (a.gate) y += *(const f4*)&part[2][k][in][quad * 4];
-            }
-            const int64_t row = (w.row0 + tok) * a.dim + w.c0;
-            float du[4], dd[4], dz[4];
-#pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2) {
-                du[e2] = real ? fmaf(dt[e2], fed[e2], skip[e2] * dy[e2]) : 0.f;
-                float v = fmaf(u.v[e2], fed[e2], moved[e2]);
-                if (a.softplus) {
-                    const float x = r.v[e2] + bias[e2];
-                    v *= sigmoid_of(x);
+                for (int k = 1; k < NW; ++k) {
+                    fed += *(const fv*)&part[0][k][in][col];
+                    moved += *(const fv*)&part[1][k][in][col];
                 }
-                dd[e2] = real ? v : 0.f;
-                s_bias[e2] += dd[e2];
-                s_skip[e2] = real ? fmaf(dy[e2], u.v[e2], s_skip[e2]) : s_skip[e2];
-            }
-            store_quad<T>(w, (T*)a.du + row, quad, du);
-            store_quad<T>(w, (T*)a.ddt + row, quad, dd);
-            if (a.gate) {
-                const Quad<T> z(raw[i].z), d(raw[i].dy);
+                const int64_t row = (w.row0 + tok) * a.dim + w.c0;
+                float du[V], dd[V], dz[V];
 #pragma unroll
-                for (int e2 = 0; e2 < 4; ++e2) {
-                    const float sg = sigmoid_of(z.v[e2]);
-                    dz[e2] = real ? d.v[e2] * fmaf(skip[e2], u.v[e2], y[e2]) * (sg * fmaf(z.v[e2], 1.f - sg, 1.f)) : 0.f;
+                for (int e = 0; e < V; ++e) {
+                    const float u = (float)raw[i].u.e[e];
+                    du[e] = real ? fmaf(dt[e], fed[e], skip[e] * dy[e]) : 0.f;
+                    float v = fmaf(u, fed[e], moved[e]);
+                    if (a.softplus) v *= sigm((float)raw[i].dt.e[e] + bias[e]);
+                    dd[e] = real ? v : 0.f;
+                    s_bias[e] += dd[e];
+                    s_skip[e] = real ? fmaf(dy[e], u, s_skip[e]) : s_skip[e];
                 }
-                store_quad<T>(w, (T*)a.dgate + row, quad, dz);
+                auto store = [&](void* p, const float (&v)[V]) {
+                    T* q = (T*)p + row;
+                    if (!whole) {
+                        store_piece<T, V>(q, col, w.left, v);
+                        return;
+                    }
+                    Packed<T, V> o;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o.e[e] = (T)v[e];
+                    *(Packed<T, V>*)(q + col) = o;
+                };
+                store(a.du, du);
+                store(a.ddt, dd);
+                if (a.gate) {
+#pragma unroll
+                    for (int k = 0; k < NW; ++k) y += *(const fv*)&part[2][k][in][col];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float z = (float)raw[i].z.e[e], sg = sigm(z);
+                        const float v = (float)raw[i].dy.e[e] * fmaf(skip[e], (float)raw[i].u.e[e], y[e]) * (sg * fmaf(z, 1.f - sg, 1.f));
+                        dz[e] = real ? v : 0.f;
+                    }
+                    store(a.dgate, dz);
+                }
             }
         }
-        if (tile > 0) fetch(tile - 1, true);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) raw[i] = next[i];
         __syncthreads();
     }
 #pragma unroll
     for (int s = 0; s < kSpw; ++s) a.part_a[m.slot(a, w.chunk, w.block, NW, s)] = da[s];
     // the channels' sums over the threads that had them, in order
-    constexpr int kHave = Q::kCount < Q::kThreads ? Q::kCount : Q::kThreads;
-    float* red = &part[0][0][0][0];
-    static_assert(sizeof(part) >= kHave * 8 * sizeof(float), "room for the sums");
-    if ((int)threadIdx.x < kHave) {
-        *(f4*)(red + threadIdx.x * 8) = s_skip;
-        *(f4*)(red + threadIdx.x * 8 + 4) = s_bias;
+    constexpr int kRows = (kPieces < kThreads ? kPieces : kThreads) / kRow;
+    static_assert(kRows <= kBack && 3 * NW >= 2, "room for the sums");
+    if (works) {
+        *(fv*)&part[0][0][in0][col] = s_skip;
+        *(fv*)&part[1][0][in0][col] = s_bias;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * kLanes; i += NW * 64) {
         const int which = i / kLanes, ch = i % kLanes;
         float v = 0.f;
-        for (int k = 0; k < kHave / 16; ++k) v += red[(k * 16 + ch / 4) * 8 + which * 4 + ch % 4];
+        for (int k = 0; k < kRows; ++k) v += part[which][0][k][ch];
         if (ch < w.left) a.part_d[(w.chunk * 2 + which) * a.dim + w.c0 + ch] = v;
     }
 }
