@@ -12,7 +12,8 @@ gconv_bwd_bias, gconv_output_dims, gconv_workspace_size, gconv_select_path,
 gconv_set_path_override; gconv_linattn_fwd, gconv_linattn_bwd,
 gconv_linattn_step, gconv_normgate_fwd, gconv_normgate_bwd, gconv_orthogonalize,
 gconv_shortconv_fwd, gconv_shortconv_bwd, gconv_shortconv_step, gconv_scan_fwd,
-gconv_scan_bwd, gconv_scan_step.
+gconv_scan_bwd, gconv_scan_step, gconv_embed_fwd, gconv_embed_bwd,
+gconv_xent_fwd, gconv_xent_bwd.
 """
 from __future__ import annotations
 
@@ -33,6 +34,8 @@ LAYOUT_NCHW, LAYOUT_NHWC = 0, 1
 F32, BF16 = 0, 1
 LINATTN_FWD, LINATTN_BWD = 0, 1
 SCAN_FWD, SCAN_BWD = 0, 1
+XENT_FWD, XENT_BWD = 0, 1
+I32, I64 = 0, 1
 GATE_NONE, GATE_FULL, GATE_SEQUENCE = 0, 1, 2
 ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 PATH_NAMES = {PATH_AUTO: "auto", PATH_DIRECT: "direct", PATH_SMALLGROUP: "smallgroup",
@@ -46,7 +49,9 @@ EXPORTS = ("gconv_output_dims", "gconv_workspace_size", "gconv_fwd", "gconv_fwd_
            "gconv_normgate_workspace_size", "gconv_normgate_fwd", "gconv_normgate_bwd",
            "gconv_orthogonalize_workspace_size", "gconv_orthogonalize",
            "gconv_shortconv_workspace_size", "gconv_shortconv_fwd", "gconv_shortconv_bwd", "gconv_shortconv_step",
-           "gconv_scan_workspace_size", "gconv_scan_fwd", "gconv_scan_bwd", "gconv_scan_step")
+           "gconv_scan_workspace_size", "gconv_scan_fwd", "gconv_scan_bwd", "gconv_scan_step",
+           "gconv_embed_workspace_size", "gconv_embed_fwd", "gconv_embed_bwd", "gconv_xent_workspace_size", "gconv_xent_fwd",
+           "gconv_xent_bwd")
 
 
 class GconvError(RuntimeError):
@@ -89,6 +94,16 @@ class gconv_scan_desc(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "packed", "sequences", "tokens", "dim", "states", "groups", "softplus")] +
                 [(n, ctypes.c_int64 * 2) for n in ("u_stride", "dt_stride", "gate_stride")] +
                 [(n, ctypes.c_int64 * 3) for n in ("b_stride", "c_stride")] + [("dy_stride", ctypes.c_int64 * 2)])
+
+
+class gconv_embed_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "index", "sequences", "tokens", "rows", "dim")] +
+                [("dy_stride", ctypes.c_int64 * 2), ("scale", ctypes.c_double)])
+
+
+class gconv_xent_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("dtype", "index", "sequences", "tokens", "vocab", "dim")] +
+                [("h_stride", ctypes.c_int64 * 2), ("scale", ctypes.c_double)])
 
 
 _lib = None
@@ -137,6 +152,12 @@ def load(path: str = LIB_PATH):
         "gconv_scan_fwd": [ctypes.POINTER(gconv_scan_desc)] + [P] * 13 + [S, P],
         "gconv_scan_bwd": [ctypes.POINTER(gconv_scan_desc)] + [P] * 21 + [S, P],
         "gconv_scan_step": [ctypes.POINTER(gconv_scan_desc)] + [P] * 10 + [ctypes.c_int64, P, P],
+        "gconv_embed_workspace_size": [ctypes.POINTER(gconv_embed_desc), ctypes.POINTER(S)],
+        "gconv_embed_fwd": [ctypes.POINTER(gconv_embed_desc)] + [P] * 4,
+        "gconv_embed_bwd": [ctypes.POINTER(gconv_embed_desc)] + [P] * 4 + [S, P],
+        "gconv_xent_workspace_size": [ctypes.POINTER(gconv_xent_desc), I, ctypes.POINTER(S)],
+        "gconv_xent_fwd": [ctypes.POINTER(gconv_xent_desc)] + [P] * 6 + [S, P],
+        "gconv_xent_bwd": [ctypes.POINTER(gconv_xent_desc)] + [P] * 9 + [S, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -1037,3 +1058,119 @@ def gconv_scan_step(u, dt, a, b, c, state, *, skip=None, gate=None, dt_bias=None
     _launch("gconv_scan_step", u.device, d, u.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), _addr(skip),
             _addr(gate), _addr(dt_bias), state.data_ptr(), _addr(slots), num, out.data_ptr())
     return out
+
+
+def _names(t, name, device):
+    """A contiguous GPU tensor of whole numbers that name tokens; its gconv_index."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a torch.Tensor" % name)
+    if t.dtype not in (torch.int32, torch.int64):
+        raise ValueError("%s must be int32 or int64, got %s" % (name, t.dtype))
+    if t.dim() not in (1, 2):
+        raise ValueError("%s must be [T] or [N, T]" % name)
+    if t.device != device or not t.is_cuda:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return I64 if t.dtype == torch.int64 else I32
+
+
+def _rows_of(t, name, lead):
+    """(sequences, tokens) of tokens [T] or [N, T], and the strides of t [T, D] or [N, T, D] between them."""
+    if tuple(t.shape[:-1]) != tuple(lead):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(lead) + ("D",)))
+    _last_axis(t, name)
+    N, T = lead if len(lead) == 2 else (1, lead[0])
+    return N, T, (ctypes.c_int64 * 2)(*((0,) + t.stride()[:1] if len(lead) == 1 else t.stride()[:2]))
+
+
+def gconv_embed_fwd(table, ids, *, scale=1.0):
+    """The embedding of tokens: scale * table[ids], 0 for an id outside the table. table [rows, D]
+    (float32 or bfloat16, contiguous), ids int32 or int64 [T] or [N, T]. Returns ids' shape + [D]."""
+    def make():
+        _seq(table, "table")
+        if table.dim() != 2:
+            raise ValueError("table must be [rows, D]")
+        _dense(table, "table", table.shape, table.dtype, table.device)
+        index = _names(ids, "ids", table.device)
+        N, T = ids.shape if ids.dim() == 2 else (1, ids.shape[0])
+        return (ctypes.byref(gconv_embed_desc(_dtype_code(table), index, N, T, table.shape[0], table.shape[1], (ctypes.c_int64 * 2)(),
+                                              float(scale))),)
+
+    d, = _plan("embed_fwd", (table, ids), (scale,), make)
+    y = table.new_empty(ids.shape + table.shape[1:])
+    _launch("gconv_embed_fwd", table.device, d, _addr(table), _addr(ids), _addr(y))
+    return y
+
+
+def gconv_embed_bwd(dy, ids, rows, *, scale=1.0, workspace=None):
+    """The gradient [rows, D] of gconv_embed_fwd's table for dy of its result (any strides with a
+    contiguous last axis): each row the sum over its tokens, in their order; rows without tokens are 0."""
+    def make():
+        _seq(dy, "dy")
+        index = _names(ids, "ids", dy.device)
+        N, T, stride = _rows_of(dy, "dy", ids.shape)
+        d = gconv_embed_desc(_dtype_code(dy), index, N, T, int(rows), dy.shape[-1], stride, float(scale))
+        n = ctypes.c_size_t()
+        _check(load().gconv_embed_workspace_size(ctypes.byref(d), ctypes.byref(n)), "gconv_embed_workspace_size")
+        return ctypes.byref(d), n.value
+
+    d, need = _plan("embed_bwd", (dy, ids), (rows, scale), make)
+    dtable = dy.new_empty((int(rows), dy.shape[-1]))
+    ws, nws = _scratch(need, dy.device, workspace)
+    _launch("gconv_embed_bwd", dy.device, d, _addr(dy), _addr(ids), _addr(dtable), _addr(ws), nws)
+    return dtable
+
+
+def _xent_desc(h, w, targets, scale):
+    _seq(h, "h")
+    _seq(w, "w")
+    if w.dim() != 2:
+        raise ValueError("w must be [vocab, D]")
+    _dense(w, "w", (w.shape[0], h.shape[-1] if h.dim() else 0), h.dtype, h.device)
+    index = _names(targets, "targets", h.device)
+    N, T, stride = _rows_of(h, "h", targets.shape)
+    return gconv_xent_desc(_dtype_code(h), index, N, T, w.shape[0], w.shape[1], stride, float(scale))
+
+
+def gconv_xent_workspace_size(desc: gconv_xent_desc, op: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gconv_xent_workspace_size(ctypes.byref(desc), int(op), ctypes.byref(n)), "gconv_xent_workspace_size")
+    return n.value
+
+
+def gconv_xent_fwd(h, w, targets, *, scale=1.0, workspace=None):
+    """Softmax cross entropy of tokens against a vocabulary, whose logits scale * h w^T are not kept.
+    h [T, D] or [N, T, D] (float32 or bfloat16, any strides with a contiguous last axis), w [vocab, D]
+    of the same type, targets int32 or int64 [T] or [N, T]; a target outside the vocabulary does not
+    count. Returns loss (0 where it does not count) and lse, the logarithm of the sum of the logits'
+    exponentials, of targets' shape in float32."""
+    def make():
+        d = _xent_desc(h, w, targets, scale)
+        return ctypes.byref(d), gconv_xent_workspace_size(d, XENT_FWD)
+
+    d, need = _plan("xent_fwd", (h, w, targets), (scale,), make)
+    torch = _torch()
+    loss, lse = (h.new_empty(targets.shape, dtype=torch.float32) for _ in range(2))
+    ws, nws = _scratch(need, h.device, workspace)
+    _launch("gconv_xent_fwd", h.device, d, _addr(h), _addr(w), _addr(targets), _addr(loss), _addr(lse), _addr(ws), nws)
+    return loss, lse
+
+
+def gconv_xent_bwd(dloss, h, w, targets, lse, *, dlse=None, scale=1.0, workspace=None):
+    """Gradients of gconv_xent_fwd for dloss of loss and dlse of lse (None: 0), both of targets' shape in
+    float32; lse as the forward pass gave it. Returns dh and dw, of h's and w's shapes and type."""
+    def make():
+        d = _xent_desc(h, w, targets, scale)
+        for t, name in ((dloss, "dloss"), (lse, "lse"), (dlse, "dlse")):
+            if t is not None or name != "dlse":
+                _dense(t, name, targets.shape, _torch().float32, h.device)
+        return ctypes.byref(d), gconv_xent_workspace_size(d, XENT_BWD)
+
+    d, need = _plan("xent_bwd", (dloss, h, w, targets, lse, dlse), (scale,), make)
+    dh, dw = h.new_empty(h.shape), w.new_empty(w.shape)
+    ws, nws = _scratch(need, h.device, workspace)
+    _launch("gconv_xent_bwd", h.device, d, _addr(dloss), _addr(dlse), _addr(h), _addr(w), _addr(targets), _addr(lse), _addr(dh), _addr(dw),
+            _addr(ws), nws)
+    return dh, dw

@@ -1,0 +1,426 @@
+// embed.hip -- the embedding of tokens and its gradient (gfx950).
+//
+//   y_t = scale table[id_t]         dtable[v] = scale sum over t with id_t = v of dy_t
+//
+// Bound by HBM: forward each row read and written, backward dy read once and
+// dtable written once. The gradient's sums are taken in the tokens' order, so
+// results are the same every time: the tokens are sorted by their ids (a stable
+// radix sort, 9 bits a pass, of numbers only), each row's tokens then follow one
+// another, and a workgroup adds up a row's from registers to the one write of it,
+// zeros where there are none. A row with more tokens than a slice of the sorted
+// order is long gets its sum slice by slice first, so a token that makes up all
+// of a text costs no more than many that do not.
+#include <cmath>
+
+#include "seq_host.h"
+#include "seq_tokens.h"
+
+namespace gconv {
+namespace {
+
+constexpr int kBits = 9, kBins = 1 << kBits;
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+struct Embed {
+    const void *table, *ids, *dy;
+    void *y, *dtable;
+    int64_t tokens, rows;     // of all sequences; of the table
+    int64_t per_seq, dy_seq, dy_tok;
+    int dim, wide;
+    float scale;
+    // sorting
+    uint32_t *key[2], *at[2]; // [tokens]: ids (rows for one outside the table) and tokens, in two orders
+    uint32_t* counts;         // [blocks][kBins]
+    uint32_t* start;          // [rows + 1]: first place of each row's tokens
+    int blocks, chunk;        // of the sort: tokens of a block, a multiple of kThreads
+    int shift;
+    // sums
+    float* part;              // [slices][2][dim]: of the row that runs into a slice, and of the one that runs out
+    int slice;                // tokens
+    int64_t slices;
+};
+
+__device__ __forceinline__ uint32_t key_of(const Embed& a, int64_t t)
+{
+    const int64_t id = a.wide ? ((const int64_t*)a.ids)[t] : (int64_t)((const int32_t*)a.ids)[t];
+    return id >= 0 && id < a.rows ? (uint32_t)id : (uint32_t)a.rows;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void embed_fwd(Embed a, int px)
+{
+    constexpr int V = 16 / sizeof(T);
+    const int rows = kThreads / px, tx = threadIdx.x % px, ty = threadIdx.x / px;
+    const int64_t t = (int64_t)blockIdx.x * rows + ty;
+    if (t >= a.tokens) return;
+    const uint32_t id = key_of(a, t);
+    const T* from = (const T*)a.table + (int64_t)id * a.dim;
+    T* to = (T*)a.y + t * a.dim;
+    for (int col = tx * V; col < a.dim; col += px * V) {
+        float v[V];
+        if (id < a.rows) {
+            const Packed<T, V> p = load_piece<T, V>(from, col, a.dim);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = a.scale * (float)p.e[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = 0.f;
+        }
+        store_piece<T, V>(to, col, a.dim, v);
+    }
+}
+
+// ---- sorting ----------------------------------------------------------------------
+
+template <bool FIRST>
+__device__ __forceinline__ uint32_t sort_key(const Embed& a, int from, int64_t i)
+{
+    return FIRST ? key_of(a, i) : a.key[from][i];
+}
+
+// How many of a block's keys have each digit.
+template <bool FIRST>
+__global__ __launch_bounds__(kThreads) void embed_count(Embed a, int from)
+{
+    __shared__ uint32_t bins[kBins];
+    for (int i = threadIdx.x; i < kBins; i += kThreads) bins[i] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(t0 + a.chunk, a.tokens);
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += kThreads) atomicAdd(&bins[sort_key<FIRST>(a, from, t) >> a.shift & (kBins - 1)], 1u);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads) a.counts[(int64_t)blockIdx.x * kBins + i] = bins[i];
+}
+
+// Sum of v over the threads before this one.
+__device__ __forceinline__ uint32_t exclusive_sum(uint32_t v, uint32_t* red)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t s = v;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+        const uint32_t o = __shfl_up(s, k);
+        if (lane >= k) s += o;
+    }
+    if (lane == 63) red[wave] = s;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int k = 0; k < wave; ++k) before += red[k];
+    __syncthreads();
+    return before + s - v;
+}
+
+// Puts a block's keys in their places: those of smaller digits, of earlier
+// blocks, of earlier waves, and of the wave's earlier keys come before each. A
+// wave takes 64 keys that follow one another at a time; lanes with the same digit
+// find one another by a vote on each of its bits.
+template <bool FIRST>
+__global__ __launch_bounds__(kThreads) void embed_place(Embed a, int from, int to)
+{
+    static_assert(kBins == 2 * kThreads, "two digits a thread");
+    __shared__ uint32_t next[kWaves][kBins], red[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // this thread's digits: all of them before this block, and in all
+    uint32_t mine[2] = {0, 0}, all[2] = {0, 0};
+    for (int k = 0; k < a.blocks; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t c = a.counts[(int64_t)k * kBins + threadIdx.x * 2 + i];
+            all[i] += c;
+            if (k < (int)blockIdx.x) mine[i] += c;
+        }
+    const uint32_t before = exclusive_sum(all[0] + all[1], red);
+    for (int i = threadIdx.x; i < kWaves * kBins; i += kThreads) next[0][i] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * a.chunk, own = t0 + (int64_t)wave * (a.chunk / kWaves);
+    const int64_t end = min(own + a.chunk / kWaves, a.tokens);
+    for (int64_t t = own + lane; t < end; t += 64) atomicAdd(&next[wave][sort_key<FIRST>(a, from, t) >> a.shift & (kBins - 1)], 1u);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t at = before + (i ? all[0] : 0) + mine[i];
+        for (int k = 0; k < kWaves; ++k) {
+            const uint32_t c = next[k][threadIdx.x * 2 + i];
+            next[k][threadIdx.x * 2 + i] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int64_t t = own; t < end; t += 64) {
+        const bool have = t + lane < end;
+        const uint32_t key = have ? sort_key<FIRST>(a, from, t + lane) : 0, digit = key >> a.shift & (kBins - 1);
+        uint64_t same = __ballot(have);
+#pragma unroll
+        for (int b = 0; b < kBits; ++b) {
+            const uint64_t set = __ballot(digit >> b & 1);
+            same &= digit >> b & 1 ? set : ~set;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        const uint32_t place = have ? next[wave][digit] + rank : 0;
+        __builtin_amdgcn_wave_barrier();
+        if (have && rank == 0) next[wave][digit] += __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        if (have) {
+            a.key[to][place] = key;
+            a.at[to][place] = FIRST ? (uint32_t)(t + lane) : a.at[from][t + lane];
+        }
+    }
+}
+
+// start[v] = the first place whose key is v or more.
+__global__ __launch_bounds__(kThreads) void embed_starts(Embed a, int from)
+{
+    const int64_t v = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (v > a.rows) return;
+    int64_t lo = 0, hi = a.tokens;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (a.key[from][mid] < v) lo = mid + 1;
+        else hi = mid;
+    }
+    a.start[v] = (uint32_t)lo;
+}
+
+// ---- sums -------------------------------------------------------------------------
+
+// Adds dy of the tokens at places [p0, p1), a piece of columns each thread.
+template <typename T, int V>
+__device__ __forceinline__ void add_tokens(const Embed& a, const uint32_t* at, uint32_t p0, uint32_t p1, int col, float (&sum)[V])
+{
+    constexpr int U = 8;
+    for (uint32_t p = p0; p < p1; p += U) {
+        Packed<T, V> v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const uint32_t t = at[min(p + i, p1 - 1)];
+            const int64_t n = t / a.per_seq;
+            v[i] = load_piece<T, V>((const T*)a.dy + n * a.dy_seq + (t - n * a.per_seq) * a.dy_tok, col, a.dim);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (p + i < p1)
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] += (float)v[i].e[e];
+    }
+}
+
+// The slices' sums of rows with more tokens than a slice has: such a row runs
+// into a slice, out of it, or both.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void embed_slices(Embed a, int from)
+{
+    constexpr int V = 16 / sizeof(T);
+    const int64_t s = blockIdx.x;
+    const uint32_t p0 = (uint32_t)(s * a.slice), p1 = (uint32_t)min(s * a.slice + a.slice, a.tokens);
+    const uint32_t *key = a.key[from], *at = a.at[from];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const uint32_t k = key[which ? p1 - 1 : p0];
+        if (k >= a.rows) continue;
+        const uint32_t b = a.start[k], e = a.start[k + 1];
+        if (e - b <= (uint32_t)a.slice || (which == 0 ? b > p0 : b <= p0)) continue;
+        if (which == 0 && b > p0) continue;
+        const uint32_t q0 = max(b, p0), q1 = min(e, p1);
+        for (int col = threadIdx.x * V; col < a.dim; col += kThreads * V) {
+            float sum[V] = {};
+            add_tokens<T, V>(a, at, q0, q1, col, sum);
+            store_piece<float, V>(a.part + (s * 2 + which) * a.dim, col, a.dim, sum);
+        }
+    }
+}
+
+// Rows of dtable.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from, int px)
+{
+    constexpr int V = 16 / sizeof(T);
+    const int per = kThreads / px, tx = threadIdx.x % px, ty = threadIdx.x / px;
+    for (int64_t r = (int64_t)blockIdx.x * per + ty; r < a.rows; r += (int64_t)gridDim.x * per) {
+        const uint32_t b = a.start[r], e = a.start[r + 1];
+        T* to = (T*)a.dtable + r * a.dim;
+        for (int col = tx * V; col < a.dim; col += px * V) {
+            float sum[V] = {};
+            if (e - b <= (uint32_t)a.slice) {
+                add_tokens<T, V>(a, a.at[from], b, e, col, sum);
+            } else {
+                const int64_t s0 = b / a.slice, s1 = (e - 1) / a.slice;
+                for (int64_t s = s0; s <= s1; ++s) {
+                    const Packed<float, V> p = load_piece<float, V>(a.part + (s * 2 + (b > s * a.slice ? 1 : 0)) * a.dim, col, a.dim);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[i] += p.e[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] *= a.scale;
+            store_piece<T, V>(to, col, a.dim, sum);
+        }
+    }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+constexpr int64_t kMaxDim = (int64_t)1 << 24;
+
+int check_desc(const gconv_embed_desc* d)
+{
+    if (!d) return fail(GCONV_ERR_NULL, "descriptor is NULL");
+    if (d->dtype != GCONV_F32 && d->dtype != GCONV_BF16) return fail(GCONV_ERR_ARG, "unknown dtype %lld", (long long)d->dtype);
+    if (d->index != GCONV_I32 && d->index != GCONV_I64) return fail(GCONV_ERR_ARG, "unknown index type %lld", (long long)d->index);
+    if (d->sequences < 0 || d->tokens < 0 || d->rows < 1 || d->dim < 1)
+        return fail(GCONV_ERR_SHAPE, "need sequences, tokens >= 0 and rows, dim >= 1 (got %lld, %lld, %lld, %lld)", (long long)d->sequences,
+                    (long long)d->tokens, (long long)d->rows, (long long)d->dim);
+    if (d->rows >= (int64_t)1 << 31) return fail(GCONV_ERR_UNSUPPORTED, "rows=%lld not below 2^31", (long long)d->rows);
+    if (d->dim > kMaxDim) return fail(GCONV_ERR_UNSUPPORTED, "dim=%lld above %lld", (long long)d->dim, (long long)kMaxDim);
+    if (d->sequences > kMaxTokens || d->tokens > kMaxTokens || (d->tokens > 0 && d->sequences > kMaxTokens / d->tokens))
+        return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
+    if (!std::isfinite(d->scale)) return fail(GCONV_ERR_ARG, "scale must be finite");
+    return GCONV_OK;
+}
+
+struct Layout {
+    size_t key[2], at[2], counts, start, part, bytes;
+};
+
+void plan(const gconv_embed_desc* d, Embed* a, Layout* l)
+{
+    a->tokens = d->sequences * d->tokens;
+    a->per_seq = std::max<int64_t>(d->tokens, 1);
+    a->rows = d->rows;
+    a->dim = (int)d->dim;
+    a->wide = d->index == GCONV_I64;
+    a->scale = (float)d->scale;
+    a->dy_seq = d->dy_stride[0];
+    a->dy_tok = d->dy_stride[1];
+    // at most 512 blocks, each of which reads all of their counts
+    int64_t chunk = 2048;
+    while (a->tokens > chunk * 512) chunk *= 2;
+    a->chunk = (int)chunk;
+    a->blocks = (int)((a->tokens + chunk - 1) / chunk);
+    // a slice about as long as the slices of one token that makes up the text are many
+    int64_t slice = 64;
+    while (slice * slice < a->tokens && slice < 4096) slice *= 2;
+    a->slice = (int)slice;
+    a->slices = (a->tokens + slice - 1) / slice;
+    Cut cut;
+    for (int i = 0; i < 2; ++i) l->key[i] = cut.take(a->tokens * 4);
+    for (int i = 0; i < 2; ++i) l->at[i] = cut.take(a->tokens * 4);
+    l->counts = cut.take((int64_t)a->blocks * kBins * 4);
+    l->start = cut.take((a->rows + 1) * 4);
+    l->part = cut.take(a->slices * 2 * a->dim * 4);
+    l->bytes = cut.bytes;
+}
+
+int width(int64_t dim, int64_t v)
+{
+    int px = 1;
+    while (px < kThreads && px * v < dim) px *= 2;
+    return px;
+}
+
+template <typename T>
+int backward(const gconv_embed_desc* d, Embed a, hipStream_t st)
+{
+    int bits = 1;
+    while ((a.rows >> bits) > 0) ++bits;
+    const unsigned blocks = (unsigned)a.blocks;
+    int from = 0;
+    for (int done = 0, pass = 0; done < bits && blocks > 0; done += kBits, ++pass) {
+        a.shift = done;
+        const int to = pass & 1;
+        if (pass == 0) {
+            embed_count<true><<<blocks, kThreads, 0, st>>>(a, 0);
+            embed_place<true><<<blocks, kThreads, 0, st>>>(a, 0, to);
+        } else {
+            embed_count<false><<<blocks, kThreads, 0, st>>>(a, from);
+            embed_place<false><<<blocks, kThreads, 0, st>>>(a, from, to);
+        }
+        from = to;
+    }
+    embed_starts<<<(unsigned)((a.rows + kThreads) / kThreads), kThreads, 0, st>>>(a, from);
+    if (a.slices > 1) embed_slices<T><<<(unsigned)a.slices, kThreads, 0, st>>>(a, from);
+    const int px = width(a.dim, 16 / (int)sizeof(T)), per = kThreads / px;
+    embed_rows<T><<<(unsigned)std::min<int64_t>((a.rows + per - 1) / per, 1 << 16), kThreads, 0, st>>>(a, from, px);
+    return finish();
+}
+
+}  // namespace
+}  // namespace gconv
+
+using namespace gconv;
+
+extern "C" {
+
+int gconv_embed_workspace_size(const gconv_embed_desc* d, size_t* bytes)
+{
+    const int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    if (!bytes) return fail(GCONV_ERR_NULL, "bytes pointer is NULL");
+    Embed a{};
+    Layout l{};
+    plan(d, &a, &l);
+    *bytes = l.bytes;
+    return GCONV_OK;
+}
+
+int gconv_embed_fwd(const gconv_embed_desc* d, const void* table, const void* ids, void* y, void* stream)
+{
+    int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    const int64_t tokens = d->sequences * d->tokens, es = d->dtype == GCONV_BF16 ? 2 : 4, is = d->index == GCONV_I64 ? 8 : 4;
+    if (!table || (tokens > 0 && (!ids || !y))) return fail(GCONV_ERR_NULL, "table, ids and y must be non-NULL");
+    const Span in[] = {{table, d->rows * d->dim * es}, {ids, tokens * is}};
+    const Span out[] = {{y, tokens * d->dim * es}};
+    st = check_overlap(in, out);
+    if (st != GCONV_OK) return st;
+    Embed a{};
+    Layout l{};
+    plan(d, &a, &l);
+    a.table = table;
+    a.ids = ids;
+    a.y = y;
+    const int px = width(d->dim, 16 / es), per = kThreads / px;
+    const int64_t blocks = (tokens + per - 1) / per;
+    if (blocks > max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
+    (void)hipGetLastError();
+    if (blocks > 0) {
+        if (d->dtype == GCONV_BF16) embed_fwd<__bf16><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a, px);
+        else embed_fwd<float><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a, px);
+    }
+    return finish();
+}
+
+int gconv_embed_bwd(const gconv_embed_desc* d, const void* dy, const void* ids, void* dtable, void* workspace, size_t workspace_bytes,
+                    void* stream)
+{
+    int st = check_desc(d);
+    if (st != GCONV_OK) return st;
+    const int64_t tokens = d->sequences * d->tokens, es = d->dtype == GCONV_BF16 ? 2 : 4, is = d->index == GCONV_I64 ? 8 : 4;
+    if (!dtable || (tokens > 0 && (!ids || !dy))) return fail(GCONV_ERR_NULL, "dy, ids and dtable must be non-NULL");
+    const Span in[] = {strided_span(dy, es, d->sequences, d->dy_stride[0], d->tokens, d->dy_stride[1], 1, 0, d->dim), {ids, tokens * is}};
+    const Span out[] = {{dtable, d->rows * d->dim * es}};
+    st = check_overlap(in, out);
+    if (st != GCONV_OK) return st;
+    Embed a{};
+    Layout l{};
+    plan(d, &a, &l);
+    st = check_workspace(workspace, workspace_bytes, l.bytes);
+    if (st != GCONV_OK) return st;
+    if (a.slices > max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
+    char* w = (char*)workspace;
+    a.dy = dy;
+    a.ids = ids;
+    a.dtable = dtable;
+    for (int i = 0; i < 2; ++i) {
+        a.key[i] = (uint32_t*)(w + l.key[i]);
+        a.at[i] = (uint32_t*)(w + l.at[i]);
+    }
+    a.counts = (uint32_t*)(w + l.counts);
+    a.start = (uint32_t*)(w + l.start);
+    a.part = (float*)(w + l.part);
+    (void)hipGetLastError();
+    if (d->dtype == GCONV_BF16) return backward<__bf16>(d, a, (hipStream_t)stream);
+    return backward<float>(d, a, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -536,6 +536,84 @@ int gconv_scan_step(const gconv_scan_desc* d, const void* u, const void* dt, con
                     const float* skip, const void* gate, const float* dt_bias, float* state, const int32_t* slots, int64_t num_slots,
                     void* y, void* stream);
 
+/* Whole numbers that name tokens. */
+typedef enum gconv_index {
+    GCONV_I32 = 0,
+    GCONV_I64 = 1
+} gconv_index;
+
+/*
+ * The embedding of tokens: y[n][t] = scale table[ids[n][t]]. ids [sequences,
+ * tokens] dense, of type `index`; table [rows, dim], y [sequences, tokens,
+ * dim] dense. An id outside 0..rows-1 (say, -1 for padding) gives 0 and has no
+ * gradient. rows up to 2^31 - 1, dim up to 2^24, 2^30 ids.
+ */
+typedef struct gconv_embed_desc {
+    int64_t dtype;              /* gconv_dtype of table, y and their gradients */
+    int64_t index;              /* gconv_index of ids */
+    int64_t sequences, tokens;
+    int64_t rows, dim;
+    int64_t dy_stride[2];       /* in elements, between sequences and tokens; read by gconv_embed_bwd only */
+    double scale;
+} gconv_embed_desc;
+
+/* Bytes of workspace gconv_embed_bwd needs, 16-byte aligned (the forward pass needs none). */
+int gconv_embed_workspace_size(const gconv_embed_desc* d, size_t* bytes);
+
+int gconv_embed_fwd(const gconv_embed_desc* d, const void* table, const void* ids, void* y, void* stream);
+
+/*
+ * dtable [rows, dim], dense, for dy of y: each row the sum over its tokens, in
+ * their order, in float32 and rounded once; rows without tokens are 0.
+ */
+int gconv_embed_bwd(const gconv_embed_desc* d, const void* dy, const void* ids, void* dtable, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
+ * Softmax cross entropy of tokens against a vocabulary, without keeping the
+ * logits: z = scale h w^T, and for each token
+ *
+ *   lse = log sum_v exp(z_v)        loss = lse - z_target
+ *
+ * h [sequences, tokens, dim] (strides in elements, [0] between sequences, [1]
+ * between tokens, the last axis contiguous), w [vocab, dim] dense (16-byte
+ * aligned where it is bfloat16 and dim a multiple of 64), targets, loss and
+ * lse [sequences, tokens] dense; targets of type `index`, loss and lse
+ * float32. A token whose target is outside 0..vocab-1 does not count: its loss
+ * is 0 (its lse is given) and it has no gradient. bfloat16 products are summed
+ * in float32; float32 ones are made of bfloat16 parts, to float32's accuracy,
+ * and an infinity in float32 h or w gives NaN. dim up to 2^20, vocab up to
+ * 2^30, 2^30 tokens.
+ */
+typedef struct gconv_xent_desc {
+    int64_t dtype;              /* gconv_dtype of h, w and their gradients */
+    int64_t index;              /* gconv_index of targets */
+    int64_t sequences, tokens;
+    int64_t vocab, dim;
+    int64_t h_stride[2];
+    double scale;
+} gconv_xent_desc;
+
+typedef enum gconv_xent_op {
+    GCONV_XENT_FWD = 0,
+    GCONV_XENT_BWD = 1
+} gconv_xent_op;
+
+/* Bytes of workspace `op` (a gconv_xent_op) needs, 16-byte aligned. */
+int gconv_xent_workspace_size(const gconv_xent_desc* d, int op, size_t* bytes);
+
+int gconv_xent_fwd(const gconv_xent_desc* d, const void* h, const void* w, const void* targets, float* loss, float* lse, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients for dloss of loss and dlse of lse (NULL: 0), [sequences, tokens]
+ * float32 dense, given the forward pass's lse: dh [sequences, tokens, dim] and
+ * dw, dense, of the inputs' type. The logits' gradient is rounded to bfloat16
+ * for the products that follow where h and w are bfloat16.
+ */
+int gconv_xent_bwd(const gconv_xent_desc* d, const float* dloss, const float* dlse, const void* h, const void* w, const void* targets,
+                   const float* lse, void* dh, void* dw, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
