@@ -150,7 +150,7 @@ def load(path: str = LIB_PATH):
         "gconv_shortconv_step": [ctypes.POINTER(gconv_shortconv_desc)] + [P] * 5 + [ctypes.c_int64, P, P],
         "gconv_scan_workspace_size": [ctypes.POINTER(gconv_scan_desc), I, ctypes.POINTER(S)],
         "gconv_scan_fwd": [ctypes.POINTER(gconv_scan_desc)] + [P] * 13 + [S, P],
-        "gconv_scan_bwd": [ctypes.POINTER(gconv_scan_desc)] + [P] * 21 + [S, P],
+        "gconv_scan_bwd": [ctypes.POINTER(gconv_scan_desc)] + [P] * 22 + [S, P],
         "gconv_scan_step": [ctypes.POINTER(gconv_scan_desc)] + [P] * 10 + [ctypes.c_int64, P, P],
         "gconv_embed_workspace_size": [ctypes.POINTER(gconv_embed_desc), ctypes.POINTER(S)],
         "gconv_embed_fwd": [ctypes.POINTER(gconv_embed_desc)] + [P] * 4,

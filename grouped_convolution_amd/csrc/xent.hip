@@ -20,7 +20,7 @@
 // The products take bfloat16. float32 operands are made into three bfloat16 parts
 // (8 bits and a sign each, so that together they are the float32), and the six
 // products of parts that count are added up in float32: what is left out is
-// below 2^-26 of the product. A float32 operand that is infinite gives NaN.
+// 2^-23 of a product at most, two of float32's own roundings. A float32 operand that is infinite gives NaN.
 // dz is rounded to bfloat16 (or three parts) as the second products' operand.
 //
 // Tokens that do not count (a target outside the vocabulary) have rows of zeros
@@ -573,7 +573,7 @@ Tile tile_of(int64_t rows, int64_t cols)
 // there are CUs without work, each at least 8 stages long.
 int splits_of(const Tile& t, int64_t rows, int64_t cols, int64_t stages)
 {
-    const int64_t count = ((rows + t.q - 1) / t.q) * ((cols + t.p - 1) / t.p);
+    const int64_t count = std::max<int64_t>(1, (rows + t.q - 1) / t.q) * ((cols + t.p - 1) / t.p);
     return (int)std::max<int64_t>(1, std::min<int64_t>(256 / count, stages / 8));
 }
 
