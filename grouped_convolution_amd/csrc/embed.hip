@@ -38,7 +38,9 @@ struct Embed {
     // sums
     float* part;              // [slices][2][dim]: of the row that runs into a slice, and of the one that runs out
     int slice;                // tokens
-    int64_t slices;
+    int64_t slices;           // none where no row can have more tokens than one
+    int64_t stretches;        // of columns
+    int flat;                 // dy's rows follow one another at its tokens' stride
 };
 
 __device__ __forceinline__ uint32_t key_of(const Embed& a, int64_t t)
@@ -122,6 +124,7 @@ __global__ __launch_bounds__(kThreads) void embed_place(Embed a, int from, int t
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     // this thread's digits: all of them before this block, and in all
     uint32_t mine[2] = {0, 0}, all[2] = {0, 0};
+#pragma unroll 8
     for (int k = 0; k < a.blocks; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -183,77 +186,140 @@ __global__ __launch_bounds__(kThreads) void embed_starts(Embed a, int from)
 
 // ---- sums -------------------------------------------------------------------------
 
-// Adds dy of the tokens at places [p0, p1), a piece of columns each thread.
-template <typename T, int V>
-__device__ __forceinline__ void add_tokens(const Embed& a, const uint32_t* at, uint32_t p0, uint32_t p1, int col, float (&sum)[V])
-{
-    constexpr int U = 8;
-    for (uint32_t p = p0; p < p1; p += U) {
-        Packed<T, V> v[U];
+constexpr int kWide = 4;  // pieces of a row that a lane holds at once
+
+// A lane's pieces of a row, 64 lanes' side by side: from column `col`.
+template <typename T>
+struct Sum {
+    static constexpr int V = 16 / sizeof(T);
+    float v[kWide][V] = {};
+    template <typename U>
+    __device__ __forceinline__ void add(const U* row, int col, int dim)
+    {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const uint32_t t = at[min(p + i, p1 - 1)];
-            const int64_t n = t / a.per_seq;
-            v[i] = load_piece<T, V>((const T*)a.dy + n * a.dy_seq + (t - n * a.per_seq) * a.dy_tok, col, a.dim);
+        for (int k = 0; k < kWide; ++k) {
+            if (col + k * 64 * V >= dim) break;
+            const Packed<U, V> p = load_piece<U, V>(row, col + k * 64 * V, dim);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[k][e] += (float)p.e[e];
         }
+    }
+    template <typename U>
+    __device__ __forceinline__ void store(U* row, int col, int dim, float scale) const
+    {
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (p + i < p1)
+        for (int k = 0; k < kWide; ++k) {
+            if (col + k * 64 * V >= dim) break;
+            float o[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) sum[e] += (float)v[i].e[e];
+            for (int e = 0; e < V; ++e) o[e] = v[k][e] * scale;
+            store_piece<U, V>(row, col + k * 64 * V, dim, o);
+        }
+    }
+};
+
+// dy's row of a token.
+template <typename T>
+__device__ __forceinline__ const T* dy_row(const Embed& a, uint32_t t)
+{
+    if (a.flat) return (const T*)a.dy + t * a.dy_tok;
+    const uint32_t n = t / (uint32_t)a.per_seq;
+    return (const T*)a.dy + n * a.dy_seq + (int64_t)(t - n * (uint32_t)a.per_seq) * a.dy_tok;
+}
+
+// Adds dy of the tokens at places [p0, p1), whose numbers the lanes read 64 at a time.
+template <typename T>
+__device__ __forceinline__ void add_tokens(const Embed& a, const uint32_t* at, uint32_t p0, uint32_t p1, int col, Sum<T>& sum)
+{
+    const int lane = threadIdx.x & 63;
+    for (uint32_t p = p0; p < p1; p += 64) {
+        const uint32_t mine = at[min(p + lane, p1 - 1)];
+        const int n = (int)min(p1 - p, 64u);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) sum.add(dy_row<T>(a, __builtin_amdgcn_readlane(mine, i)), col, a.dim);
     }
 }
 
 // The slices' sums of rows with more tokens than a slice has: such a row runs
-// into a slice, out of it, or both.
+// into a slice, out of it, or both. A wave a slice and stretch of columns.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void embed_slices(Embed a, int from)
 {
-    constexpr int V = 16 / sizeof(T);
-    const int64_t s = blockIdx.x;
+    constexpr int kCols = 64 * kWide * Sum<T>::V;
+    const int lane = threadIdx.x & 63;
+    const int64_t id = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), s = id / a.stretches;
+    if (s >= a.slices) return;
+    const int col = (int)(id - s * a.stretches) * kCols + lane * Sum<T>::V;
     const uint32_t p0 = (uint32_t)(s * a.slice), p1 = (uint32_t)min(s * a.slice + a.slice, a.tokens);
-    const uint32_t *key = a.key[from], *at = a.at[from];
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        const uint32_t k = key[which ? p1 - 1 : p0];
+        const uint32_t k = a.key[from][which ? p1 - 1 : p0];
         if (k >= a.rows) continue;
         const uint32_t b = a.start[k], e = a.start[k + 1];
         if (e - b <= (uint32_t)a.slice || (which == 0 ? b > p0 : b <= p0)) continue;
-        if (which == 0 && b > p0) continue;
-        const uint32_t q0 = max(b, p0), q1 = min(e, p1);
-        for (int col = threadIdx.x * V; col < a.dim; col += kThreads * V) {
-            float sum[V] = {};
-            add_tokens<T, V>(a, at, q0, q1, col, sum);
-            store_piece<float, V>(a.part + (s * 2 + which) * a.dim, col, a.dim, sum);
-        }
+        Sum<T> sum;
+        add_tokens<T>(a, a.at[from], max(b, p0), min(e, p1), col, sum);
+        sum.store(a.part + (s * 2 + which) * a.dim, col, a.dim, 1.f);
     }
 }
 
-// Rows of dtable.
+// Rows of dtable, a wave a row: rows that follow one another in turn, the next
+// one's tokens looked up while one is written. The first workgroups take the rows
+// with more tokens than a slice has, each that of the slice in which it begins,
+// from the slices' sums: a quarter of them a wave, then the quarters.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from, int px)
+__global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from)
 {
-    constexpr int V = 16 / sizeof(T);
-    const int per = kThreads / px, tx = threadIdx.x % px, ty = threadIdx.x / px;
-    for (int64_t r = (int64_t)blockIdx.x * per + ty; r < a.rows; r += (int64_t)gridDim.x * per) {
-        const uint32_t b = a.start[r], e = a.start[r + 1];
-        T* to = (T*)a.dtable + r * a.dim;
-        for (int col = tx * V; col < a.dim; col += px * V) {
-            float sum[V] = {};
-            if (e - b <= (uint32_t)a.slice) {
-                add_tokens<T, V>(a, a.at[from], b, e, col, sum);
-            } else {
-                const int64_t s0 = b / a.slice, s1 = (e - 1) / a.slice;
-                for (int64_t s = s0; s <= s1; ++s) {
-                    const Packed<float, V> p = load_piece<float, V>(a.part + (s * 2 + (b > s * a.slice ? 1 : 0)) * a.dim, col, a.dim);
+    constexpr int V = Sum<T>::V, kCols = 64 * kWide * V;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (blockIdx.x < a.slices) {
+        __shared__ float red[kWaves][kWide][V][64];
+        const int64_t s0 = blockIdx.x;
+        const uint32_t p0 = (uint32_t)(s0 * a.slice), p1 = (uint32_t)min(s0 * a.slice + a.slice, a.tokens);
+        const uint32_t k = a.key[from][p1 - 1];
+        if (k >= a.rows) return;
+        const uint32_t b = a.start[k], e = a.start[k + 1];
+        if (e - b <= (uint32_t)a.slice || b < p0) return;
+        const int64_t s1 = (e - 1) / a.slice + 1, per = (s1 - s0 + kWaves - 1) / kWaves;
+        for (int c0 = 0; c0 < a.dim; c0 += kCols) {
+            Sum<T> sum;
+            const int64_t from_s = s0 + wave * per, to_s = min(from_s + per, s1);
+#pragma unroll 4
+            for (int64_t s = from_s; s < to_s; ++s)
+                sum.add(a.part + (s * 2 + (b > s * a.slice ? 1 : 0)) * a.dim, c0 + lane * V, a.dim);
+            __syncthreads();
 #pragma unroll
-                    for (int i = 0; i < V; ++i) sum[i] += p.e[i];
-                }
+            for (int q = 0; q < kWide; ++q)
+#pragma unroll
+                for (int i = 0; i < V; ++i) red[wave][q][i][lane] = sum.v[q][i];
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+                    for (int q = 0; q < kWide; ++q)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) sum.v[q][i] += red[w][q][i][lane];
+                sum.store((T*)a.dtable + (int64_t)k * a.dim, c0 + lane * V, a.dim, a.scale);
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] *= a.scale;
-            store_piece<T, V>(to, col, a.dim, sum);
         }
+        return;
+    }
+    const int64_t waves = (gridDim.x - a.slices) * kWaves, first = (blockIdx.x - a.slices) * kWaves + wave;
+    const int64_t per = (a.rows + waves - 1) / waves, r0 = first * per, r1 = min(r0 + per, a.rows);
+    if (r0 >= r1) return;
+    uint32_t b = a.start[r0], e = a.start[r0 + 1];
+    for (int64_t r = r0; r < r1; ++r) {
+        const uint32_t next = r + 1 < r1 ? a.start[r + 2] : 0;
+        if (e - b <= (uint32_t)a.slice) {
+            for (int c0 = 0; c0 < a.dim; c0 += kCols) {
+                Sum<T> sum;
+                add_tokens<T>(a, a.at[from], b, e, c0 + lane * V, sum);
+                sum.store((T*)a.dtable + r * a.dim, c0 + lane * V, a.dim, a.scale);
+            }
+        }
+        b = e;
+        e = next;
     }
 }
 
@@ -292,16 +358,19 @@ void plan(const gconv_embed_desc* d, Embed* a, Layout* l)
     a->scale = (float)d->scale;
     a->dy_seq = d->dy_stride[0];
     a->dy_tok = d->dy_stride[1];
-    // at most 512 blocks, each of which reads all of their counts
-    int64_t chunk = 2048;
-    while (a->tokens > chunk * 512) chunk *= 2;
+    a->flat = d->sequences == 1 || d->dy_stride[0] == d->tokens * d->dy_stride[1];
+    // at most 256 blocks, each of which reads all of their counts
+    int64_t chunk = 512;
+    while (a->tokens > chunk * 256) chunk *= 2;
     a->chunk = (int)chunk;
     a->blocks = (int)((a->tokens + chunk - 1) / chunk);
-    // a slice about as long as the slices of one token that makes up the text are many
-    int64_t slice = 64;
-    while (slice * slice < a->tokens && slice < 4096) slice *= 2;
+    // four waves add up a long row's slices: a slice a quarter as long as the slices of a token that makes up the text are many
+    int64_t slice = 32;
+    while (slice * slice * 4 < a->tokens && slice < 4096) slice *= 2;
     a->slice = (int)slice;
-    a->slices = (a->tokens + slice - 1) / slice;
+    a->slices = a->tokens > slice ? (a->tokens + slice - 1) / slice : 0;
+    const int64_t cols = 64 * kWide * (d->dtype == GCONV_BF16 ? 8 : 4);
+    a->stretches = (a->dim + cols - 1) / cols;
     Cut cut;
     for (int i = 0; i < 2; ++i) l->key[i] = cut.take(a->tokens * 4);
     for (int i = 0; i < 2; ++i) l->at[i] = cut.take(a->tokens * 4);
@@ -338,9 +407,8 @@ int backward(const gconv_embed_desc* d, Embed a, hipStream_t st)
         from = to;
     }
     embed_starts<<<(unsigned)((a.rows + kThreads) / kThreads), kThreads, 0, st>>>(a, from);
-    if (a.slices > 1) embed_slices<T><<<(unsigned)a.slices, kThreads, 0, st>>>(a, from);
-    const int px = width(a.dim, 16 / (int)sizeof(T)), per = kThreads / px;
-    embed_rows<T><<<(unsigned)std::min<int64_t>((a.rows + per - 1) / per, 1 << 16), kThreads, 0, st>>>(a, from, px);
+    if (a.slices) embed_slices<T><<<(unsigned)((a.slices * a.stretches + kWaves - 1) / kWaves), kThreads, 0, st>>>(a, from);
+    embed_rows<T><<<(unsigned)(a.slices + std::min<int64_t>((a.rows + kWaves - 1) / kWaves, 4096)), kThreads, 0, st>>>(a, from);
     return finish();
 }
 
@@ -406,7 +474,7 @@ int gconv_embed_bwd(const gconv_embed_desc* d, const void* dy, const void* ids, 
     plan(d, &a, &l);
     st = check_workspace(workspace, workspace_bytes, l.bytes);
     if (st != GCONV_OK) return st;
-    if (a.slices > max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
+    if (a.slices + 4096 > max_blocks(kThreads) || a.slices * a.stretches / kWaves >= max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
     char* w = (char*)workspace;
     a.dy = dy;
     a.ids = ids;

@@ -37,13 +37,20 @@ struct Conv {
     int nx;               // workgroups along the channels
 };
 
+// ACT: the activation, or ANY for the one that `act` says.
+constexpr int ANY = -1;
+
+template <int ACT>
 __device__ __forceinline__ float act_of(float p, int act)
 {
+    if (ACT != ANY) act = ACT;
     return act == GCONV_ACT_NONE ? p : act == GCONV_ACT_SIGMOID ? sigmoid_of(p) : p * sigmoid_of(p);
 }
 
+template <int ACT>
 __device__ __forceinline__ float act_grad(float p, int act)
 {
+    if (ACT != ANY) act = ACT;
     if (act == GCONV_ACT_NONE) return 1.f;
     const float s = sigmoid_of(p);
     return act == GCONV_ACT_SIGMOID ? s * (1.f - s) : s * fmaf(p, 1.f - s, 1.f);
@@ -51,7 +58,8 @@ __device__ __forceinline__ float act_grad(float p, int act)
 
 // Where a workgroup's thread works: its piece of channels and its slice.
 struct Place {
-    int col;       // first channel, >= dim: none
+    int col;       // first channel
+    bool live;     // whether there is one
     int64_t slice; // chunk, or (past chunk_blocks) sequence
     bool state;
 };
@@ -62,9 +70,26 @@ __device__ __forceinline__ Place place_of(const Conv& a, int ve)
     const int64_t by = blockIdx.x / a.nx;
     Place p;
     p.col = ((int)(blockIdx.x % a.nx) * a.px + tx) * ve;
+    p.live = p.col < a.dim;
+    // The last piece of a row that is not made of whole ones begins further left:
+    // its first channels are the neighbour's too, and both write the same there.
+    p.col = min(p.col, a.dim - ve);
     p.state = by >= a.chunk_blocks;
     p.slice = (p.state ? by - a.chunk_blocks : by) * cy + ty;
     return p;
+}
+
+// V channels of a row.
+template <typename T, int V>
+__device__ __forceinline__ Packed<T, V> whole_piece(const T* p) { return *(const Packed<T, V>*)p; }
+
+template <typename T, int V>
+__device__ __forceinline__ void put_piece(T* p, const float (&v)[V])
+{
+    Packed<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o.e[e] = (T)v[e];
+    *(Packed<T, V>*)p = o;
 }
 
 template <typename T, int K, int V>
@@ -78,9 +103,9 @@ struct Window {
             const int64_t from = at - (K - 1) + i;
             Packed<T, V> p;
             if (from >= 0) {
-                p = load_piece<T, V>(x + from * tok, col, dim);
+                p = whole_piece<T, V>(x + from * tok + col);
             } else if (init) {
-                p = load_piece<T, V>(init + (from + K - 1) * dim, col, dim);
+                p = whole_piece<T, V>(init + (from + K - 1) * dim + col);
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) p.e[e] = (T)0.f;
@@ -107,12 +132,18 @@ struct Taps {
     float w[K][V], bias[V];
     __device__ __forceinline__ void load(const Conv& a, int col)
     {
+        const T* from = (const T*)a.w + (int64_t)col * K;
+        const Packed<T, V * K> p = *(const Packed<T, V * K>*)from;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const bool in = col + e < a.dim;
 #pragma unroll
-            for (int j = 0; j < K; ++j) w[j][e] = in ? (float)((const T*)a.w)[(int64_t)(col + e) * K + j] : 0.f;
-            bias[e] = in && a.bias ? (float)((const T*)a.bias)[col + e] : 0.f;
+            for (int j = 0; j < K; ++j) w[j][e] = (float)p.e[e * K + j];
+            bias[e] = 0.f;
+        }
+        if (a.bias) {
+            const Packed<T, V> q = whole_piece<T, V>((const T*)a.bias + col);
+#pragma unroll
+            for (int e = 0; e < V; ++e) bias[e] = (float)q.e[e];
         }
     }
     __device__ __forceinline__ float at(const Window<T, K, V>& win, const float (&x)[V], int e) const
@@ -171,11 +202,11 @@ __device__ __forceinline__ const T* sequence(const Conv& a, int64_t n, int64_t* 
     return (const T*)a.x + s0 * a.x_tok;
 }
 
-template <typename T, int K, int V>
+template <typename T, int K, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void conv_fwd(Conv a)
 {
     const Place p = place_of(a, V);
-    if (p.col >= a.dim) return;
+    if (!p.live) return;
     const int64_t held = (int64_t)(K - 1) * a.dim;
     if (p.state) {
         // what the sequence leaves behind: its last K - 1 inputs, of the initial ones where it is shorter
@@ -185,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd(Conv a)
         Window<T, K, V> win;
         win.load(x, a.x_tok, len, a.init ? (const T*)a.init + p.slice * held : nullptr, p.col, a.dim);
 #pragma unroll
-        for (int i = 0; i < K - 1; ++i) store_piece<T, V>((T*)a.final_ + p.slice * held + (int64_t)i * a.dim, p.col, a.dim, win.v[i]);
+        for (int i = 0; i < K - 1; ++i) put_piece<T, V>((T*)a.final_ + p.slice * held + (int64_t)i * a.dim + p.col, win.v[i]);
         return;
     }
     if (p.slice >= a.chunks) return;
@@ -198,36 +229,46 @@ __global__ __launch_bounds__(kThreads) void conv_fwd(Conv a)
          [&](int n, int64_t s0, int64_t, int64_t t0, int64_t t1) {
              Window<T, K, V> win;
              win.load(x + s0 * a.x_tok, a.x_tok, t0 - s0, a.init ? (const T*)a.init + n * held : nullptr, p.col, a.dim);
-             for (int64_t t = t0; t < t1; t += kAhead) {
-                 Packed<T, V> raw[kAhead];
+             Packed<T, V> raw[kAhead], next[kAhead];
+             auto fetch = [&](Packed<T, V>(&to)[kAhead], int64_t t) {
 #pragma unroll
-                 for (int i = 0; i < kAhead; ++i)
-                     raw[i] = load_piece<T, V>(x + min(t + i, t1 - 1) * a.x_tok, p.col, a.dim);
+                 for (int i = 0; i < kAhead; ++i) to[i] = whole_piece<T, V>(x + min(t + i, t1 - 1) * a.x_tok + p.col);
+             };
+             // (without checks the tokens are one stretch of code, through which the window moves by renaming)
+             auto tokens = [&](int64_t t, auto checked) {
 #pragma unroll
                  for (int i = 0; i < kAhead; ++i) {
-                     if (t + i >= t1) break;
+                     if (decltype(checked)::value && t + i >= t1) break;
                      float in[V], out[V];
 #pragma unroll
                      for (int e = 0; e < V; ++e) in[e] = (float)raw[i].e[e];
 #pragma unroll
-                     for (int e = 0; e < V; ++e) out[e] = act_of(taps.at(win, in, e), a.act);
-                     store_piece<T, V>(y + (t + i) * a.dim, p.col, a.dim, out);
+                     for (int e = 0; e < V; ++e) out[e] = act_of<ACT>(taps.at(win, in, e), a.act);
+                     put_piece<T, V>(y + (t + i) * a.dim + p.col, out);
                      win.push(in);
                  }
+             };
+             fetch(raw, t0);
+             for (int64_t t = t0; t < t1; t += kAhead) {
+                 if (t + kAhead < t1) fetch(next, t + kAhead);
+                 if (t + kAhead <= t1) tokens(t, std::false_type{});
+                 else tokens(t, std::true_type{});
+#pragma unroll
+                 for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
              }
          },
          [&](int64_t t0, int64_t t1) {
              const float zero[V] = {};
-             for (int64_t t = t0; t < t1; ++t) store_piece<T, V>(y + t * a.dim, p.col, a.dim, zero);
+             for (int64_t t = t0; t < t1; ++t) put_piece<T, V>(y + t * a.dim + p.col, zero);
          });
 }
 
-template <typename T, int K, int V>
+template <typename T, int K, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
 {
     __shared__ float red[kThreads * V];
     const Place p = place_of(a, V);
-    const bool live = p.col < a.dim;
+    const bool live = p.live;
     const int64_t held = (int64_t)(K - 1) * a.dim;
     Taps<T, K, V> taps;
     taps.load(a, p.col);
@@ -244,13 +285,13 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
 #pragma unroll
         for (int t = 0; t < K - 1; ++t) {
             if (t >= len) break;
-            const Packed<T, V> rx = load_piece<T, V>(x + t * a.x_tok, p.col, a.dim), rd = load_piece<T, V>(dy + t * a.dy_tok, p.col, a.dim);
+            const Packed<T, V> rx = whole_piece<T, V>(x + t * a.x_tok + p.col), rd = whole_piece<T, V>(dy + t * a.dy_tok + p.col);
             float in[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) in[e] = (float)rx.e[e];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float dp = (float)rd.e[e] * act_grad(taps.at(win, in, e), a.act);
+                const float dp = (float)rd.e[e] * act_grad<ACT>(taps.at(win, in, e), a.act);
 #pragma unroll
                 for (int i = 0; i < K - 1; ++i)
                     if (i >= t) g[i][e] = fmaf(taps.w[i >= t ? i - t : 0][e], dp, g[i][e]);
@@ -260,11 +301,11 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
 #pragma unroll
         for (int i = 0; i < K - 1; ++i) {
             if (i >= len && a.dfinal) {
-                const Packed<T, V> r = load_piece<T, V>((const T*)a.dfinal + p.slice * held + (i - len) * a.dim, p.col, a.dim);
+                const Packed<T, V> r = whole_piece<T, V>((const T*)a.dfinal + p.slice * held + (i - len) * a.dim + p.col);
 #pragma unroll
                 for (int e = 0; e < V; ++e) g[i][e] += (float)r.e[e];
             }
-            store_piece<T, V>((T*)a.dinit + p.slice * held + (int64_t)i * a.dim, p.col, a.dim, g[i]);
+            put_piece<T, V>((T*)a.dinit + p.slice * held + (int64_t)i * a.dim + p.col, g[i]);
         }
         return;
     }
@@ -280,23 +321,27 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
                  win.load(x + s0 * a.x_tok, a.x_tok, t0 - s0, a.init ? (const T*)a.init + n * held : nullptr, p.col, a.dim);
                  float acc[K][V] = {};  // [i]: the gradient of token t - i so far
                  const int64_t last = min(t1 + K - 1, s1);
-                 for (int64_t t = t0; t < last; t += kAhead) {
-                     Packed<T, V> rx[kAhead], rd[kAhead];
+                 Packed<T, V> rx[kAhead], rd[kAhead], nx[kAhead], nd[kAhead];
+                 auto fetch = [&](Packed<T, V>(&to_x)[kAhead], Packed<T, V>(&to_d)[kAhead], int64_t t) {
 #pragma unroll
                      for (int i = 0; i < kAhead; ++i) {
-                         rx[i] = load_piece<T, V>(x + min(t + i, last - 1) * a.x_tok, p.col, a.dim);
-                         rd[i] = load_piece<T, V>(dy + min(t + i, last - 1) * a.dy_tok, p.col, a.dim);
+                         to_x[i] = whole_piece<T, V>(x + min(t + i, last - 1) * a.x_tok + p.col);
+                         to_d[i] = whole_piece<T, V>(dy + min(t + i, last - 1) * a.dy_tok + p.col);
                      }
+                 };
+                 // (without checks: tokens of the chunk, each of which completes the gradient of one of the chunk)
+                 auto tokens = [&](int64_t t, auto checked) {
+                     constexpr bool kChecked = decltype(checked)::value;
 #pragma unroll
                      for (int i = 0; i < kAhead; ++i) {
-                         if (t + i >= last) break;
-                         const bool mine = t + i < t1;
+                         if (kChecked && t + i >= last) break;
+                         const bool mine = !kChecked || t + i < t1;
                          float in[V];
 #pragma unroll
                          for (int e = 0; e < V; ++e) in[e] = (float)rx[i].e[e];
 #pragma unroll
                          for (int e = 0; e < V; ++e) {
-                             const float dp = (float)rd[i].e[e] * act_grad(taps.at(win, in, e), a.act);
+                             const float dp = (float)rd[i].e[e] * act_grad<ACT>(taps.at(win, in, e), a.act);
 #pragma unroll
                              for (int j = 0; j < K; ++j) acc[j][e] = fmaf(taps.w[K - 1 - j][e], dp, acc[j][e]);
                              if (mine) {
@@ -306,7 +351,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
                                  db[e] += dp;
                              }
                          }
-                         if (t + i - (K - 1) >= t0) store_piece<T, V>(dx + (t + i - (K - 1)) * a.dim, p.col, a.dim, acc[K - 1]);
+                         if (!kChecked || t + i - (K - 1) >= t0) put_piece<T, V>(dx + (t + i - (K - 1)) * a.dim + p.col, acc[K - 1]);
 #pragma unroll
                          for (int j = K - 1; j > 0; --j)
 #pragma unroll
@@ -314,6 +359,17 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
 #pragma unroll
                          for (int e = 0; e < V; ++e) acc[0][e] = 0.f;
                          win.push(in);
+                     }
+                 };
+                 fetch(rx, rd, t0);
+                 for (int64_t t = t0; t < last; t += kAhead) {
+                     if (t + kAhead < last) fetch(nx, nd, t + kAhead);
+                     if (t - (K - 1) >= t0 && t + kAhead <= t1) tokens(t, std::false_type{});
+                     else tokens(t, std::true_type{});
+#pragma unroll
+                     for (int i = 0; i < kAhead; ++i) {
+                         rx[i] = nx[i];
+                         rd[i] = nd[i];
                      }
                  }
                  // the sequence's last tokens, which fewer read and which it leaves behind
@@ -323,17 +379,17 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
                          const int64_t t = last - i;
                          if (t < t0 || t >= t1) continue;
                          if (a.dfinal) {
-                             const Packed<T, V> r = load_piece<T, V>((const T*)a.dfinal + n * held + (int64_t)(K - 1 - i) * a.dim, p.col, a.dim);
+                             const Packed<T, V> r = whole_piece<T, V>((const T*)a.dfinal + n * held + (int64_t)(K - 1 - i) * a.dim + p.col);
 #pragma unroll
                              for (int e = 0; e < V; ++e) acc[i][e] += (float)r.e[e];
                          }
-                         store_piece<T, V>(dx + t * a.dim, p.col, a.dim, acc[i]);
+                         put_piece<T, V>(dx + t * a.dim + p.col, acc[i]);
                      }
                  }
              },
              [&](int64_t t0, int64_t t1) {
                  const float zero[V] = {};
-                 for (int64_t t = t0; t < t1; ++t) store_piece<T, V>(dx + t * a.dim, p.col, a.dim, zero);
+                 for (int64_t t = t0; t < t1; ++t) put_piece<T, V>(dx + t * a.dim + p.col, zero);
              });
     }
     // the workgroup's chunks, in order
@@ -351,7 +407,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(Conv a)
             for (int q = 1; q < cy; ++q)
 #pragma unroll
                 for (int e = 0; e < V; ++e) s[e] += red[(q * a.px + tx) * V + e];
-            store_piece<float, V>(part + (int64_t)row * a.dim, p.col, a.dim, s);
+            put_piece<float, V>(part + (int64_t)row * a.dim + p.col, s);
         }
     };
 #pragma unroll
@@ -397,11 +453,12 @@ struct Step {
     int dim, act;
 };
 
-// One token of each sequence: the state moves up by one input, in place.
+// One token of each sequence: the state moves up by one input, in place. (Rows
+// are whole pieces: two that met would read what the other wrote.)
 template <typename T, int K, int V>
 __global__ __launch_bounds__(kThreads) void conv_step(Step a)
 {
-    const int pieces = (a.dim + V - 1) / V;
+    const int pieces = a.dim / V;
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x, i = id / pieces;
     if (i >= a.batch) return;
     const int col = (int)(id - i * pieces) * V;
@@ -409,7 +466,7 @@ __global__ __launch_bounds__(kThreads) void conv_step(Step a)
     const int64_t slot = a.slots ? a.slots[i] : i;
     if (slot < 0 || slot >= a.num_slots) {
         const float zero[V] = {};
-        store_piece<T, V>(y, col, a.dim, zero);
+        put_piece<T, V>(y + col, zero);
         return;
     }
     Conv c{};
@@ -419,18 +476,18 @@ __global__ __launch_bounds__(kThreads) void conv_step(Step a)
     T* state = (T*)a.state + slot * (K - 1) * a.dim;
     Window<T, K, V> win;
     win.load(state, a.dim, K - 1, nullptr, col, a.dim);
-    const Packed<T, V> raw = load_piece<T, V>((const T*)a.x + i * a.x_stride, col, a.dim);
+    const Packed<T, V> raw = whole_piece<T, V>((const T*)a.x + i * a.x_stride + col);
     Taps<T, K, V> taps;
     taps.load(c, col);
     float in[V], out[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) in[e] = (float)raw.e[e];
 #pragma unroll
-    for (int e = 0; e < V; ++e) out[e] = act_of(taps.at(win, in, e), a.act);
-    store_piece<T, V>(y, col, a.dim, out);
+    for (int e = 0; e < V; ++e) out[e] = act_of<ANY>(taps.at(win, in, e), a.act);
+    put_piece<T, V>(y + col, out);
     win.push(in);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) store_piece<T, V>(state + (int64_t)j * a.dim, col, a.dim, win.v[j]);
+    for (int j = 0; j < K - 1; ++j) put_piece<T, V>(state + (int64_t)j * a.dim + col, win.v[j]);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -458,20 +515,30 @@ int check_desc(const gconv_shortconv_desc* d)
 int64_t outer_of(const gconv_shortconv_desc* d) { return d->packed ? 1 : d->sequences; }
 int64_t rows_of(const gconv_shortconv_desc* d) { return outer_of(d) * d->tokens; }
 
-// Channels a thread holds: 16 bytes, half of that where more than four taps of bf16 would not fit the registers.
-int piece_of(const gconv_shortconv_desc* d) { return d->dtype == GCONV_BF16 && d->taps <= 4 ? 8 : 4; }
+enum Use { FORWARD, BACKWARD, STEP };
+
+// Channels a thread holds: 16 bytes; of bf16 half of that backward, where it
+// holds five values of each channel for a tap (330 registers for 8 channels and
+// four taps), and with more than four taps. One where a row has not as many (or,
+// in place, is not made of whole ones).
+int piece_of(const gconv_shortconv_desc* d, Use use)
+{
+    const int v = d->dtype == GCONV_BF16 && d->taps <= 4 && use != BACKWARD ? 8 : 4;
+    return use == STEP ? (d->dim % v == 0 ? v : 1) : (d->dim >= v ? v : 1);
+}
 
 // The launch: as long chunks as leave enough threads (a chunk's first K - 1
 // tokens are read by two).
-void plan(const gconv_shortconv_desc* d, bool states, int longest, Conv* a)
+void plan(const gconv_shortconv_desc* d, Use use, bool states, int longest, Conv* a)
 {
-    const int64_t pieces = (d->dim + piece_of(d) - 1) / piece_of(d);
+    const int v = piece_of(d, use);
+    const int64_t pieces = (d->dim + v - 1) / v;
     int px = 1;
     while (px < 64 && px < pieces) px *= 2;
     a->px = px;
     a->nx = (int)((pieces + px - 1) / px);
     int chunk = longest;
-    while (chunk > 4 && pieces * outer_of(d) * ((d->tokens + chunk - 1) / chunk) < (int64_t)1 << 17) chunk /= 2;
+    while (chunk > 4 && pieces * outer_of(d) * ((d->tokens + chunk - 1) / chunk) < (int64_t)1 << 18) chunk /= 2;
     a->chunk = chunk;
     a->per = std::max<int64_t>(1, (d->tokens + chunk - 1) / chunk);
     a->chunks = d->tokens > 0 ? outer_of(d) * a->per : 0;
@@ -488,7 +555,7 @@ void plan(const gconv_shortconv_desc* d, bool states, int longest, Conv* a)
     a->dy_tok = d->dy_stride[1];
 }
 
-constexpr int kFwdChunk = 64, kBwdChunk = 64;
+constexpr int kFwdChunk = 32, kBwdChunk = 32;
 
 int check_blocks(const Conv& a)
 {
@@ -496,7 +563,7 @@ int check_blocks(const Conv& a)
     return blocks > max_blocks(kThreads) ? fail(GCONV_ERR_UNSUPPORTED, "too many rows") : GCONV_OK;
 }
 
-template <typename T, int V, typename F>
+template <typename F>
 void by_taps(int taps, F f)
 {
     switch (taps) {
@@ -511,15 +578,18 @@ void by_taps(int taps, F f)
     }
 }
 
-// f(type, taps, channels a thread) for the descriptor's.
-template <typename F>
-void by_kind(const gconv_shortconv_desc* d, F f)
+// f(type, taps, channels a thread, activation) for the descriptor's. (SiLU has
+// kernels of its own; so few channels that a thread takes one do without.)
+template <Use USE, typename F>
+void by_kind(const gconv_shortconv_desc* d, int v, F f)
 {
-    if (d->dtype == GCONV_F32) by_taps<float, 4>((int)d->taps, [&](auto k) { f(0.f, k, std::integral_constant<int, 4>{}); });
-    else
-        by_taps<__bf16, 8>((int)d->taps, [&](auto k) {
-            f((__bf16)0.f, k, std::integral_constant<int, (decltype(k)::value <= 4 ? 8 : 4)>{});
-        });
+    auto pick = [&](auto t, auto k, auto most) {
+        if (v == 1) f(t, k, std::integral_constant<int, 1>{}, std::integral_constant<int, ANY>{});
+        else if (d->act == GCONV_ACT_SILU) f(t, k, most, std::integral_constant<int, GCONV_ACT_SILU>{});
+        else f(t, k, most, std::integral_constant<int, ANY>{});
+    };
+    if (d->dtype == GCONV_F32) by_taps((int)d->taps, [&](auto k) { pick(0.f, k, std::integral_constant<int, 4>{}); });
+    else by_taps((int)d->taps, [&](auto k) { pick((__bf16)0.f, k, std::integral_constant<int, (decltype(k)::value <= 4 && USE != BACKWARD ? 8 : 4)>{}); });
 }
 
 }  // namespace
@@ -535,7 +605,7 @@ int gconv_shortconv_workspace_size(const gconv_shortconv_desc* d, size_t* bytes)
     if (st != GCONV_OK) return st;
     if (!bytes) return fail(GCONV_ERR_NULL, "bytes pointer is NULL");
     Conv a{};
-    plan(d, true, kBwdChunk, &a);
+    plan(d, BACKWARD, true, kBwdChunk, &a);
     *bytes = (size_t)a.chunk_blocks * (d->taps + 1) * d->dim * 4;
     return GCONV_OK;
 }
@@ -554,7 +624,7 @@ int gconv_shortconv_fwd(const gconv_shortconv_desc* d, const void* x, const void
     st = check_overlap(in, out);
     if (st != GCONV_OK) return st;
     Conv a{};
-    plan(d, final_state && d->taps > 1, kFwdChunk, &a);
+    plan(d, FORWARD, final_state && d->taps > 1, kFwdChunk, &a);
     st = check_blocks(a);
     if (st != GCONV_OK) return st;
     a.x = x;
@@ -567,8 +637,8 @@ int gconv_shortconv_fwd(const gconv_shortconv_desc* d, const void* x, const void
     (void)hipGetLastError();
     const int64_t blocks = (a.chunk_blocks + a.state_blocks) * a.nx;
     if (blocks > 0)
-        by_kind(d, [&](auto t, auto k, auto v) {
-            conv_fwd<decltype(t), decltype(k)::value, decltype(v)::value><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a);
+        by_kind<FORWARD>(d, piece_of(d, FORWARD), [&](auto t, auto k, auto v, auto act) {
+            conv_fwd<decltype(t), decltype(k)::value, decltype(v)::value, decltype(act)::value><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a);
         });
     return finish();
 }
@@ -591,7 +661,7 @@ int gconv_shortconv_bwd(const gconv_shortconv_desc* d, const void* dy, const voi
     st = check_overlap(in, out);
     if (st != GCONV_OK) return st;
     Conv a{};
-    plan(d, d_initial_state && d->taps > 1, kBwdChunk, &a);
+    plan(d, BACKWARD, d_initial_state && d->taps > 1, kBwdChunk, &a);
     st = check_blocks(a);
     if (st != GCONV_OK) return st;
     st = check_workspace(workspace, workspace_bytes, (size_t)a.chunk_blocks * (d->taps + 1) * d->dim * 4);
@@ -610,8 +680,8 @@ int gconv_shortconv_bwd(const gconv_shortconv_desc* d, const void* dy, const voi
     hipStream_t hs = (hipStream_t)stream;
     const int64_t blocks = (a.chunk_blocks + a.state_blocks) * a.nx;
     if (blocks > 0)
-        by_kind(d, [&](auto t, auto k, auto v) {
-            conv_bwd<decltype(t), decltype(k)::value, decltype(v)::value><<<(unsigned)blocks, kThreads, 0, hs>>>(a);
+        by_kind<BACKWARD>(d, piece_of(d, BACKWARD), [&](auto t, auto k, auto v, auto act) {
+            conv_bwd<decltype(t), decltype(k)::value, decltype(v)::value, decltype(act)::value><<<(unsigned)blocks, kThreads, 0, hs>>>(a);
         });
     const dim3 grid((unsigned)((d->dim + 63) / 64), (unsigned)d->taps + (bias ? 1 : 0));
     if (d->dtype == GCONV_BF16) conv_fold<__bf16><<<grid, 1024, 0, hs>>>(a.part, a.chunk_blocks, (int)d->taps, a.dim, (__bf16*)dw, (__bf16*)dbias);
@@ -636,13 +706,13 @@ int gconv_shortconv_step(const gconv_shortconv_desc* d, const void* x, const voi
     const Span out[] = {{state, num_slots * (d->taps - 1) * d->dim * es}, {y, d->sequences * d->dim * es}};
     st = check_overlap(in, out);
     if (st != GCONV_OK) return st;
-    const int v = piece_of(d);
-    const int64_t threads = d->sequences * ((d->dim + v - 1) / v), blocks = (threads + kThreads - 1) / kThreads;
+    const int v = piece_of(d, STEP);
+    const int64_t threads = d->sequences * (d->dim / v), blocks = (threads + kThreads - 1) / kThreads;
     if (blocks > max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many rows");
     (void)hipGetLastError();
     if (blocks > 0) {
         const Step a{x, w, bias, state, y, slots, d->x_stride[0], num_slots, d->sequences, (int)d->dim, (int)d->act};
-        by_kind(d, [&](auto t, auto k, auto vv) {
+        by_kind<STEP>(d, v, [&](auto t, auto k, auto vv, auto) {
             conv_step<decltype(t), decltype(k)::value, decltype(vv)::value><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a);
         });
     }
