@@ -186,37 +186,45 @@ __global__ __launch_bounds__(kThreads) void embed_starts(Embed a, int from)
 
 // ---- sums -------------------------------------------------------------------------
 
-constexpr int kWide = 4;  // pieces of a row that a lane holds at once
-
-// A lane's pieces of a row, 64 lanes' side by side: from column `col`.
-template <typename T>
+// A lane's pieces of a row: V columns each, W of them, 64 lanes' side by side. No
+// branches: a piece that would end past the row begins further left (or is the
+// row's last once more), so that the rows of many tokens load side by side; what
+// two lanes hold twice is the same and they write the same.
+template <int V, int W>
 struct Sum {
-    static constexpr int V = 16 / sizeof(T);
-    float v[kWide][V] = {};
+    float v[W][V] = {};
     template <typename U>
-    __device__ __forceinline__ void add(const U* row, int col, int dim)
+    __device__ __forceinline__ void add(const U* row, const int (&col)[W])
     {
+        Packed<U, V> p[W];
 #pragma unroll
-        for (int k = 0; k < kWide; ++k) {
-            if (col + k * 64 * V >= dim) break;
-            const Packed<U, V> p = load_piece<U, V>(row, col + k * 64 * V, dim);
+        for (int k = 0; k < W; ++k) p[k] = *(const Packed<U, V>*)(row + col[k]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[k][e] += (float)p.e[e];
-        }
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[k][e] += (float)p[k].e[e];
     }
+    // first: the column of the lane's first piece, before any was moved
     template <typename U>
-    __device__ __forceinline__ void store(U* row, int col, int dim, float scale) const
+    __device__ __forceinline__ void store(U* row, const int (&col)[W], int first, int dim, float scale) const
     {
 #pragma unroll
-        for (int k = 0; k < kWide; ++k) {
-            if (col + k * 64 * V >= dim) break;
-            float o[V];
+        for (int k = 0; k < W; ++k) {
+            if (first + k * 64 * V >= dim) break;
+            Packed<U, V> o;
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = v[k][e] * scale;
-            store_piece<U, V>(row, col + k * 64 * V, dim, o);
+            for (int e = 0; e < V; ++e) o.e[e] = (U)(v[k][e] * scale);
+            *(Packed<U, V>*)(row + col[k]) = o;
         }
     }
 };
+
+template <int V, int W>
+__device__ __forceinline__ void columns(int first, int dim, int (&col)[W])
+{
+#pragma unroll
+    for (int k = 0; k < W; ++k) col[k] = min(first + k * 64 * V, dim - V);
+}
 
 // dy's row of a token.
 template <typename T>
@@ -227,29 +235,48 @@ __device__ __forceinline__ const T* dy_row(const Embed& a, uint32_t t)
     return (const T*)a.dy + n * a.dy_seq + (int64_t)(t - n * (uint32_t)a.per_seq) * a.dy_tok;
 }
 
-// Adds dy of the tokens at places [p0, p1), whose numbers the lanes read 64 at a time.
-template <typename T>
-__device__ __forceinline__ void add_tokens(const Embed& a, const uint32_t* at, uint32_t p0, uint32_t p1, int col, Sum<T>& sum)
+// Adds dy of the tokens at places [p0, p1), whose numbers the lanes read 64 at a
+// time, eight tokens' rows under way at once.
+template <typename T, int V, int W>
+__device__ __forceinline__ void add_tokens(const Embed& a, const uint32_t* at, uint32_t p0, uint32_t p1, const int (&col)[W], Sum<V, W>& sum)
 {
     const int lane = threadIdx.x & 63;
     for (uint32_t p = p0; p < p1; p += 64) {
         const uint32_t mine = at[min(p + lane, p1 - 1)];
         const int n = (int)min(p1 - p, 64u);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) sum.add(dy_row<T>(a, __builtin_amdgcn_readlane(mine, i)), col, a.dim);
+        constexpr int U = 8;
+        int i = 0;
+        for (; i + U <= n; i += U) {
+            Packed<T, V> r[U][W];
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                const T* row = dy_row<T>(a, __builtin_amdgcn_readlane(mine, i + q));
+#pragma unroll
+                for (int k = 0; k < W; ++k) r[q][k] = *(const Packed<T, V>*)(row + col[k]);
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) sum.v[k][e] += (float)r[q][k].e[e];
+        }
+        for (; i < n; ++i) sum.add(dy_row<T>(a, __builtin_amdgcn_readlane(mine, i)), col);
     }
 }
 
 // The slices' sums of rows with more tokens than a slice has: such a row runs
 // into a slice, out of it, or both. A wave a slice and stretch of columns.
-template <typename T>
+template <typename T, int V, int W>
 __global__ __launch_bounds__(kThreads) void embed_slices(Embed a, int from)
 {
-    constexpr int kCols = 64 * kWide * Sum<T>::V;
+    constexpr int kCols = 64 * W * V;
     const int lane = threadIdx.x & 63;
     const int64_t id = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), s = id / a.stretches;
     if (s >= a.slices) return;
-    const int col = (int)(id - s * a.stretches) * kCols + lane * Sum<T>::V;
+    const int c0 = (int)(id - s * a.stretches) * kCols + lane * V;
+    int col[W];
+    columns<V, W>(c0, a.dim, col);
     const uint32_t p0 = (uint32_t)(s * a.slice), p1 = (uint32_t)min(s * a.slice + a.slice, a.tokens);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
@@ -257,9 +284,9 @@ __global__ __launch_bounds__(kThreads) void embed_slices(Embed a, int from)
         if (k >= a.rows) continue;
         const uint32_t b = a.start[k], e = a.start[k + 1];
         if (e - b <= (uint32_t)a.slice || (which == 0 ? b > p0 : b <= p0)) continue;
-        Sum<T> sum;
-        add_tokens<T>(a, a.at[from], max(b, p0), min(e, p1), col, sum);
-        sum.store(a.part + (s * 2 + which) * a.dim, col, a.dim, 1.f);
+        Sum<V, W> sum;
+        add_tokens<T, V, W>(a, a.at[from], max(b, p0), min(e, p1), col, sum);
+        sum.store(a.part + (s * 2 + which) * a.dim, col, c0, a.dim, 1.f);
     }
 }
 
@@ -267,13 +294,13 @@ __global__ __launch_bounds__(kThreads) void embed_slices(Embed a, int from)
 // one's tokens looked up while one is written. The first workgroups take the rows
 // with more tokens than a slice has, each that of the slice in which it begins,
 // from the slices' sums: a quarter of them a wave, then the quarters.
-template <typename T>
+template <typename T, int V, int W>
 __global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from)
 {
-    constexpr int V = Sum<T>::V, kCols = 64 * kWide * V;
+    constexpr int kCols = 64 * W * V;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x < a.slices) {
-        __shared__ float red[kWaves][kWide][V][64];
+        __shared__ float red[kWaves][W][V][64];
         const int64_t s0 = blockIdx.x;
         const uint32_t p0 = (uint32_t)(s0 * a.slice), p1 = (uint32_t)min(s0 * a.slice + a.slice, a.tokens);
         const uint32_t k = a.key[from][p1 - 1];
@@ -282,14 +309,15 @@ __global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from)
         if (e - b <= (uint32_t)a.slice || b < p0) return;
         const int64_t s1 = (e - 1) / a.slice + 1, per = (s1 - s0 + kWaves - 1) / kWaves;
         for (int c0 = 0; c0 < a.dim; c0 += kCols) {
-            Sum<T> sum;
+            Sum<V, W> sum;
+            int col[W];
+            columns<V, W>(c0 + lane * V, a.dim, col);
             const int64_t from_s = s0 + wave * per, to_s = min(from_s + per, s1);
 #pragma unroll 4
-            for (int64_t s = from_s; s < to_s; ++s)
-                sum.add(a.part + (s * 2 + (b > s * a.slice ? 1 : 0)) * a.dim, c0 + lane * V, a.dim);
+            for (int64_t s = from_s; s < to_s; ++s) sum.add(a.part + (s * 2 + (b > s * a.slice ? 1 : 0)) * a.dim, col);
             __syncthreads();
 #pragma unroll
-            for (int q = 0; q < kWide; ++q)
+            for (int q = 0; q < W; ++q)
 #pragma unroll
                 for (int i = 0; i < V; ++i) red[wave][q][i][lane] = sum.v[q][i];
             __syncthreads();
@@ -297,10 +325,10 @@ __global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from)
 #pragma unroll
                 for (int w = 1; w < kWaves; ++w)
 #pragma unroll
-                    for (int q = 0; q < kWide; ++q)
+                    for (int q = 0; q < W; ++q)
 #pragma unroll
                         for (int i = 0; i < V; ++i) sum.v[q][i] += red[w][q][i][lane];
-                sum.store((T*)a.dtable + (int64_t)k * a.dim, c0 + lane * V, a.dim, a.scale);
+                sum.store((T*)a.dtable + (int64_t)k * a.dim, col, c0 + lane * V, a.dim, a.scale);
             }
         }
         return;
@@ -313,9 +341,11 @@ __global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from)
         const uint32_t next = r + 1 < r1 ? a.start[r + 2] : 0;
         if (e - b <= (uint32_t)a.slice) {
             for (int c0 = 0; c0 < a.dim; c0 += kCols) {
-                Sum<T> sum;
-                add_tokens<T>(a, a.at[from], b, e, c0 + lane * V, sum);
-                sum.store((T*)a.dtable + r * a.dim, c0 + lane * V, a.dim, a.scale);
+                Sum<V, W> sum;
+                int col[W];
+                columns<V, W>(c0 + lane * V, a.dim, col);
+                add_tokens<T, V, W>(a, a.at[from], b, e, col, sum);
+                sum.store((T*)a.dtable + r * a.dim, col, c0 + lane * V, a.dim, a.scale);
             }
         }
         b = e;
@@ -344,6 +374,15 @@ int check_desc(const gconv_embed_desc* d)
     return GCONV_OK;
 }
 
+// Columns of a lane's piece (16 bytes, or one where a row has not as many) and
+// pieces of a lane.
+void pieces(const gconv_embed_desc* d, int* v, int* w)
+{
+    const int most = d->dtype == GCONV_BF16 ? 8 : 4;
+    *v = d->dim >= most ? most : 1;
+    *w = d->dim <= 64 * *v ? 1 : 2;
+}
+
 struct Layout {
     size_t key[2], at[2], counts, start, part, bytes;
 };
@@ -369,8 +408,9 @@ void plan(const gconv_embed_desc* d, Embed* a, Layout* l)
     while (slice * slice * 4 < a->tokens && slice < 4096) slice *= 2;
     a->slice = (int)slice;
     a->slices = a->tokens > slice ? (a->tokens + slice - 1) / slice : 0;
-    const int64_t cols = 64 * kWide * (d->dtype == GCONV_BF16 ? 8 : 4);
-    a->stretches = (a->dim + cols - 1) / cols;
+    int v, w;
+    pieces(d, &v, &w);
+    a->stretches = (a->dim + 64 * v * w - 1) / (64 * v * w);
     Cut cut;
     for (int i = 0; i < 2; ++i) l->key[i] = cut.take(a->tokens * 4);
     for (int i = 0; i < 2; ++i) l->at[i] = cut.take(a->tokens * 4);
@@ -407,8 +447,19 @@ int backward(const gconv_embed_desc* d, Embed a, hipStream_t st)
         from = to;
     }
     embed_starts<<<(unsigned)((a.rows + kThreads) / kThreads), kThreads, 0, st>>>(a, from);
-    if (a.slices) embed_slices<T><<<(unsigned)((a.slices * a.stretches + kWaves - 1) / kWaves), kThreads, 0, st>>>(a, from);
-    embed_rows<T><<<(unsigned)(a.slices + std::min<int64_t>((a.rows + kWaves - 1) / kWaves, 4096)), kThreads, 0, st>>>(a, from);
+    const unsigned slices = (unsigned)((a.slices * a.stretches + kWaves - 1) / kWaves);
+    const unsigned rows = (unsigned)(a.slices + std::min<int64_t>((a.rows + kWaves - 1) / kWaves, 4096));
+    auto sums = [&](auto v, auto w) {
+        constexpr int V = decltype(v)::value, W = decltype(w)::value;
+        if (slices) embed_slices<T, V, W><<<slices, kThreads, 0, st>>>(a, from);
+        embed_rows<T, V, W><<<rows, kThreads, 0, st>>>(a, from);
+    };
+    int v, w;
+    pieces(d, &v, &w);
+    constexpr std::integral_constant<int, 16 / sizeof(T)> most;
+    if (v == 1) sums(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    else if (w == 1) sums(most, std::integral_constant<int, 1>{});
+    else sums(most, std::integral_constant<int, 2>{});
     return finish();
 }
 
