@@ -49,27 +49,29 @@ __device__ __forceinline__ uint32_t key_of(const Embed& a, int64_t t)
     return id >= 0 && id < a.rows ? (uint32_t)id : (uint32_t)a.rows;
 }
 
-template <typename T>
+// A thread: a piece of V columns (the last of a row begins further left where it
+// would end past it) of R tokens, whose rows are under way together.
+template <typename T, int V, int R>
 __global__ __launch_bounds__(kThreads) void embed_fwd(Embed a, int px)
 {
-    constexpr int V = 16 / sizeof(T);
-    const int rows = kThreads / px, tx = threadIdx.x % px, ty = threadIdx.x / px;
-    const int64_t t = (int64_t)blockIdx.x * rows + ty;
-    if (t >= a.tokens) return;
-    const uint32_t id = key_of(a, t);
-    const T* from = (const T*)a.table + (int64_t)id * a.dim;
-    T* to = (T*)a.y + t * a.dim;
-    for (int col = tx * V; col < a.dim; col += px * V) {
-        float v[V];
-        if (id < a.rows) {
-            const Packed<T, V> p = load_piece<T, V>(from, col, a.dim);
+    const int per = kThreads / px, tx = threadIdx.x % px, ty = threadIdx.x / px;
+    const int64_t t0 = (int64_t)blockIdx.x * per * R + ty;
+    uint32_t id[R];
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = a.scale * (float)p.e[e];
-        } else {
+    for (int i = 0; i < R; ++i) id[i] = t0 + i * per < a.tokens ? key_of(a, t0 + i * per) : (uint32_t)a.rows;
+    for (int first = tx * V; first < a.dim; first += px * V) {
+        const int col = min(first, a.dim - V);
+        Packed<T, V> p[R];
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = 0.f;
+        for (int i = 0; i < R; ++i) p[i] = *(const Packed<T, V>*)((const T*)a.table + (int64_t)(id[i] < a.rows ? id[i] : 0) * a.dim + col);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (t0 + i * per >= a.tokens) break;
+            Packed<T, V> o;
+#pragma unroll
+            for (int e = 0; e < V; ++e) o.e[e] = id[i] < a.rows ? (T)(a.scale * (float)p[i].e[e]) : (T)0.f;
+            *(Packed<T, V>*)((T*)a.y + (t0 + i * per) * a.dim + col) = o;
         }
-        store_piece<T, V>(to, col, a.dim, v);
     }
 }
 
@@ -498,13 +500,25 @@ int gconv_embed_fwd(const gconv_embed_desc* d, const void* table, const void* id
     a.table = table;
     a.ids = ids;
     a.y = y;
-    const int px = width(d->dim, 16 / es), per = kThreads / px;
-    const int64_t blocks = (tokens + per - 1) / per;
+    int v, w;
+    pieces(d, &v, &w);
+    const int px = width(d->dim, v), per = kThreads / px;
+    // four tokens a thread where that leaves every CU several workgroups (16384 tokens of 2048: 40 us by one, 24 by four)
+    const int r = v > 1 && tokens / per >= 4 * 2048 ? 4 : 1;
+    const int64_t blocks = (tokens + per * r - 1) / (per * r);
     if (blocks > max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
     (void)hipGetLastError();
     if (blocks > 0) {
-        if (d->dtype == GCONV_BF16) embed_fwd<__bf16><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a, px);
-        else embed_fwd<float><<<(unsigned)blocks, kThreads, 0, (hipStream_t)stream>>>(a, px);
+        auto go = [&](auto t, auto most) {
+            using T = decltype(t);
+            constexpr int V = decltype(most)::value;
+            hipStream_t st = (hipStream_t)stream;
+            if (v == 1) embed_fwd<T, 1, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a, px);
+            else if (r == 1) embed_fwd<T, V, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a, px);
+            else embed_fwd<T, V, 4><<<(unsigned)blocks, kThreads, 0, st>>>(a, px);
+        };
+        if (d->dtype == GCONV_BF16) go((__bf16)0.f, std::integral_constant<int, 8>{});
+        else go(0.f, std::integral_constant<int, 4>{});
     }
     return finish();
 }

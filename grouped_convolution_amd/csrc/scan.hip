@@ -59,6 +59,8 @@ struct Scan {
     float* adds;        // the same of the adjoint; later that after each chunk
     float* sums;        // [chunks][blocks][64]: sum of dt
     int32_t* breaks;    // [chunks]: whether a sequence begins in it
+    float* hist;        // backward, [places / kBack][blocks][NW][4][64]: states before every kBack tokens, from 0 before the chunk
+    float* hist_sum;    // [places / kBack][blocks][64]: sum of dt since the chunk's start; not a number where a sequence has begun since
     float* part_a;      // [chunks][blocks][NW][4][64]: of da
     float* part_d;      // [chunks][2][dim]: of dskip and ddt_bias
     float* part_bc;     // [blocks of a group][groups][NW][places][8]: of db and dc
@@ -100,14 +102,14 @@ __device__ __forceinline__ Where where(const Scan& a)
     return w;
 }
 
-// softplus(x) = max(x, 0) + log(1 + w), w = exp(-|x|). The logarithm of 1 + w as
-// it was rounded, times w over what was added: right to the last bits however
-// small w is.
+// softplus(x) = max(x, 0) + log(1 + w), w = exp(-|x|): the logarithm of 1 + w as
+// it was rounded, and what the rounding left of w (at most 2^-24, where w is near
+// 1 and half as much would be right; exact where w is small), so right to the last
+// bits however small w is.
 __device__ __forceinline__ float softplus_of(float x)
 {
-    const float w = __builtin_amdgcn_exp2f(fabsf(x) * -kLog2e), v = 1.f + w, d = v - 1.f;
-    const float l = d == 0.f ? w : __builtin_amdgcn_logf(v) * (kLn2 * w) * __builtin_amdgcn_rcpf(d);
-    return fmaxf(x, 0.f) + l;
+    const float w = __builtin_amdgcn_exp2f(fabsf(x) * -kLog2e), v = 1.f + w;
+    return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(v), kLn2, w - (v - 1.f));
 }
 
 template <typename T>
@@ -173,6 +175,15 @@ __global__ __launch_bounds__(256) void scan_empty(Sequences seq, const float* fr
 // Read-only while the kernel runs, at an address that is the same for a wave: scalar loads.
 typedef const __attribute__((address_space(4))) float* scalar_floats;
 
+// The kernel's arguments, read again: what only tokens with marks ask for does not
+// stay in scalar registers, of which the rest of the kernel has need.
+__device__ __forceinline__ const __attribute__((address_space(4))) Scan* again()
+{
+    auto p = (const __attribute__((address_space(4))) Scan*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
 // The states of lane's channel that its wave holds.
 struct Mine {
     int lane, wave;
@@ -195,18 +206,18 @@ struct Mine {
     // p[n][dim][states] of sequence n, or 0: no branches, a state that does not
     // exist is read (and written) past the resource's end
     __device__ __forceinline__ uint32_t offset(int s) const { return s < have ? (uint32_t)(at + s) * 4 : kOOB; }
-    __device__ __forceinline__ f4 get(const Scan& a, const float* p, int64_t n) const
+    __device__ __forceinline__ f4 get(int dim, int states, const float* p, int64_t n) const
     {
-        const int64_t size = (int64_t)a.dim * a.states;
+        const int64_t size = (int64_t)dim * states;
         const __amdgpu_buffer_rsrc_t r = make_rsrc(p + (p ? n * size : 0), p ? (uint32_t)size * 4 : 0);
         f4 v;
 #pragma unroll
         for (int s = 0; s < kSpw; ++s) v[s] = load_f32(r, offset(s));
         return v;
     }
-    __device__ __forceinline__ void put(const Scan& a, float* p, int64_t n, f4 v) const
+    __device__ __forceinline__ void put(int dim, int states, float* p, int64_t n, f4 v) const
     {
-        const int64_t size = (int64_t)a.dim * a.states;
+        const int64_t size = (int64_t)dim * states;
         const __amdgpu_buffer_rsrc_t r = make_rsrc(p + (p ? n * size : 0), p ? (uint32_t)size * 4 : 0);
 #pragma unroll
         for (int s = 0; s < kSpw; ++s) store_f32(r, offset(s), v[s]);
@@ -304,7 +315,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     const int quad = threadIdx.x & 15;
     const f4 bias = channel_quad(a.dt_bias, w, quad), skip = channel_quad(a.skip, w, quad);
 
-    f4 a2 = m.get(a, a.a, 0) * kLog2e;
+    f4 a2 = m.get(a.dim, a.states, a.a, 0) * kLog2e;
     f4 h = {0, 0, 0, 0}, p = {1, 1, 1, 1}, r = {0, 0, 0, 0};
     float total = 0.f;
     int broken = 0;
@@ -364,8 +375,14 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
             const uint32_t firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kTile) - 1);
             const uint32_t lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kTile) - 1);
             auto token = [&](int i, auto marked) {
+                if (ADJ && i % kBack == 0) {
+                    const int64_t at = ((w.place0 + tile * kTile + i) / kBack * a.blocks + w.block);
+#pragma unroll
+                    for (int s = 0; s < kSpw; ++s) a.hist[((at * NW + m.wave) * kSpw + s) * kLanes + m.lane] = h[s];
+                    if (m.wave == 0) a.hist_sum[at * kLanes + m.lane] = broken ? __builtin_nanf("") : total;
+                }
                 if (decltype(marked)::value && (firsts >> i & 1)) {
-                    h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
+                    h = m.get(again()->dim, again()->states, again()->init, __builtin_amdgcn_readlane(mk, i) >> 2);
                     p = f4{0, 0, 0, 0};
                     broken = 1;
                 }
@@ -387,8 +404,8 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
                 if (OUT) yp[tile & 1][OUT ? m.wave : 0][OUT ? i : 0][m.lane] = y;
                 if (decltype(marked)::value && (lasts >> i & 1)) {
                     const int n = __builtin_amdgcn_readlane(mk, i) >> 2;
-                    if (OUT && a.final_) m.put(a, a.final_, n, h);
-                    if (ADJ && a.dfinal) r += p * m.get(a, a.dfinal, n);
+                    if (OUT && again()->final_) m.put(again()->dim, again()->states, again()->final_, n, h);
+                    if (ADJ && again()->dfinal) r += p * m.get(again()->dim, again()->states, again()->dfinal, n);
                     h = f4{0, 0, 0, 0};
                 }
             };
@@ -493,16 +510,8 @@ __device__ __forceinline__ float row16_sum(float v)
     return add(v, std::integral_constant<int, 0x121>{});
 }
 
-// Tokens of a chunk of the backward pass: its states at every kBack tokens stay in LDS.
-template <int NW>
-constexpr int back_chunk()
-{
-    return NW <= 4 ? 64 : 256 / NW;
-}
-
-// A chunk's gradients. Forward once over the chunk, keeping the state at each
-// tile; then tile by tile from the last, forward again with the states and decays
-// of its tokens in registers, and back over them.
+// A chunk's gradients, tile by tile from the last: forward over its tokens, with
+// their states and decays in registers, and back over them.
 //
 // The sums over channels (dc, db) go through the matrix pipe, which is idle
 // otherwise: a product with a matrix that has ones in one row adds the 64 lanes'
@@ -511,13 +520,12 @@ constexpr int back_chunk()
 template <typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
 {
-    constexpr int kTiles = back_chunk<NW>() / kBack, kThreads = NW * 64;
+    constexpr int kThreads = NW * 64;
     // A thread's pieces of a tile: V channels of a token.
     constexpr int V = NW <= 2 ? 4 : NW == 4 ? 2 : 1, kRow = kLanes / V, kPieces = kBack * kRow;
     constexpr int kPer = (kPieces + kThreads - 1) / kThreads;
     __shared__ float sd[kBack][3][kLanes];            // dt, dt u, dy'
     __shared__ float part[3][NW][kBack][kLanes];      // of s, the sum of a m, and y
-    __shared__ f4 held[kTiles][NW * 64];
     typedef float fv __attribute__((ext_vector_type(V)));
     const Where w = where(a);
     const Mine m = Mine::of<NW>(a, w);
@@ -532,12 +540,12 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         skip[e] = in && a.skip ? a.skip[w.c0 + col + e] : 0.f;
         s_skip[e] = s_bias[e] = 0.f;
     }
-    const f4 av = m.get(a, a.a, 0), a2 = av * kLog2e;
-    f4 h = {0, 0, 0, 0}, g = {0, 0, 0, 0}, da = {0, 0, 0, 0};
+    const f4 av = m.get(a.dim, a.states, a.a, 0), a2 = av * kLog2e;
+    f4 before0 = {0, 0, 0, 0}, g = {0, 0, 0, 0}, da = {0, 0, 0, 0};  // the state before the chunk; the adjoint after it
     if (a.per > 1) {
 #pragma unroll
         for (int s = 0; s < kSpw; ++s) {
-            h[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
+            before0[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
             g[s] = a.adds[m.slot(a, w.chunk, w.block, NW, s)];
         }
     }
@@ -556,7 +564,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         if (whole) return *(const Packed<T, V>*)q;
         return load_piece<T, V>(q - col, col, w.left);
     };
-    auto fetch = [&](Raw (&to)[kPer], int tile, bool all) {
+    auto fetch = [&](Raw (&to)[kPer], int tile) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int in = in0 + i * (kThreads / kRow), tok = tile * kBack + in;
@@ -565,12 +573,11 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
             to[i].mark = a.mark[w.place0 + tok];
             to[i].u = load(pu, a.u_s[1], tok);
             to[i].dt = load(pdt, a.dt_s[1], tok);
-            if (!all) continue;
             if (a.gate) to[i].z = load(pz, a.gate_s[1], tok);
             to[i].dy = load(pdy, a.dy_s[1], tok);
         }
     };
-    auto stage = [&](bool all) {
+    auto stage = [&]() {
         if (!works) return;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -583,15 +590,13 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                 if (a.softplus) v = softplus_of(v);
                 dt[e] = real ? v : 0.f;
                 dtu[e] = real ? v * (float)raw[i].u.e[e] : 0.f;
-                if (all) {
-                    float y = (float)raw[i].dy.e[e];
-                    if (a.gate) y *= silu_of((float)raw[i].z.e[e]);
-                    dy[e] = real ? y : 0.f;
-                }
+                float y = (float)raw[i].dy.e[e];
+                if (a.gate) y *= silu_of((float)raw[i].z.e[e]);
+                dy[e] = real ? y : 0.f;
             }
             *(fv*)&row[0][col] = dt;
             *(fv*)&row[1][col] = dtu;
-            if (all) *(fv*)&row[2][col] = dy;
+            *(fv*)&row[2][col] = dy;
         }
     };
     const int tiles = (w.n + kBack - 1) / kBack;
@@ -613,37 +618,30 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kBack) - 1);
         lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kBack) - 1);
     };
-    fetch(raw, 0, tiles == 1);
-    for (int tile = 0; tile + 1 < tiles; ++tile) {
-        held[tile][threadIdx.x] = h;
-        stage(false);
-        __syncthreads();
-        fetch(raw, tile + 1, tile + 2 == tiles);
-        marks(tile);
-        auto token = [&](int i, auto marked) {
-            if (decltype(marked)::value && (firsts >> i & 1)) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
-            const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane];
-            const scalar_floats o = bc + (tile * kBack + i) * 8;
+    // The state before a tile: its chunk's own part, and what is left of the state before the chunk.
+    f4 own, own_next;
+    float since, since_next;
+    auto history = [&](int tile, f4& v, float& sum) {
+        const int64_t at = (w.place0 / kBack + tile) * a.blocks + w.block;
 #pragma unroll
-            for (int s = 0; s < kSpw; ++s) h[s] = fmaf(__builtin_amdgcn_exp2f(dt * a2[s]), h[s], dtu * o[s]);
-            if (decltype(marked)::value && (lasts >> i & 1)) h = f4{0, 0, 0, 0};
-        };
-        if ((firsts | lasts) == 0) {
-#pragma unroll
-            for (int i = 0; i < kBack; ++i) token(i, std::false_type{});
-        } else {
-#pragma unroll 1
-            for (int i = 0; i < kBack; ++i) token(i, std::true_type{});
-        }
-        __syncthreads();
-    }
-    held[tiles - 1][threadIdx.x] = h;
+        for (int s = 0; s < kSpw; ++s) v[s] = a.hist[((at * NW + m.wave) * kSpw + s) * kLanes + m.lane];
+        sum = a.hist_sum[at * kLanes + m.lane];
+    };
+    fetch(raw, tiles - 1);
+    history(tiles - 1, own, since);
     for (int tile = tiles - 1; tile >= 0; --tile) {
-        stage(true);
+        stage();
         __syncthreads();
-        if (tile > 0) fetch(next, tile - 1, true);
+        if (tile > 0) {
+            fetch(next, tile - 1);
+            history(tile - 1, own_next, since_next);
+        }
         marks(tile);
-        h = held[tile][threadIdx.x];
+        f4 h = own;
+        if (since == since) {  // (no sequence has begun since the chunk's start)
+#pragma unroll
+            for (int s = 0; s < kSpw; ++s) h[s] = fmaf(__builtin_amdgcn_exp2f(since * a2[s]), before0[s], own[s]);
+        }
         f4 sum_c[kBack / 4], sum_b[kBack / 4];
 #pragma unroll
         for (int i = 0; i < kBack / 4; ++i) sum_c[i] = sum_b[i] = f4{0, 0, 0, 0};
@@ -655,7 +653,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
             f4 before[kBack], e[kBack];
 #pragma unroll
             for (int i = 0; i < kBack; ++i) {
-                if (decltype(marked)::value && (firsts >> i & 1)) h = m.get(a, a.init, __builtin_amdgcn_readlane(mk, i) >> 2);
+                if (decltype(marked)::value && (firsts >> i & 1)) h = m.get(again()->dim, again()->states, again()->init, __builtin_amdgcn_readlane(mk, i) >> 2);
                 const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
                 const scalar_floats o = bc + (tile * kBack + i) * 8;
                 before[i] = h;
@@ -672,7 +670,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
             }
 #pragma unroll
             for (int i = kBack - 1; i >= 0; --i) {
-                if (decltype(marked)::value && (lasts >> i & 1)) g = m.get(a, a.dfinal, __builtin_amdgcn_readlane(mk, i) >> 2);
+                if (decltype(marked)::value && (lasts >> i & 1)) g = m.get(again()->dim, again()->states, again()->dfinal, __builtin_amdgcn_readlane(mk, i) >> 2);
                 const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
                 const scalar_floats o = bc + (tile * kBack + i) * 8;
                 float fed = 0.f, moved = 0.f;
@@ -689,7 +687,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                 part[0][m.wave][i][m.lane] = fed;
                 part[1][m.wave][i][m.lane] = moved;
                 if (decltype(marked)::value && (firsts >> i & 1)) {
-                    if (a.dinit) m.put(a, a.dinit, __builtin_amdgcn_readlane(mk, i) >> 2, g);
+                    if (again()->dinit) m.put(again()->dim, again()->states, again()->dinit, __builtin_amdgcn_readlane(mk, i) >> 2, g);
                     g = f4{0, 0, 0, 0};
                 }
             }
@@ -762,6 +760,8 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) raw[i] = next[i];
+        own = own_next;
+        since = since_next;
         __syncthreads();
     }
 #pragma unroll
@@ -958,12 +958,15 @@ int64_t rows_of(const gconv_scan_desc* d) { return outer_of(d) * d->tokens; }
 
 struct Layout {
     int nw;
-    size_t bc, mark, ends, adds, sums, breaks, part_a, part_d, part_bc, bytes;
+    size_t bc, mark, ends, adds, sums, breaks, hist, hist_sum, part_a, part_d, part_bc, bytes;
 };
 
 // Workgroups of the forward pass that leave no CU without work. A sequence is
 // cut only as far as it takes to have them: each chunk is run over twice.
 constexpr int64_t kForwardBlocks = 512;
+// ... and the backward pass, whose longer chunks carry fewer states from one to
+// the next but need as many workgroups.
+constexpr int64_t kBackBlocks = 1024;
 
 void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
 {
@@ -980,7 +983,7 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
     a->seq.count = (int)d->sequences;
     int64_t chunk;
     if (back) {
-        chunk = l->nw <= 4 ? 64 : 256 / l->nw;
+        chunk = outer_of(d) * a->blocks * ((d->tokens + 127) / 128) >= kBackBlocks ? 128 : 64;
     } else {
         const int64_t have = std::max<int64_t>(1, outer_of(d) * a->blocks);
         const int64_t per = have * 2 > kForwardBlocks ? 1 : (kForwardBlocks + have - 1) / have;
@@ -997,10 +1000,12 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
     l->bc = cut.take(a->places * a->groups * l->nw * 8 * 4);
     l->mark = cut.take(a->places * 4);
     const bool cuts = a->per > 1;
-    l->ends = cut.take(cuts ? states : 0);
-    l->sums = cut.take(cuts ? a->chunks * a->blocks * kLanes * 4 : 0);
-    l->breaks = cut.take(cuts ? a->chunks * 4 : 0);
-    l->adds = cut.take(back && cuts ? states : 0);
+    l->ends = cut.take(cuts || back ? states : 0);
+    l->sums = cut.take(cuts || back ? a->chunks * a->blocks * kLanes * 4 : 0);
+    l->breaks = cut.take(cuts || back ? a->chunks * 4 : 0);
+    l->adds = cut.take(back ? states : 0);
+    l->hist = cut.take(back ? a->places / kBack * a->blocks * l->nw * kSpw * kLanes * 4 : 0);
+    l->hist_sum = cut.take(back ? a->places / kBack * a->blocks * kLanes * 4 : 0);
     l->part_a = cut.take(back ? states : 0);
     l->part_d = cut.take(back ? a->chunks * 2 * a->dim * 4 : 0);
     l->part_bc = cut.take(back ? a->places * a->groups * l->nw * 8 * 4 * a->gblocks : 0);
@@ -1016,6 +1021,8 @@ void place(const Layout& l, void* workspace, Scan* a)
     a->sums = (float*)(w + l.sums);
     a->breaks = (int32_t*)(w + l.breaks);
     a->adds = (float*)(w + l.adds);
+    a->hist = (float*)(w + l.hist);
+    a->hist_sum = (float*)(w + l.hist_sum);
     a->part_a = (float*)(w + l.part_a);
     a->part_d = (float*)(w + l.part_d);
     a->part_bc = (float*)(w + l.part_bc);
@@ -1211,8 +1218,8 @@ int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, cons
             by_waves(l.nw, [&](auto n) {
                 constexpr int NW = decltype(n)::value;
                 const unsigned blocks = (unsigned)(a.chunks * a.blocks);
+                scan_run<T, NW, false, true><<<blocks, NW * 64, 0, hs>>>(a);
                 if (a.per > 1) {
-                    scan_run<T, NW, false, true><<<blocks, NW * 64, 0, hs>>>(a);
                     scan_carry<<<dim3(blocks_of(a.chunks / a.per * a.blocks * NW * kSpw * kLanes, 256), 2), 256, 0, hs>>>(a, NW, a.chunks / a.per);
                 }
                 scan_back<T, NW><<<blocks, NW * 64, 0, hs>>>(a);
