@@ -498,25 +498,66 @@ __global__ __launch_bounds__(256) void scan_carry(Scan a, int nw, int64_t outers
 
 // ---- backward ---------------------------------------------------------------------
 
-// Sum over the 16 lanes of a row, in all of them.
-__device__ __forceinline__ float row16_sum(float v)
+// Sums over lanes, in which registers that hold different sums meet: after each
+// step half as many registers hold them, each sum in half as many lanes. 64 sums
+// over 64 lanes take some 2 operations each, where each alone would take 6.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v)
 {
-    auto add = [](float x, auto ctrl) {
-        return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
-    };
-    v = add(v, std::integral_constant<int, 0x128>{});  // row_ror 8, 4, 2, 1
-    v = add(v, std::integral_constant<int, 0x124>{});
-    v = add(v, std::integral_constant<int, 0x122>{});
-    return add(v, std::integral_constant<int, 0x121>{});
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// Lanes 0 to 31 get a's sum over lanes l and l + 32, the others b's.
+__device__ __forceinline__ float meet32(float a, float b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];  // (a bit_cast of an element itself takes the first one's bits)
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Of each 32 lanes the first 16 get a's sum over lanes l and l + 16, the others b's.
+__device__ __forceinline__ float meet16(float a, float b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];  // (a bit_cast of an element itself takes the first one's bits)
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Of each 16 (then 8) lanes the first half get a's sum over lanes l and 15 - l (7 - l), the others b's.
+__device__ __forceinline__ float meet8(float a, float b, int lane)
+{
+    const float x = a + moved<0x140>(a), y = b + moved<0x140>(b);
+    return lane & 8 ? y : x;
+}
+
+__device__ __forceinline__ float meet4(float a, float b, int lane)
+{
+    const float x = a + moved<0x141>(a), y = b + moved<0x141>(b);
+    return lane & 4 ? y : x;
+}
+
+// The sum over four lanes, in each of them.
+__device__ __forceinline__ float quad_sum(float v)
+{
+    v += moved<0xb1>(v);
+    return v + moved<0x4e>(v);
+}
+
+// One token's four states' values over 64 channels, in sixteens: row r of 16 lanes
+// has state 0, 2, 1, 3.
+__device__ __forceinline__ float join_states(const float (&v)[kSpw]) { return meet16(meet32(v[0], v[1]), meet32(v[2], v[3])); }
+
+// Four tokens of those: lane l has token (l >> 3 & 1) + 2 (l >> 2 & 1).
+__device__ __forceinline__ float join_tokens(const float* v, int lane)
+{
+    return quad_sum(meet4(meet8(v[0], v[1], lane), meet8(v[2], v[3], lane), lane));
 }
 
 // A chunk's gradients, tile by tile from the last: forward over its tokens, with
 // their states and decays in registers, and back over them.
 //
-// The sums over channels (dc, db) go through the matrix pipe, which is idle
-// otherwise: a product with a matrix that has ones in one row adds the 64 lanes'
-// values in fours into that row, exactly as float32 sums; what is left, 16 lanes,
-// takes four shifted additions for 16 such rows at once.
+// (The sums over channels, dc and db, by products with a matrix of ones held the
+// waves up: a float32 product takes the matrix pipe 32 cycles for 64 values.)
 template <typename T, int NW>
 __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
 {
@@ -603,13 +644,9 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
     const scalar_floats bc = (scalar_floats)(a.bc + ((w.g * NW + m.wave) * a.places + w.place0) * 8);
     float* out_bc = a.part_bc + ((((int64_t)w.gb * a.groups + w.g) * NW + m.wave) * a.places + w.place0) * 8;
 
-    // [r]: a matrix with ones in row r; kept as values (as conditions they take twice the scalar registers there are)
-    float ones[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        ones[r] = (m.lane & 15) == r ? 1.f : 0.f;
-        asm volatile("" : "+v"(ones[r]));
-    }
+    // lane's place in a tile's [8 tokens][db, dc][4 states]
+    const int out_at = ((m.lane >> 3 & 1) + 2 * (m.lane >> 2 & 1) + (m.lane & 2 ? 4 : 0)) * 8 + (m.lane & 1) * 4 +
+                       (m.lane >> 5) + 2 * (m.lane >> 4 & 1);
     int mk = -1;
     uint32_t firsts = 0, lasts = 0;
     auto marks = [&](int tile) {
@@ -642,13 +679,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
 #pragma unroll
             for (int s = 0; s < kSpw; ++s) h[s] = fmaf(__builtin_amdgcn_exp2f(since * a2[s]), before0[s], own[s]);
         }
-        f4 sum_c[kBack / 4], sum_b[kBack / 4];
-#pragma unroll
-        for (int i = 0; i < kBack / 4; ++i) sum_c[i] = sum_b[i] = f4{0, 0, 0, 0};
-        // adds the 64 lanes' v into row 4 (i % 4) + s of a group of four tokens
-        auto gather = [&](f4& acc, int i, int s, float v) {
-            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(ones[(i & 3) * 4 + s], v, acc, 0, 0, 0);
-        };
+        float sum_c[kBack], sum_b[kBack];
         auto tokens = [&](auto marked) {
             f4 before[kBack], e[kBack];
 #pragma unroll
@@ -657,14 +688,15 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                 const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
                 const scalar_floats o = bc + (tile * kBack + i) * 8;
                 before[i] = h;
-                float y = 0.f;
+                float y = 0.f, v[kSpw];
 #pragma unroll
                 for (int s = 0; s < kSpw; ++s) {
                     e[i][s] = __builtin_amdgcn_exp2f(dt * a2[s]);
                     h[s] = fmaf(e[i][s], h[s], dtu * o[s]);
                     y = fmaf(o[4 + s], h[s], y);
-                    gather(sum_c[i / 4], i, s, dy * h[s]);
+                    v[s] = dy * h[s];
                 }
+                sum_c[i] = join_states(v);
                 part[2][m.wave][i][m.lane] = y;
                 if (decltype(marked)::value && (lasts >> i & 1)) h = f4{0, 0, 0, 0};
             }
@@ -673,17 +705,18 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                 if (decltype(marked)::value && (lasts >> i & 1)) g = m.get(again()->dim, again()->states, again()->dfinal, __builtin_amdgcn_readlane(mk, i) >> 2);
                 const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
                 const scalar_floats o = bc + (tile * kBack + i) * 8;
-                float fed = 0.f, moved = 0.f;
+                float fed = 0.f, moved = 0.f, v[kSpw];
 #pragma unroll
                 for (int s = 0; s < kSpw; ++s) {
                     g[s] = fmaf(o[4 + s], dy, g[s]);
-                    gather(sum_b[i / 4], i, s, g[s] * dtu);
+                    v[s] = g[s] * dtu;
                     fed = fmaf(g[s], o[s], fed);
                     g[s] *= e[i][s];
                     const float q = g[s] * before[i][s];
                     da[s] = fmaf(q, dt, da[s]);
                     moved = fmaf(q, av[s], moved);
                 }
+                sum_b[i] = join_states(v);
                 part[0][m.wave][i][m.lane] = fed;
                 part[1][m.wave][i][m.lane] = moved;
                 if (decltype(marked)::value && (firsts >> i & 1)) {
@@ -694,17 +727,13 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         };
         if ((firsts | lasts) == 0) tokens(std::false_type{});
         else tokens(std::true_type{});
-        // the first lane of 16 has db of its token, the second dc
-#pragma unroll
-        for (int i = 0; i < kBack / 4; ++i) {
-            f4 vb, vc;
-#pragma unroll
-            for (int s = 0; s < kSpw; ++s) {
-                vb[s] = row16_sum(sum_b[i][s]);
-                vc[s] = row16_sum(sum_c[i][s]);
-            }
-            const int tok = tile * kBack + i * 4 + (m.lane >> 4), which = m.lane & 15;
-            if (which < 2) *(f4*)(out_bc + tok * 8 + which * 4) = which ? vc : vb;
+        // of four lanes with the same sums each writes another: db and dc of tokens 0 to 3 and of 4 to 7
+        {
+            static_assert(kBack == 8, "two groups of four tokens");
+            const float b0 = join_tokens(sum_b, m.lane), c0 = join_tokens(sum_c, m.lane), b1 = join_tokens(sum_b + 4, m.lane),
+                        c1 = join_tokens(sum_c + 4, m.lane);
+            const float v = m.lane & 2 ? (m.lane & 1 ? c1 : b1) : (m.lane & 1 ? c0 : b0);
+            out_bc[tile * kBack * 8 + out_at] = v;
         }
         __syncthreads();
         if (works) {
