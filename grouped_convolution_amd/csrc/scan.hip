@@ -175,6 +175,25 @@ __global__ __launch_bounds__(256) void scan_empty(Sequences seq, const float* fr
 // Read-only while the kernel runs, at an address that is the same for a wave: scalar loads.
 typedef const __attribute__((address_space(4))) float* scalar_floats;
 
+// Asks for TOKENS tokens' b and c of a wave, a line of the scalar cache each 64
+// bytes, well before they are used: from memory they take longer than a few
+// tokens' work. settle() is where they have to be there.
+template <int TOKENS>
+struct Ahead {
+    float line[TOKENS / 2];
+    __device__ __forceinline__ void ask(scalar_floats p)
+    {
+#pragma unroll
+        for (int i = 0; i < TOKENS / 2; ++i) line[i] = p[i * 16];
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ void settle() const
+    {
+#pragma unroll
+        for (int i = 0; i < TOKENS / 2; ++i) asm volatile("" ::"s"(line[i]));
+    }
+};
+
 // The kernel's arguments, read again: what only tokens with marks ask for does not
 // stay in scalar registers, of which the rest of the kernel has need.
 __device__ __forceinline__ const __attribute__((address_space(4))) Scan* again()
@@ -325,13 +344,19 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     }
     struct Raw {
         Packed<T, 4> u, dt, z, dy;
+        int mark;
     } raw[Q::kPer];
     Packed<T, 4> cur_u[Q::kPer], cur_z[Q::kPer], old_u[Q::kPer], old_z[Q::kPer];  // of this tile and the one before
+    int cur_mark[Q::kPer], old_mark[Q::kPer];
+    // marks of a tile, a token a lane: asked for a tile ahead, as loads come back in order
+    auto mark_of = [&](int tile) { return a.mark[w.place0 + tile * kTile + (m.lane & (kTile - 1))]; };
+    int mk = mark_of(0), mk_next = -1;
     auto fetch = [&](int tile) {
 #pragma unroll
         for (int i = 0; i < Q::kPer; ++i) {
             const int q = Q::of(i), tok = min(tile * kTile + q / 16, w.n - 1);
             if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+            raw[i].mark = a.mark[w.place0 + tile * kTile + q / 16];
             raw[i].u = load_quad<T>(a.u, a.u_s, w, w.t0 + tok, quad);
             raw[i].dt = load_quad<T>(a.dt, a.dt_s, w, w.t0 + tok, quad);
             if ((OUT || ADJ) && a.gate) raw[i].z = load_quad<T>(a.gate, a.gate_s, w, w.t0 + tok, quad);
@@ -341,9 +366,9 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     auto stage = [&](int tile) {  // of what was fetched
 #pragma unroll
         for (int i = 0; i < Q::kPer; ++i) {
-            const int q = Q::of(i), tok = tile * kTile + q / 16;
+            const int q = Q::of(i);
             if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
-            const bool real = a.mark[w.place0 + tok] >= 0;
+            const bool real = raw[i].mark >= 0;
             f4 dt, dtu;
             step_sizes<T>(a, bias, raw[i].dt, raw[i].u, real, &dt, &dtu);
             float(*row)[kLanes] = sd[tile & 1][q / 16];
@@ -353,25 +378,31 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
             if (OUT) {
                 old_u[i] = cur_u[i];
                 old_z[i] = cur_z[i];
+                old_mark[i] = cur_mark[i];
                 cur_u[i] = raw[i].u;
                 cur_z[i] = raw[i].z;
+                cur_mark[i] = raw[i].mark;
             }
         }
     };
     const int tiles = (w.n + kTile - 1) / kTile;
     const scalar_floats bc = (scalar_floats)(a.bc + ((w.g * NW + m.wave) * a.places + w.place0) * 8);
+    Ahead<kTile> ahead;
     fetch(0);
+    ahead.ask(bc);
     stage(0);
+    ahead.settle();
     __syncthreads();
     // One barrier a tile: while the waves run over a tile, its outputs go to one
     // buffer, those of the tile before are read from the other, and the next
     // tile's inputs are put beside this one's.
     for (int tile = 0; tile < tiles + (OUT ? 1 : 0); ++tile) {
-        if (tile + 1 < tiles) fetch(tile + 1);
+        if (tile + 1 < tiles) {
+            mk_next = mark_of(tile + 1);
+            fetch(tile + 1);
+            ahead.ask(bc + (tile + 1) * kTile * 8);
+        }
         if (tile < tiles) {
-            // marks of the tile, a token a lane
-            const int tok = tile * kTile + (m.lane & (kTile - 1));
-            const int mk = a.mark[w.place0 + tok];
             const uint32_t firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kTile) - 1);
             const uint32_t lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kTile) - 1);
             auto token = [&](int i, auto marked) {
@@ -436,14 +467,18 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] *= silu_of(z.v[e]);
                 }
-                const bool real = a.mark[w.place0 + tok] >= 0;
+                const bool real = (last ? cur_mark[i] : old_mark[i]) >= 0;
                 float o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = real ? v[e] : 0.f;
                 store_quad<T>(w, (T*)a.y + (w.row0 + tok) * a.dim + w.c0, quad, o);
             }
         }
-        if (tile + 1 < tiles) stage(tile + 1);
+        if (tile + 1 < tiles) {
+            stage(tile + 1);
+            ahead.settle();
+        }
+        mk = mk_next;
         __syncthreads();
     }
     if (!OUT) {
@@ -647,11 +682,11 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
     // lane's place in a tile's [8 tokens][db, dc][4 states]
     const int out_at = ((m.lane >> 3 & 1) + 2 * (m.lane >> 2 & 1) + (m.lane & 2 ? 4 : 0)) * 8 + (m.lane & 1) * 4 +
                        (m.lane >> 5) + 2 * (m.lane >> 4 & 1);
-    int mk = -1;
+    // marks of a tile, a token a lane: asked for a tile ahead, as loads come back in order
+    auto mark_of = [&](int tile) { return a.mark[w.place0 + tile * kBack + (m.lane & (kBack - 1))]; };
+    int mk = mark_of(tiles - 1), mk_next = -1;
     uint32_t firsts = 0, lasts = 0;
-    auto marks = [&](int tile) {
-        const int tok = tile * kBack + (m.lane & (kBack - 1));
-        mk = a.mark[w.place0 + tok];
+    auto marks = [&]() {
         firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kBack) - 1);
         lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kBack) - 1);
     };
@@ -664,16 +699,21 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         for (int s = 0; s < kSpw; ++s) v[s] = a.hist[((at * NW + m.wave) * kSpw + s) * kLanes + m.lane];
         sum = a.hist_sum[at * kLanes + m.lane];
     };
+    Ahead<kBack> ahead;
     fetch(raw, tiles - 1);
     history(tiles - 1, own, since);
+    ahead.ask(bc + (tiles - 1) * kBack * 8);
+    ahead.settle();
     for (int tile = tiles - 1; tile >= 0; --tile) {
         stage();
         __syncthreads();
+        marks();
         if (tile > 0) {
+            mk_next = mark_of(tile - 1);
             fetch(next, tile - 1);
             history(tile - 1, own_next, since_next);
+            ahead.ask(bc + (tile - 1) * kBack * 8);
         }
-        marks(tile);
         f4 h = own;
         if (since == since) {  // (no sequence has begun since the chunk's start)
 #pragma unroll
@@ -789,8 +829,10 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) raw[i] = next[i];
+        if (tile > 0) ahead.settle();
         own = own_next;
         since = since_next;
+        mk = mk_next;
         __syncthreads();
     }
 #pragma unroll
@@ -1015,7 +1057,7 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
         chunk = outer_of(d) * a->blocks * ((d->tokens + 127) / 128) >= kBackBlocks ? 128 : 64;
     } else {
         const int64_t have = std::max<int64_t>(1, outer_of(d) * a->blocks);
-        const int64_t per = have * 2 > kForwardBlocks ? 1 : (kForwardBlocks + have - 1) / have;
+        const int64_t per = have * 2 >= kForwardBlocks ? 1 : (kForwardBlocks + have - 1) / have;
         chunk = std::max<int64_t>(4 * kTile, ((d->tokens + per - 1) / per + kTile - 1) / kTile * kTile);
         chunk = std::min<int64_t>(chunk, (int64_t)1 << 30);
     }
