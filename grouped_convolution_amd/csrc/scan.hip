@@ -39,7 +39,7 @@ namespace gconv {
 namespace {
 
 constexpr int kLanes = 64;   // channels of a workgroup
-constexpr int kSpw = 4;      // states of a wave
+constexpr int kSpw = 4;      // states that lie together in memory
 constexpr int kTile = 16;    // tokens passed through LDS at once
 constexpr int kBack = 8;     // the same, of the backward pass
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
@@ -204,13 +204,14 @@ __device__ __forceinline__ const __attribute__((address_space(4))) Scan* again()
 }
 
 // The states of lane's channel that its wave holds.
+template <int SPW>
 struct Mine {
+    typedef float fs __attribute__((ext_vector_type(SPW)));
     int lane, wave;
     int ch;         // channel, clamped to one that exists
     bool live;
     int at;         // element of [dim][states]
-    int have;       // states that exist, of kSpw
-    template <int NW>
+    int have;       // states that exist, of SPW
     __device__ __forceinline__ static Mine of(const Scan& a, const Where& w)
     {
         Mine m;
@@ -218,33 +219,37 @@ struct Mine {
         m.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         m.live = m.lane < w.left;
         m.ch = w.c0 + (m.live ? m.lane : 0);
-        m.at = m.ch * a.states + m.wave * kSpw;
-        m.have = m.live ? max(0, min(kSpw, a.states - m.wave * kSpw)) : 0;
+        m.at = m.ch * a.states + m.wave * SPW;
+        m.have = m.live ? max(0, min(SPW, a.states - m.wave * SPW)) : 0;
         return m;
     }
     // p[n][dim][states] of sequence n, or 0: no branches, a state that does not
     // exist is read (and written) past the resource's end
     __device__ __forceinline__ uint32_t offset(int s) const { return s < have ? (uint32_t)(at + s) * 4 : kOOB; }
-    __device__ __forceinline__ f4 get(int dim, int states, const float* p, int64_t n) const
+    __device__ __forceinline__ fs get(int dim, int states, const float* p, int64_t n) const
     {
         const int64_t size = (int64_t)dim * states;
         const __amdgpu_buffer_rsrc_t r = make_rsrc(p + (p ? n * size : 0), p ? (uint32_t)size * 4 : 0);
-        f4 v;
+        fs v;
 #pragma unroll
-        for (int s = 0; s < kSpw; ++s) v[s] = load_f32(r, offset(s));
+        for (int s = 0; s < SPW; ++s) v[s] = load_f32(r, offset(s));
         return v;
     }
-    __device__ __forceinline__ void put(int dim, int states, float* p, int64_t n, f4 v) const
+    __device__ __forceinline__ void put(int dim, int states, float* p, int64_t n, fs v) const
     {
         const int64_t size = (int64_t)dim * states;
         const __amdgpu_buffer_rsrc_t r = make_rsrc(p + (p ? n * size : 0), p ? (uint32_t)size * 4 : 0);
 #pragma unroll
-        for (int s = 0; s < kSpw; ++s) store_f32(r, offset(s), v[s]);
+        for (int s = 0; s < SPW; ++s) store_f32(r, offset(s), v[s]);
     }
+    // element of [groups][fours][places][8] where its states are, before the place
+    __device__ __forceinline__ int64_t four(const Scan& a, int g, int fours) const { return (int64_t)(g * fours + wave * SPW / 4) * a.places; }
+    // ... and within the eight
+    __device__ __forceinline__ int within() const { return wave * SPW % 4; }
     // index into `ends` and its like, of state s
     __device__ __forceinline__ int64_t slot(const Scan& a, int64_t chunk, int block, int nw, int s) const
     {
-        return ((((chunk * a.blocks + block) * nw + wave) * kSpw + s) * kLanes) + lane;
+        return ((((chunk * a.blocks + block) * nw + wave) * SPW + s) * kLanes) + lane;
     }
 };
 
@@ -322,7 +327,7 @@ __device__ __forceinline__ f4 gated(const Scan& a, const Packed<T, 4>& dy, const
 
 // OUT: the outputs, from the state before each chunk; else each chunk's own
 // contribution to the state after it (and, ADJ, to the adjoint before it).
-template <typename T, int NW, bool OUT, bool ADJ>
+template <typename T, int NW, int SPW, bool OUT, bool ADJ>
 __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
 {
     using Q = Quads<T, NW, kTile>;
@@ -330,17 +335,19 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     __shared__ float sd[2][kTile][kW][kLanes];            // dt, dt u (, dy')
     __shared__ float yp[OUT ? 2 : 1][OUT ? NW : 1][OUT ? kTile : 1][kLanes];
     const Where w = where(a);
-    const Mine m = Mine::of<NW>(a, w);
+    const Mine<SPW> m = Mine<SPW>::of(a, w);
+    typedef typename Mine<SPW>::fs fs;
     const int quad = threadIdx.x & 15;
     const f4 bias = channel_quad(a.dt_bias, w, quad), skip = channel_quad(a.skip, w, quad);
 
-    f4 a2 = m.get(a.dim, a.states, a.a, 0) * kLog2e;
-    f4 h = {0, 0, 0, 0}, p = {1, 1, 1, 1}, r = {0, 0, 0, 0};
+    const fs a2 = m.get(a.dim, a.states, a.a, 0) * kLog2e;
+    fs h = {}, p = {}, r = {};
+    p += 1.f;
     float total = 0.f;
     int broken = 0;
     if (OUT && a.per > 1) {
 #pragma unroll
-        for (int s = 0; s < kSpw; ++s) h[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
+        for (int s = 0; s < SPW; ++s) h[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
     }
     struct Raw {
         Packed<T, 4> u, dt, z, dy;
@@ -386,7 +393,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         }
     };
     const int tiles = (w.n + kTile - 1) / kTile;
-    const scalar_floats bc = (scalar_floats)(a.bc + ((w.g * NW + m.wave) * a.places + w.place0) * 8);
+    const scalar_floats bc = (scalar_floats)(a.bc + (m.four(a, w.g, NW * SPW / 4) + w.place0) * 8 + m.within());
     Ahead<kTile> ahead;
     fetch(0);
     ahead.ask(bc);
@@ -409,12 +416,12 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
                 if (ADJ && i % kBack == 0) {
                     const int64_t at = ((w.place0 + tile * kTile + i) / kBack * a.blocks + w.block);
 #pragma unroll
-                    for (int s = 0; s < kSpw; ++s) a.hist[((at * NW + m.wave) * kSpw + s) * kLanes + m.lane] = h[s];
+                    for (int s = 0; s < SPW; ++s) a.hist[((at * NW + m.wave) * SPW + s) * kLanes + m.lane] = h[s];
                     if (m.wave == 0) a.hist_sum[at * kLanes + m.lane] = broken ? __builtin_nanf("") : total;
                 }
                 if (decltype(marked)::value && (firsts >> i & 1)) {
                     h = m.get(again()->dim, again()->states, again()->init, __builtin_amdgcn_readlane(mk, i) >> 2);
-                    p = f4{0, 0, 0, 0};
+                    p = fs{};
                     broken = 1;
                 }
                 const float dt = sd[tile & 1][i][0][m.lane], dtu = sd[tile & 1][i][1][m.lane];
@@ -423,7 +430,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
                 if (ADJ) dy = sd[tile & 1][i][kW - 1][m.lane];
                 if (!OUT) total += dt;
 #pragma unroll
-                for (int s = 0; s < kSpw; ++s) {
+                for (int s = 0; s < SPW; ++s) {
                     const float e = __builtin_amdgcn_exp2f(dt * a2[s]);
                     h[s] = fmaf(e, h[s], dtu * o[s]);
                     if (OUT) y = fmaf(o[4 + s], h[s], y);
@@ -437,7 +444,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
                     const int n = __builtin_amdgcn_readlane(mk, i) >> 2;
                     if (OUT && again()->final_) m.put(again()->dim, again()->states, again()->final_, n, h);
                     if (ADJ && again()->dfinal) r += p * m.get(again()->dim, again()->states, again()->dfinal, n);
-                    h = f4{0, 0, 0, 0};
+                    h = fs{};
                 }
             };
             // (without marks the tokens are one stretch of code, whose loads are all under way early)
@@ -483,7 +490,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     }
     if (!OUT) {
 #pragma unroll
-        for (int s = 0; s < kSpw; ++s) {
+        for (int s = 0; s < SPW; ++s) {
             a.ends[m.slot(a, w.chunk, w.block, NW, s)] = h[s];
             if (ADJ) a.adds[m.slot(a, w.chunk, w.block, NW, s)] = r[s];
         }
@@ -580,7 +587,9 @@ __device__ __forceinline__ float quad_sum(float v)
 
 // One token's four states' values over 64 channels, in sixteens: row r of 16 lanes
 // has state 0, 2, 1, 3.
-__device__ __forceinline__ float join_states(const float (&v)[kSpw]) { return meet16(meet32(v[0], v[1]), meet32(v[2], v[3])); }
+__device__ __forceinline__ float join_states(const float (&v)[4]) { return meet16(meet32(v[0], v[1]), meet32(v[2], v[3])); }
+// ... two states': the halves of the wave have one each.
+__device__ __forceinline__ float join_states(const float (&v)[2]) { return meet32(v[0], v[1]); }
 
 // Four tokens of those: lane l has token (l >> 3 & 1) + 2 (l >> 2 & 1).
 __device__ __forceinline__ float join_tokens(const float* v, int lane)
@@ -588,13 +597,20 @@ __device__ __forceinline__ float join_tokens(const float* v, int lane)
     return quad_sum(meet4(meet8(v[0], v[1], lane), meet8(v[2], v[3], lane), lane));
 }
 
+// Eight tokens of two states: lane l has token (l >> 4 & 1) + 2 (l >> 3 & 1) + 4 (l >> 2 & 1).
+__device__ __forceinline__ float join_pairs(const float* v, int lane)
+{
+    const float x = meet8(meet16(v[0], v[1]), meet16(v[2], v[3]), lane), y = meet8(meet16(v[4], v[5]), meet16(v[6], v[7]), lane);
+    return quad_sum(meet4(x, y, lane));
+}
+
 // A chunk's gradients, tile by tile from the last: forward over its tokens, with
 // their states and decays in registers, and back over them.
 //
 // (The sums over channels, dc and db, by products with a matrix of ones held the
 // waves up: a float32 product takes the matrix pipe 32 cycles for 64 values.)
-template <typename T, int NW>
-__global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
+template <typename T, int NW, int SPW>
+__global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
 {
     constexpr int kThreads = NW * 64;
     // A thread's pieces of a tile: V channels of a token.
@@ -603,8 +619,9 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
     __shared__ float sd[kBack][3][kLanes];            // dt, dt u, dy'
     __shared__ float part[3][NW][kBack][kLanes];      // of s, the sum of a m, and y
     typedef float fv __attribute__((ext_vector_type(V)));
+    typedef typename Mine<SPW>::fs fs;
     const Where w = where(a);
-    const Mine m = Mine::of<NW>(a, w);
+    const Mine<SPW> m = Mine<SPW>::of(a, w);
     const int col = (threadIdx.x % kRow) * V;          // channel of the workgroup's
     const int in0 = threadIdx.x / kRow;                // token of the tile, of the thread's first piece
     const bool works = (int)threadIdx.x < kPieces, whole = w.left == kLanes;
@@ -616,11 +633,11 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         skip[e] = in && a.skip ? a.skip[w.c0 + col + e] : 0.f;
         s_skip[e] = s_bias[e] = 0.f;
     }
-    const f4 av = m.get(a.dim, a.states, a.a, 0), a2 = av * kLog2e;
-    f4 before0 = {0, 0, 0, 0}, g = {0, 0, 0, 0}, da = {0, 0, 0, 0};  // the state before the chunk; the adjoint after it
+    const fs av = m.get(a.dim, a.states, a.a, 0), a2 = av * kLog2e;
+    fs before0 = {}, g = {}, da = {};  // the state before the chunk; the adjoint after it
     if (a.per > 1) {
 #pragma unroll
-        for (int s = 0; s < kSpw; ++s) {
+        for (int s = 0; s < SPW; ++s) {
             before0[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
             g[s] = a.adds[m.slot(a, w.chunk, w.block, NW, s)];
         }
@@ -676,12 +693,13 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         }
     };
     const int tiles = (w.n + kBack - 1) / kBack;
-    const scalar_floats bc = (scalar_floats)(a.bc + ((w.g * NW + m.wave) * a.places + w.place0) * 8);
-    float* out_bc = a.part_bc + ((((int64_t)w.gb * a.groups + w.g) * NW + m.wave) * a.places + w.place0) * 8;
+    const scalar_floats bc = (scalar_floats)(a.bc + (m.four(a, w.g, NW * SPW / 4) + w.place0) * 8 + m.within());
+    float* out_bc = a.part_bc + (m.four(a, w.gb * a.groups + w.g, NW * SPW / 4) + w.place0) * 8 + m.within();
 
     // lane's place in a tile's [8 tokens][db, dc][4 states]
-    const int out_at = ((m.lane >> 3 & 1) + 2 * (m.lane >> 2 & 1) + (m.lane & 2 ? 4 : 0)) * 8 + (m.lane & 1) * 4 +
-                       (m.lane >> 5) + 2 * (m.lane >> 4 & 1);
+    const int out_at = SPW == 4 ? ((m.lane >> 3 & 1) + 2 * (m.lane >> 2 & 1) + (m.lane & 2 ? 4 : 0)) * 8 + (m.lane & 1) * 4 + (m.lane >> 5) +
+                                      2 * (m.lane >> 4 & 1)
+                                : ((m.lane >> 4 & 1) + 2 * (m.lane >> 3 & 1) + 4 * (m.lane >> 2 & 1)) * 8 + (m.lane & 1) * 4 + (m.lane >> 5);
     // marks of a tile, a token a lane: asked for a tile ahead, as loads come back in order
     auto mark_of = [&](int tile) { return a.mark[w.place0 + tile * kBack + (m.lane & (kBack - 1))]; };
     int mk = mark_of(tiles - 1), mk_next = -1;
@@ -691,12 +709,12 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         lasts = (uint32_t)__ballot(mk >= 0 && (mk & LAST)) & ((1u << kBack) - 1);
     };
     // The state before a tile: its chunk's own part, and what is left of the state before the chunk.
-    f4 own, own_next;
+    fs own, own_next;
     float since, since_next;
-    auto history = [&](int tile, f4& v, float& sum) {
+    auto history = [&](int tile, fs& v, float& sum) {
         const int64_t at = (w.place0 / kBack + tile) * a.blocks + w.block;
 #pragma unroll
-        for (int s = 0; s < kSpw; ++s) v[s] = a.hist[((at * NW + m.wave) * kSpw + s) * kLanes + m.lane];
+        for (int s = 0; s < SPW; ++s) v[s] = a.hist[((at * NW + m.wave) * SPW + s) * kLanes + m.lane];
         sum = a.hist_sum[at * kLanes + m.lane];
     };
     Ahead<kBack> ahead;
@@ -714,23 +732,23 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
             history(tile - 1, own_next, since_next);
             ahead.ask(bc + (tile - 1) * kBack * 8);
         }
-        f4 h = own;
+        fs h = own;
         if (since == since) {  // (no sequence has begun since the chunk's start)
 #pragma unroll
-            for (int s = 0; s < kSpw; ++s) h[s] = fmaf(__builtin_amdgcn_exp2f(since * a2[s]), before0[s], own[s]);
+            for (int s = 0; s < SPW; ++s) h[s] = fmaf(__builtin_amdgcn_exp2f(since * a2[s]), before0[s], own[s]);
         }
         float sum_c[kBack], sum_b[kBack];
         auto tokens = [&](auto marked) {
-            f4 before[kBack], e[kBack];
+            fs before[kBack], e[kBack];
 #pragma unroll
             for (int i = 0; i < kBack; ++i) {
                 if (decltype(marked)::value && (firsts >> i & 1)) h = m.get(again()->dim, again()->states, again()->init, __builtin_amdgcn_readlane(mk, i) >> 2);
                 const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
                 const scalar_floats o = bc + (tile * kBack + i) * 8;
                 before[i] = h;
-                float y = 0.f, v[kSpw];
+                float y = 0.f, v[SPW];
 #pragma unroll
-                for (int s = 0; s < kSpw; ++s) {
+                for (int s = 0; s < SPW; ++s) {
                     e[i][s] = __builtin_amdgcn_exp2f(dt * a2[s]);
                     h[s] = fmaf(e[i][s], h[s], dtu * o[s]);
                     y = fmaf(o[4 + s], h[s], y);
@@ -738,16 +756,16 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                 }
                 sum_c[i] = join_states(v);
                 part[2][m.wave][i][m.lane] = y;
-                if (decltype(marked)::value && (lasts >> i & 1)) h = f4{0, 0, 0, 0};
+                if (decltype(marked)::value && (lasts >> i & 1)) h = fs{};
             }
 #pragma unroll
             for (int i = kBack - 1; i >= 0; --i) {
                 if (decltype(marked)::value && (lasts >> i & 1)) g = m.get(again()->dim, again()->states, again()->dfinal, __builtin_amdgcn_readlane(mk, i) >> 2);
                 const float dt = sd[i][0][m.lane], dtu = sd[i][1][m.lane], dy = sd[i][2][m.lane];
                 const scalar_floats o = bc + (tile * kBack + i) * 8;
-                float fed = 0.f, moved = 0.f, v[kSpw];
+                float fed = 0.f, moved = 0.f, v[SPW];
 #pragma unroll
-                for (int s = 0; s < kSpw; ++s) {
+                for (int s = 0; s < SPW; ++s) {
                     g[s] = fmaf(o[4 + s], dy, g[s]);
                     v[s] = g[s] * dtu;
                     fed = fmaf(g[s], o[s], fed);
@@ -761,19 +779,21 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
                 part[1][m.wave][i][m.lane] = moved;
                 if (decltype(marked)::value && (firsts >> i & 1)) {
                     if (again()->dinit) m.put(again()->dim, again()->states, again()->dinit, __builtin_amdgcn_readlane(mk, i) >> 2, g);
-                    g = f4{0, 0, 0, 0};
+                    g = fs{};
                 }
             }
         };
         if ((firsts | lasts) == 0) tokens(std::false_type{});
         else tokens(std::true_type{});
-        // of four lanes with the same sums each writes another: db and dc of tokens 0 to 3 and of 4 to 7
-        {
-            static_assert(kBack == 8, "two groups of four tokens");
+        // of four lanes with the same sums each writes another: db and dc, of four states those of tokens 0 to 3 and of 4 to 7
+        static_assert(kBack == 8, "two groups of four tokens");
+        if constexpr (SPW == 4) {
             const float b0 = join_tokens(sum_b, m.lane), c0 = join_tokens(sum_c, m.lane), b1 = join_tokens(sum_b + 4, m.lane),
                         c1 = join_tokens(sum_c + 4, m.lane);
-            const float v = m.lane & 2 ? (m.lane & 1 ? c1 : b1) : (m.lane & 1 ? c0 : b0);
-            out_bc[tile * kBack * 8 + out_at] = v;
+            out_bc[tile * kBack * 8 + out_at] = m.lane & 2 ? (m.lane & 1 ? c1 : b1) : (m.lane & 1 ? c0 : b0);
+        } else {
+            const float b0 = join_pairs(sum_b, m.lane), c0 = join_pairs(sum_c, m.lane);
+            if ((m.lane & 2) == 0) out_bc[tile * kBack * 8 + out_at] = m.lane & 1 ? c0 : b0;
         }
         __syncthreads();
         if (works) {
@@ -836,7 +856,7 @@ __global__ __launch_bounds__(NW * 64) void scan_back(Scan a)
         __syncthreads();
     }
 #pragma unroll
-    for (int s = 0; s < kSpw; ++s) a.part_a[m.slot(a, w.chunk, w.block, NW, s)] = da[s];
+    for (int s = 0; s < SPW; ++s) a.part_a[m.slot(a, w.chunk, w.block, NW, s)] = da[s];
     // the channels' sums over the threads that had them, in order
     constexpr int kRows = (kPieces < kThreads ? kPieces : kThreads) / kRow;
     static_assert(kRows <= kBack && 3 * NW >= 2, "room for the sums");
@@ -1083,6 +1103,10 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
     l->bytes = cut.bytes;
 }
 
+// Whether the forward pass gives a wave two states: twice the waves where there
+// is no more than a workgroup a CU.
+bool narrow_forward(const Scan& a) { return a.chunks * a.blocks <= 256; }
+
 void place(const Layout& l, void* workspace, Scan* a)
 {
     char* w = (char*)workspace;
@@ -1123,15 +1147,33 @@ void strides(const gconv_scan_desc* d, Scan* a)
     a->c_s[2] = d->c_stride[2];
 }
 
-template <typename F>
-void by_waves(int nw, F f)
+// f(waves, states of a wave) for `fours` times four states: two states a wave
+// where a workgroup's waves then are no more than 16 and `narrow` asks for it
+// (ALWAYS: it does).
+template <bool ALWAYS = false, typename F>
+void by_waves(int fours, bool narrow, F f)
 {
-    switch (nw) {
-        case 1: f(std::integral_constant<int, 1>{}); break;
-        case 2: f(std::integral_constant<int, 2>{}); break;
-        case 4: f(std::integral_constant<int, 4>{}); break;
-        case 8: f(std::integral_constant<int, 8>{}); break;
-        default: f(std::integral_constant<int, 16>{}); break;
+    constexpr std::integral_constant<int, 2> two;
+    constexpr std::integral_constant<int, 4> four;
+    if (narrow && fours <= 8) {
+        switch (fours) {
+            case 1: f(std::integral_constant<int, 2>{}, two); break;
+            case 2: f(std::integral_constant<int, 4>{}, two); break;
+            case 4: f(std::integral_constant<int, 8>{}, two); break;
+            default: f(std::integral_constant<int, 16>{}, two); break;
+        }
+        return;
+    }
+    if constexpr (ALWAYS) {
+        f(std::integral_constant<int, 16>{}, four);
+    } else {
+        switch (fours) {
+            case 1: f(std::integral_constant<int, 1>{}, four); break;
+            case 2: f(std::integral_constant<int, 2>{}, four); break;
+            case 4: f(std::integral_constant<int, 4>{}, four); break;
+            case 8: f(std::integral_constant<int, 8>{}, four); break;
+            default: f(std::integral_constant<int, 16>{}, four); break;
+        }
     }
 }
 
@@ -1213,14 +1255,14 @@ int gconv_scan_fwd(const gconv_scan_desc* d, const void* u, const void* dt, cons
     by_type(d->dtype, [&](auto t) {
         using T = decltype(t);
         scan_prep<T><<<blocks_of(a.places * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw);
-        by_waves(l.nw, [&](auto n) {
-            constexpr int NW = decltype(n)::value;
-            const unsigned blocks = (unsigned)(a.chunks * a.blocks);
+        const unsigned blocks = (unsigned)(a.chunks * a.blocks);
+        by_waves(l.nw, narrow_forward(a), [&](auto n, auto m) {
+            constexpr int NW = decltype(n)::value, SPW = decltype(m)::value;
             if (a.per > 1) {
-                scan_run<T, NW, false, false><<<blocks, NW * 64, 0, hs>>>(a);
-                scan_carry<<<blocks_of(a.chunks / a.per * a.blocks * NW * kSpw * kLanes, 256), 256, 0, hs>>>(a, NW, a.chunks / a.per);
+                scan_run<T, NW, SPW, false, false><<<blocks, NW * 64, 0, hs>>>(a);
+                scan_carry<<<blocks_of(a.chunks / a.per * a.blocks * l.nw * kSpw * kLanes, 256), 256, 0, hs>>>(a, l.nw, a.chunks / a.per);
             }
-            scan_run<T, NW, true, false><<<blocks, NW * 64, 0, hs>>>(a);
+            scan_run<T, NW, SPW, true, false><<<blocks, NW * 64, 0, hs>>>(a);
         });
     });
     return finish();
@@ -1286,14 +1328,16 @@ int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, cons
         using T = decltype(t);
         if (rows > 0) {
             scan_prep<T><<<blocks_of(a.places * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw);
-            by_waves(l.nw, [&](auto n) {
-                constexpr int NW = decltype(n)::value;
-                const unsigned blocks = (unsigned)(a.chunks * a.blocks);
-                scan_run<T, NW, false, true><<<blocks, NW * 64, 0, hs>>>(a);
-                if (a.per > 1) {
-                    scan_carry<<<dim3(blocks_of(a.chunks / a.per * a.blocks * NW * kSpw * kLanes, 256), 2), 256, 0, hs>>>(a, NW, a.chunks / a.per);
-                }
-                scan_back<T, NW><<<blocks, NW * 64, 0, hs>>>(a);
+            const unsigned blocks = (unsigned)(a.chunks * a.blocks);
+            by_waves(l.nw, false, [&](auto n, auto m) {
+                constexpr int NW = decltype(n)::value, SPW = decltype(m)::value;
+                scan_run<T, NW, SPW, false, true><<<blocks, NW * 64, 0, hs>>>(a);
+            });
+            if (a.per > 1)
+                scan_carry<<<dim3(blocks_of(a.chunks / a.per * a.blocks * l.nw * kSpw * kLanes, 256), 2), 256, 0, hs>>>(a, l.nw, a.chunks / a.per);
+            by_waves<true>(l.nw, true, [&](auto n, auto m) {
+                constexpr int NW = decltype(n)::value, SPW = decltype(m)::value;
+                scan_back<T, NW, SPW><<<blocks, NW * 64, 0, hs>>>(a);
             });
             scan_fold_bc<T><<<blocks_of(a.places * a.groups * l.nw, 256), 256, 0, hs>>>(a, l.nw, (T*)db, (T*)dc);
         }
