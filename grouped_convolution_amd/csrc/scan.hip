@@ -112,14 +112,41 @@ __device__ __forceinline__ float softplus_of(float x)
     return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(v), kLn2, w - (v - 1.f));
 }
 
-template <typename T>
-struct Quad {
-    float v[4];
-    __device__ __forceinline__ Quad() {}
-    __device__ __forceinline__ explicit Quad(const Packed<T, 4>& p)
+// V elements of a row as they were loaded. As whole words, not elements: where the
+// ways to load them meet, elements would be taken apart, which waits for the load.
+template <typename T, int V>
+struct Bits {
+    static constexpr int N = (V * (int)sizeof(T) + 3) / 4;
+    struct __attribute__((packed, aligned(sizeof(T)))) Words {
+        uint32_t w[N];
+    };
+    uint32_t w[N];
+    __device__ __forceinline__ float get(int e) const
     {
+        if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[e]);
+        const uint32_t v = w[e / 2];
+        return __builtin_bit_cast(float, e & 1 ? v & 0xffff0000u : v << 16);
+    }
+    // from `row`; unless all of it is there (the same for a workgroup), `have` elements, the others 0
+    __device__ __forceinline__ void load(const T* row, bool whole, int have)
+    {
+        if constexpr (V * sizeof(T) < 4) {
+            w[0] = 0;
+            if (have > 0) w[0] = *(const uint16_t*)row;
+        } else if (whole) {
+            const Words v = *(const Words*)row;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (float)p.e[e];
+            for (int i = 0; i < N; ++i) w[i] = v.w[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = 0;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (e < have) {
+                    if constexpr (sizeof(T) == 4) w[e] = *(const uint32_t*)(row + e);
+                    else w[e / 2] |= (uint32_t) * (const uint16_t*)(row + e) << (e & 1 ? 16 : 0);
+                }
+        }
     }
 };
 
@@ -262,11 +289,10 @@ struct Quads {
 };
 
 template <typename T>
-__device__ __forceinline__ Packed<T, 4> load_quad(const void* p, const int64_t* stride, const Where& w, int64_t t, int quad)
+__device__ __forceinline__ void load_quad(Bits<T, 4>& to, const void* p, const int64_t* stride, const Where& w, int64_t t, int quad)
 {
     const T* row = (const T*)p + w.outer * stride[0] + t * stride[1] + w.c0;
-    if (w.left == kLanes) return *(const Packed<T, 4>*)(row + quad * 4);  // (the same for the whole workgroup)
-    return load_piece<T, 4>(row, quad * 4, w.left);
+    to.load(row + quad * 4, w.left == kLanes, w.left - quad * 4);
 }
 
 template <typename T>
@@ -281,16 +307,14 @@ __device__ __forceinline__ void store_quad(const Where& w, T* row, int quad, con
 
 // dt and dt u of a quad of channels; 0 for a token of no sequence.
 template <typename T>
-__device__ __forceinline__ void step_sizes(const Scan& a, const f4& bias, const Packed<T, 4>& raw, const Packed<T, 4>& u, bool real, f4* dt,
-                                           f4* dtu)
+__device__ __forceinline__ void step_sizes(const Scan& a, const f4& bias, const Bits<T, 4>& raw, const Bits<T, 4>& u, bool real, f4* dt, f4* dtu)
 {
-    const Quad<T> r(raw), uu(u);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        float v = r.v[e] + bias[e];
+        float v = raw.get(e) + bias[e];
         if (a.softplus) v = softplus_of(v);
         (*dt)[e] = real ? v : 0.f;
-        (*dtu)[e] = real ? v * uu.v[e] : 0.f;
+        (*dtu)[e] = real ? v * u.get(e) : 0.f;
     }
 }
 
@@ -311,14 +335,12 @@ __device__ __forceinline__ float silu_of(float z) { return z * sigm(z); }
 
 // dy' of a quad of channels; 0 for a token of no sequence.
 template <typename T>
-__device__ __forceinline__ f4 gated(const Scan& a, const Packed<T, 4>& dy, const Packed<T, 4>& gate, bool real)
+__device__ __forceinline__ f4 gated(const Scan& a, const Bits<T, 4>& dy, const Bits<T, 4>& gate, bool real)
 {
-    const Quad<T> d(dy);
-    f4 v = {d.v[0], d.v[1], d.v[2], d.v[3]};
+    f4 v = {dy.get(0), dy.get(1), dy.get(2), dy.get(3)};
     if (a.gate) {
-        const Quad<T> z(gate);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= silu_of(z.v[e]);
+        for (int e = 0; e < 4; ++e) v[e] *= silu_of(gate.get(e));
     }
     return real ? v : f4{0, 0, 0, 0};
 }
@@ -350,10 +372,10 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         for (int s = 0; s < SPW; ++s) h[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
     }
     struct Raw {
-        Packed<T, 4> u, dt, z, dy;
+        Bits<T, 4> u, dt, z, dy;
         int mark;
     } raw[Q::kPer];
-    Packed<T, 4> cur_u[Q::kPer], cur_z[Q::kPer], old_u[Q::kPer], old_z[Q::kPer];  // of this tile and the one before
+    Bits<T, 4> cur_u[Q::kPer], cur_z[Q::kPer], old_u[Q::kPer], old_z[Q::kPer];  // of this tile and the one before
     int cur_mark[Q::kPer], old_mark[Q::kPer];
     // marks of a tile, a token a lane: asked for a tile ahead, as loads come back in order
     auto mark_of = [&](int tile) { return a.mark[w.place0 + tile * kTile + (m.lane & (kTile - 1))]; };
@@ -364,10 +386,10 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
             const int q = Q::of(i), tok = min(tile * kTile + q / 16, w.n - 1);
             if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
             raw[i].mark = a.mark[w.place0 + tile * kTile + q / 16];
-            raw[i].u = load_quad<T>(a.u, a.u_s, w, w.t0 + tok, quad);
-            raw[i].dt = load_quad<T>(a.dt, a.dt_s, w, w.t0 + tok, quad);
-            if ((OUT || ADJ) && a.gate) raw[i].z = load_quad<T>(a.gate, a.gate_s, w, w.t0 + tok, quad);
-            if (ADJ) raw[i].dy = load_quad<T>(a.dy, a.dy_s, w, w.t0 + tok, quad);
+            load_quad<T>(raw[i].u, a.u, a.u_s, w, w.t0 + tok, quad);
+            load_quad<T>(raw[i].dt, a.dt, a.dt_s, w, w.t0 + tok, quad);
+            if ((OUT || ADJ) && a.gate) load_quad<T>(raw[i].z, a.gate, a.gate_s, w, w.t0 + tok, quad);
+            if (ADJ) load_quad<T>(raw[i].dy, a.dy, a.dy_s, w, w.t0 + tok, quad);
         }
     };
     auto stage = [&](int tile) {  // of what was fetched
@@ -463,16 +485,16 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
                 const int q = Q::of(i), tok = (tile - 1) * kTile + q / 16;
                 if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
                 if (tok >= w.n) continue;
-                const Quad<T> u(last ? cur_u[i] : old_u[i]);
+                const Bits<T, 4> u = last ? cur_u[i] : old_u[i];
                 f4 v = {0, 0, 0, 0};
 #pragma unroll
                 for (int k = 0; k < NW; ++k) v += *(const f4*)&yp[OUT ? (tile - 1) & 1 : 0][OUT ? k : 0][OUT ? q / 16 : 0][quad * 4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fmaf(skip[e], u.v[e], v[e]);
+                for (int e = 0; e < 4; ++e) v[e] = fmaf(skip[e], u.get(e), v[e]);
                 if (a.gate) {
-                    const Quad<T> z(last ? cur_z[i] : old_z[i]);
+                    const Bits<T, 4> z = last ? cur_z[i] : old_z[i];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] *= silu_of(z.v[e]);
+                    for (int e = 0; e < 4; ++e) v[e] *= silu_of(z.get(e));
                 }
                 const bool real = (last ? cur_mark[i] : old_mark[i]) >= 0;
                 float o[4];
@@ -643,7 +665,7 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
         }
     }
     struct Raw {
-        Packed<T, V> u, dt, z, dy;
+        Bits<T, V> u, dt, z, dy;
         int mark;
     };
     Raw raw[kPer], next[kPer];
@@ -652,11 +674,7 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
         return (const T*)p + w.outer * stride[0] + (w.t0 + in0) * stride[1] + w.c0 + col;
     };
     const T *pu = first(a.u, a.u_s), *pdt = first(a.dt, a.dt_s), *pz = a.gate ? first(a.gate, a.gate_s) : nullptr, *pdy = first(a.dy, a.dy_s);
-    auto load = [&](const T* p, int64_t step, int tok) {
-        const T* q = p + (tok - in0) * step;
-        if (whole) return *(const Packed<T, V>*)q;
-        return load_piece<T, V>(q - col, col, w.left);
-    };
+    auto load = [&](Bits<T, V>& to, const T* p, int64_t step, int tok) { to.load(p + (tok - in0) * step, whole, w.left - col); };
     auto fetch = [&](Raw (&to)[kPer], int tile) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -664,10 +682,10 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
             to[i].mark = -1;
             if (!works || tok >= w.n) continue;
             to[i].mark = a.mark[w.place0 + tok];
-            to[i].u = load(pu, a.u_s[1], tok);
-            to[i].dt = load(pdt, a.dt_s[1], tok);
-            if (a.gate) to[i].z = load(pz, a.gate_s[1], tok);
-            to[i].dy = load(pdy, a.dy_s[1], tok);
+            load(to[i].u, pu, a.u_s[1], tok);
+            load(to[i].dt, pdt, a.dt_s[1], tok);
+            if (a.gate) load(to[i].z, pz, a.gate_s[1], tok);
+            load(to[i].dy, pdy, a.dy_s[1], tok);
         }
     };
     auto stage = [&]() {
@@ -679,12 +697,12 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
             fv dt, dtu, dy;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                float v = (float)raw[i].dt.e[e] + bias[e];
+                float v = raw[i].dt.get(e) + bias[e];
                 if (a.softplus) v = softplus_of(v);
                 dt[e] = real ? v : 0.f;
-                dtu[e] = real ? v * (float)raw[i].u.e[e] : 0.f;
-                float y = (float)raw[i].dy.e[e];
-                if (a.gate) y *= silu_of((float)raw[i].z.e[e]);
+                dtu[e] = real ? v * raw[i].u.get(e) : 0.f;
+                float y = raw[i].dy.get(e);
+                if (a.gate) y *= silu_of(raw[i].z.get(e));
                 dy[e] = real ? y : 0.f;
             }
             *(fv*)&row[0][col] = dt;
@@ -813,10 +831,10 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
                 float du[V], dd[V], dz[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float u = (float)raw[i].u.e[e];
+                    const float u = raw[i].u.get(e);
                     du[e] = real ? fmaf(dt[e], fed[e], skip[e] * dy[e]) : 0.f;
                     float v = fmaf(u, fed[e], moved[e]);
-                    if (a.softplus) v *= sigm((float)raw[i].dt.e[e] + bias[e]);
+                    if (a.softplus) v *= sigm(raw[i].dt.get(e) + bias[e]);
                     dd[e] = real ? v : 0.f;
                     s_bias[e] += dd[e];
                     s_skip[e] = real ? fmaf(dy[e], u, s_skip[e]) : s_skip[e];
@@ -839,8 +857,8 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
                     for (int k = 0; k < NW; ++k) y += *(const fv*)&part[2][k][in][col];
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        const float z = (float)raw[i].z.e[e], sg = sigm(z);
-                        const float v = (float)raw[i].dy.e[e] * fmaf(skip[e], (float)raw[i].u.e[e], y[e]) * (sg * fmaf(z, 1.f - sg, 1.f));
+                        const float z = raw[i].z.get(e), sg = sigm(z);
+                        const float v = raw[i].dy.get(e) * fmaf(skip[e], raw[i].u.get(e), y[e]) * (sg * fmaf(z, 1.f - sg, 1.f));
                         dz[e] = real ? v : 0.f;
                     }
                     store(a.dgate, dz);
@@ -974,6 +992,7 @@ __global__ __launch_bounds__(256) void scan_step(Step a)
     const bool live = ch < a.dim;
     const int64_t at = (int64_t)ch * a.states + s0;
     const int have = live ? min(kSpw, a.states - s0) : 0;
+    const bool whole = a.states % 4 == 0;  // (then have is 4 or not above 0)
     f4 a2 = {0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < kSpw; ++s)
@@ -993,17 +1012,20 @@ __global__ __launch_bounds__(256) void scan_step(Step a)
             float dt = (float)((const T*)a.dt)[i * a.dt_s + ch] + bias;
             if (a.gate) z = (float)((const T*)a.gate)[i * a.gate_s + ch];
             float* h = a.state + slot * a.dim * a.states + at;
-            const Packed<float, 4> old = load_piece<float, 4>(h, 0, have);
-            const Packed<T, 4> b = load_piece<T, 4>((const T*)a.b + i * a.b_s[0] + g * a.b_s[1], s0, a.states);
-            const Packed<T, 4> c = load_piece<T, 4>((const T*)a.c + i * a.c_s[0] + g * a.c_s[1], s0, a.states);
+            Bits<float, 4> old;
+            Bits<T, 4> b, c;
+            old.load(h, whole, have);
+            b.load((const T*)a.b + i * a.b_s[0] + g * a.b_s[1] + s0, whole, have);
+            c.load((const T*)a.c + i * a.c_s[0] + g * a.c_s[1] + s0, whole, have);
             if (a.softplus) dt = softplus_of(dt);
             float now[4];
 #pragma unroll
             for (int s = 0; s < kSpw; ++s) {
-                now[s] = fmaf(__builtin_amdgcn_exp2f(dt * a2[s]), old.e[s], dt * u * (float)b.e[s]);
-                sum = s < have ? fmaf((float)c.e[s], now[s], sum) : sum;
+                now[s] = fmaf(__builtin_amdgcn_exp2f(dt * a2[s]), old.get(s), dt * u * b.get(s));
+                sum = s < have ? fmaf(c.get(s), now[s], sum) : sum;
             }
-            store_piece<float, 4>(h, 0, have, now);
+            if (whole) *(Packed<float, 4>*)h = Packed<float, 4>{{now[0], now[1], now[2], now[3]}};
+            else store_piece<float, 4>(h, 0, have, now);
         }
         for (int k = a.per / 2; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
         if (live && lane == 0) {
