@@ -355,6 +355,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     using Q = Quads<T, NW, kTile>;
     constexpr int kW = ADJ ? 3 : 2;
     __shared__ float sd[2][kTile][kW][kLanes];            // dt, dt u (, dy')
+    __shared__ f4 sbc[2][NW * SPW / 4][kTile][2];          // b and c of the tile
     __shared__ float yp[OUT ? 2 : 1][OUT ? NW : 1][OUT ? kTile : 1][kLanes];
     const Where w = where(a);
     const Mine<SPW> m = Mine<SPW>::of(a, w);
@@ -380,7 +381,12 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     // marks of a tile, a token a lane: asked for a tile ahead, as loads come back in order
     auto mark_of = [&](int tile) { return a.mark[w.place0 + tile * kTile + (m.lane & (kTile - 1))]; };
     int mk = mark_of(0), mk_next = -1;
+    constexpr int kFours = NW * SPW / 4;
+    f4 raw_bc;
+    const bool brings = (int)threadIdx.x < kFours * kTile * 2;  // 16 bytes of b or c a tile
+    const float* bc = a.bc + (((int64_t)w.g * kFours + threadIdx.x / (kTile * 2)) * a.places + w.place0) * 8 + threadIdx.x % (kTile * 2) * 4;
     auto fetch = [&](int tile) {
+        if (brings) raw_bc = *(const f4*)(bc + tile * kTile * 8);
 #pragma unroll
         for (int i = 0; i < Q::kPer; ++i) {
             const int q = Q::of(i), tok = min(tile * kTile + q / 16, w.n - 1);
@@ -393,6 +399,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         }
     };
     auto stage = [&](int tile) {  // of what was fetched
+        if (brings) (&sbc[tile & 1][0][0][0])[threadIdx.x] = raw_bc;
 #pragma unroll
         for (int i = 0; i < Q::kPer; ++i) {
             const int q = Q::of(i);
@@ -415,12 +422,8 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         }
     };
     const int tiles = (w.n + kTile - 1) / kTile;
-    const scalar_floats bc = (scalar_floats)(a.bc + (m.four(a, w.g, NW * SPW / 4) + w.place0) * 8 + m.within());
-    Ahead<kTile> ahead;
     fetch(0);
-    ahead.ask(bc);
     stage(0);
-    ahead.settle();
     __syncthreads();
     // One barrier a tile: while the waves run over a tile, its outputs go to one
     // buffer, those of the tile before are read from the other, and the next
@@ -429,7 +432,6 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         if (tile + 1 < tiles) {
             mk_next = mark_of(tile + 1);
             fetch(tile + 1);
-            ahead.ask(bc + (tile + 1) * kTile * 8);
         }
         if (tile < tiles) {
             const uint32_t firsts = (uint32_t)__ballot(mk >= 0 && (mk & FIRST)) & ((1u << kTile) - 1);
@@ -447,18 +449,19 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
                     broken = 1;
                 }
                 const float dt = sd[tile & 1][i][0][m.lane], dtu = sd[tile & 1][i][1][m.lane];
-                const scalar_floats o = bc + (tile * kTile + i) * 8;
+                const float* o = (const float*)&sbc[tile & 1][m.wave * SPW / 4][i][0] + m.within();
+                const fs ob = *(const fs*)o, oc = *(const fs*)(o + 4);
                 float y = 0.f, dy = 0.f;
                 if (ADJ) dy = sd[tile & 1][i][kW - 1][m.lane];
                 if (!OUT) total += dt;
 #pragma unroll
                 for (int s = 0; s < SPW; ++s) {
                     const float e = __builtin_amdgcn_exp2f(dt * a2[s]);
-                    h[s] = fmaf(e, h[s], dtu * o[s]);
-                    if (OUT) y = fmaf(o[4 + s], h[s], y);
+                    h[s] = fmaf(e, h[s], dtu * ob[s]);
+                    if (OUT) y = fmaf(oc[s], h[s], y);
                     if (ADJ) {
                         p[s] *= e;
-                        r[s] = fmaf(p[s], o[4 + s] * dy, r[s]);
+                        r[s] = fmaf(p[s], oc[s] * dy, r[s]);
                     }
                 }
                 if (OUT) yp[tile & 1][OUT ? m.wave : 0][OUT ? i : 0][m.lane] = y;
@@ -505,7 +508,6 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         }
         if (tile + 1 < tiles) {
             stage(tile + 1);
-            ahead.settle();
         }
         mk = mk_next;
         __syncthreads();
