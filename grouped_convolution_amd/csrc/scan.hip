@@ -1041,6 +1041,7 @@ __global__ __launch_bounds__(256) void scan_step(Step a)
 // ---- host ------------------------------------------------------------------------
 
 constexpr int kMaxStates = 64;
+constexpr int64_t kCus = 256;
 constexpr int64_t kMaxDim = (int64_t)1 << 20;  // (times 64 states of 4 bytes: a sequence's states stay below 2^31 bytes)
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
 
@@ -1076,9 +1077,12 @@ struct Layout {
     size_t bc, mark, ends, adds, sums, breaks, hist, hist_sum, part_a, part_d, part_bc, bytes;
 };
 
-// Workgroups of the forward pass that leave no CU without work. A sequence is
-// cut only as far as it takes to have them: each chunk is run over twice.
-constexpr int64_t kForwardBlocks = 512;
+// Workgroups of the forward pass. A sequence is cut, and then run over twice, only
+// where there is less than one workgroup a CU; then into as many chunks as make
+// three, as many as run at once (32768 tokens of 2048 channels: 568 us in chunks
+// for 768 workgroups, 640 for 512; 4 x 2048 of 4096, 256 workgroups uncut: 265,
+// and 280 in three chunks).
+constexpr int64_t kForwardBlocks = 768;
 // ... and the backward pass, whose longer chunks carry fewer states from one to
 // the next but need as many workgroups.
 constexpr int64_t kBackBlocks = 1024;
@@ -1101,7 +1105,7 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
         chunk = outer_of(d) * a->blocks * ((d->tokens + 127) / 128) >= kBackBlocks ? 128 : 64;
     } else {
         const int64_t have = std::max<int64_t>(1, outer_of(d) * a->blocks);
-        const int64_t per = have * 2 >= kForwardBlocks ? 1 : (kForwardBlocks + have - 1) / have;
+        const int64_t per = have >= kCus ? 1 : (kForwardBlocks + have - 1) / have;
         chunk = std::max<int64_t>(4 * kTile, ((d->tokens + per - 1) / per + kTile - 1) / kTile * kTile);
         chunk = std::min<int64_t>(chunk, (int64_t)1 << 30);
     }
@@ -1129,7 +1133,7 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
 
 // Whether the forward pass gives a wave two states: twice the waves where there
 // is no more than a workgroup a CU.
-bool narrow_forward(const Scan& a) { return a.chunks * a.blocks <= 256; }
+bool narrow_forward(const Scan& a) { return a.chunks * a.blocks <= kCus; }
 
 void place(const Layout& l, void* workspace, Scan* a)
 {
