@@ -67,7 +67,7 @@ struct Gemm {
     // DH, DW
     float* sums;         // [splits][rows][cols]
     void* out;           // [rows][cols]: NULL while the sums go on
-    int add, vec;        // sums hold something; out takes four elements at once
+    int add, vec;        // sums hold something; out takes this many elements at once
 };
 
 __device__ __forceinline__ int64_t target_of(const Gemm& a, int row)
@@ -194,16 +194,43 @@ struct AcrossRows {
     }
 };
 
+// v in bfloat16; past its largest value cut off in place of rounded up to infinity.
+__device__ __forceinline__ __bf16 part_of(float v)
+{
+    const __bf16 o = (__bf16)v;
+    return finite_bits(o) || !finite_bits(v) ? o : __builtin_bit_cast(__bf16, (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16));
+}
+
 // v in three bfloat16 parts, whose sum it is but for what lies below the last.
 __device__ __forceinline__ void split3(float v, __bf16 (&o)[3])
 {
-    o[0] = (__bf16)v;
-    // past bfloat16's largest value: cut off in place of rounded up to infinity
-    if (!finite_bits(o[0]) && finite_bits(v)) o[0] = __builtin_bit_cast(__bf16, (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16));
+    o[0] = part_of(v);
     const float r = v - (float)o[0];
     o[1] = (__bf16)r;
     o[2] = (__bf16)(r - (float)o[1]);
 }
+
+// A tile of bfloat16 by way of LDS, so that it is stored in whole lines: a lane of
+// the accumulators holds 8 bytes of each of 16 rows. put() takes the four columns
+// from `col` of row `row` of the tile, the 8-byte pieces of a row at piece ^ (row &
+// 15), so that 16 rows' lie in different banks; store() writes the tile.
+template <int BQ, int BP, int THREADS>
+struct TileOut {
+    static __device__ __forceinline__ void put(char* lds, int row, int col, u2 v)
+    {
+        *(u2*)(lds + row * (BP * 2) + ((col / 4) ^ (row & 15)) * 8) = v;
+    }
+    static __device__ __forceinline__ void store(const char* lds, __bf16* out, int64_t pitch, int rows, int cols)
+    {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < BQ * (BP / 8); i += THREADS) {
+            const int row = i / (BP / 8), col = i % (BP / 8) * 8, x = row & 15;
+            if (row >= rows || col >= cols) continue;
+            const u4 v = *(const u4*)(lds + row * (BP * 2) + ((col / 4) ^ (x & ~1)) * 8);
+            *(u4*)(out + row * pitch + col) = x & 1 ? u4{v[2], v[3], v[0], v[1]} : v;
+        }
+    }
+};
 
 // One BQ x BP tile of an output (of one of its splits). The matrix instruction's
 // rows run along the output's columns, so a lane holds four consecutive elements
@@ -362,41 +389,63 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void xent_gemm(Gemm a)
             a.part[(int64_t)tp * a.rows + i0 + r] = v;
         }
     } else if constexpr (OP == DZ) {
+        using Out = TileOut<BQ, BP, 64 * NW>;
+        constexpr int kParts = sizeof(T) == 2 ? 1 : 3;
 #pragma unroll
         for (int i = 0; i < FQ; ++i) {
             const int row = row0 + i * 16;
-            if (row >= a.rows) continue;
-            const int64_t target = target_of(a, row);
+            const bool there = row < a.rows;
+            const int64_t target = there ? target_of(a, row) : -1;
             const bool counts = target >= 0 && target < a.vocab;
             const float dl = counts ? a.dloss[row] * a.scale : 0.f;
             const float all_of = counts ? (a.dlse ? fmaf(a.dlse[row], a.scale, dl) : dl) : 0.f;
-            const float low = a.lse[row] * kLog2e, up = a.scale * kLog2e;
+            const float low = there ? a.lse[row] * kLog2e : 0.f, up = a.scale * kLog2e;
             const int want = wanted(target - a.col0, col0);
-            __bf16* o = a.dz + (int64_t)row * a.dz_pitch;
 #pragma unroll
             for (int j = 0; j < FP; ++j) {
                 const int col = col0 + j * 16;
-                f4 v;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    v[r] = all_of * __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], up, -low));
-                    if (want == j * 16 + r) v[r] -= dl;
-                    if (!counts || col + r >= a.cols) v[r] = 0.f;
-                }
-                if (col >= a.dz_pitch) continue;
-                if constexpr (sizeof(T) == 2) {
-                    *(u2*)(o + col) = pack4(v);
-                } else {
-                    __bf16 e[4][3];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) split3(v[r], e[r]);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) *(bf4*)(o + k * a.dz_plane + col) = bf4{e[0][k], e[1][k], e[2][k], e[3][k]};
+                    float v = all_of * __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], up, -low));
+                    if (want == j * 16 + r) v -= dl;
+                    if (!counts || col + r >= a.cols) v = 0.f;
+                    acc[i][j][r] = v;
                 }
             }
         }
+        // (a part of float32's is left in the accumulators for the next)
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < FQ; ++i)
+#pragma unroll
+                for (int j = 0; j < FP; ++j) {
+                    bf4 e;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float v = acc[i][j][r];
+                        e[r] = kParts == 1 ? (__bf16)v : part_of(v);
+                        if (kParts > 1) acc[i][j][r] = v - (float)e[r];
+                    }
+                    Out::put(lds, row0 - i0 + i * 16, col0 - j0 + j * 16, __builtin_bit_cast(u2, e));
+                }
+            __syncthreads();
+            Out::store(lds, a.dz + k * a.dz_plane + (int64_t)i0 * a.dz_pitch + j0, a.dz_pitch, a.rows - i0, (int)min(a.dz_pitch - j0, (int64_t)BP));
+        }
     } else {
         float* sums = a.sums ? a.sums + (int64_t)split * a.rows * a.cols : nullptr;
+        if (sizeof(T) == 2 && a.vec == 8 && a.out && !a.add) {
+            using Out = TileOut<BQ, BP, 64 * NW>;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < FQ; ++i)
+#pragma unroll
+                for (int j = 0; j < FP; ++j) Out::put(lds, row0 - i0 + i * 16, col0 - j0 + j * 16, pack4(acc[i][j]));
+            __syncthreads();
+            Out::store(lds, (__bf16*)a.out + (int64_t)i0 * a.cols + j0, a.cols, a.rows - i0, min(a.cols - j0, BP));
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < FQ; ++i) {
             const int row = row0 + i * 16;
@@ -407,7 +456,7 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void xent_gemm(Gemm a)
                 const int col = col0 + j * 16;
                 if (col >= a.cols) continue;
                 f4 v = acc[i][j];
-                const bool whole = a.vec && col + 4 <= a.cols;
+                const bool whole = a.vec > 1 && col + 4 <= a.cols;
                 if (a.add) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
@@ -549,16 +598,16 @@ int check_desc(const gconv_xent_desc* d)
 struct Tile {
     int kind, q, p;
 };
-constexpr Tile kTiles[] = {{0, 256, 256}, {1, 128, 128}, {2, 64, 256}};
+constexpr Tile kTiles[] = {{0, 256, 256}, {1, 128, 128}, {2, 64, 256}, {3, 128, 256}};
 
 // The tile whose whole rounds of 256 workgroups take least, its area over the
 // rate it reaches, counting splits of the reduction where there are any.
 Tile tile_of(int64_t rows, int64_t cols)
 {
-    constexpr double rate[] = {1.0, 0.68, 0.5};
+    constexpr double rate[] = {1.0, 0.68, 0.5, 0.85};
     int best = 0;
     double least = 0;
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const int64_t count = ((rows + kTiles[i].q - 1) / kTiles[i].q) * ((cols + kTiles[i].p - 1) / kTiles[i].p);
         const double cost = (double)((count + 255) / 256) * kTiles[i].q * kTiles[i].p / rate[i];
         if (i == 0 || cost < least) {
@@ -637,7 +686,8 @@ int launch(Gemm a, const Tile& t, hipStream_t st)
     const unsigned n = (unsigned)blocks;
     if (t.kind == 0) xent_gemm<T, 256, 256, 2, 4, OP><<<n, 512, 0, st>>>(a);
     else if (t.kind == 1) xent_gemm<T, 128, 128, 2, 4, OP><<<n, 512, 0, st>>>(a);
-    else xent_gemm<T, 64, 256, 1, 8, OP><<<n, 512, 0, st>>>(a);
+    else if (t.kind == 2) xent_gemm<T, 64, 256, 1, 8, OP><<<n, 512, 0, st>>>(a);
+    else xent_gemm<T, 128, 256, 2, 4, OP><<<n, 512, 0, st>>>(a);
     return GCONV_OK;
 }
 
@@ -700,7 +750,7 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         if ((rc = pack<T>(w, 0, d->dim, d->vocab, d->vocab, d->dim, p.pitch, nullptr, 0, 0, (__bf16*)(ws + p.w), st))) return rc;
     }
     const Operand dz{(const __bf16*)(ws + p.dzs), p.piece, p.rows * p.piece};
-    const int vec = d->dim % 4 == 0;
+    const int vec = d->dim % 8 == 0 ? 8 : d->dim % 4 == 0 ? 4 : 1;
     for (int64_t i = 0; i < p.pieces; ++i) {
         const int64_t v0 = i * p.piece, cols = std::min(p.piece, d->vocab - v0);
         const Operand rows{wp.p + v0 * wp.pitch, wp.pitch, wp.plane};
@@ -735,7 +785,7 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         b.sums = p.dh_splits > 1 || p.pieces > 1 ? (float*)(ws + p.dh_sums) : nullptr;
         b.add = i > 0;
         b.out = p.dh_splits == 1 && i + 1 == p.pieces ? dh : nullptr;
-        b.vec = vec && ((uintptr_t)dh & 15) == 0;
+        b.vec = ((uintptr_t)dh & 15) == 0 ? vec : 1;
         if ((rc = launch<T, DH>(b, p.dh, st))) return rc;
         Gemm c{};
         c.q = dz;
@@ -748,7 +798,7 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         T* to = (T*)dw + v0 * d->dim;
         c.sums = p.dw_splits > 1 ? (float*)(ws + p.dw_sums) : nullptr;
         c.out = p.dw_splits > 1 ? nullptr : to;
-        c.vec = vec && ((uintptr_t)to & 15) == 0;
+        c.vec = ((uintptr_t)to & 15) == 0 ? vec : 1;
         if ((rc = launch<T, DW>(c, p.dw, st))) return rc;
         if (p.dw_splits > 1) {
             const int64_t count = cols * d->dim;
