@@ -12,6 +12,7 @@
 // of a text costs no more than many that do not.
 #include <cmath>
 
+#include "embed_internal.h"
 #include "seq_host.h"
 #include "seq_tokens.h"
 
@@ -41,6 +42,10 @@ struct Embed {
     int64_t slices;           // none where no row can have more tokens than one
     int64_t stretches;        // of columns
     int flat;                 // dy's rows follow one another at its tokens' stride
+    // sums for rows that have tokens alone (embed_internal.h)
+    const float* weight;      // [tokens]
+    void* runs;               // a row's sum, at its tokens' first place
+    int64_t row0, row1;       // rows that are asked for
 };
 
 __device__ __forceinline__ uint32_t key_of(const Embed& a, int64_t t)
@@ -196,7 +201,7 @@ template <int V, int W>
 struct Sum {
     float v[W][V] = {};
     template <typename U>
-    __device__ __forceinline__ void add(const U* row, const int (&col)[W])
+    __device__ __forceinline__ void add(const U* row, const int (&col)[W], float weight = 1.f)
     {
         Packed<U, V> p[W];
 #pragma unroll
@@ -204,7 +209,7 @@ struct Sum {
 #pragma unroll
         for (int k = 0; k < W; ++k)
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[k][e] += (float)p[k].e[e];
+            for (int e = 0; e < V; ++e) v[k][e] = fmaf(weight, (float)p[k].e[e], v[k][e]);
     }
     // first: the column of the lane's first piece, before any was moved
     template <typename U>
@@ -239,12 +244,14 @@ __device__ __forceinline__ const T* dy_row(const Embed& a, uint32_t t)
 
 // Adds dy of the tokens at places [p0, p1), whose numbers the lanes read 64 at a
 // time, eight tokens' rows under way at once.
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool RUNS>
 __device__ __forceinline__ void add_tokens(const Embed& a, const uint32_t* at, uint32_t p0, uint32_t p1, const int (&col)[W], Sum<V, W>& sum)
 {
     const int lane = threadIdx.x & 63;
     for (uint32_t p = p0; p < p1; p += 64) {
         const uint32_t mine = at[min(p + lane, p1 - 1)];
+        const int weight = RUNS ? __builtin_bit_cast(int, a.weight[mine]) : 0;
+        auto weight_of = [&](int i) { return RUNS ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(weight, i)) : 1.f; };
         const int n = (int)min(p1 - p, 64u);
         constexpr int U = 8;
         int i = 0;
@@ -261,15 +268,15 @@ __device__ __forceinline__ void add_tokens(const Embed& a, const uint32_t* at, u
 #pragma unroll
                 for (int k = 0; k < W; ++k)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) sum.v[k][e] += (float)r[q][k].e[e];
+                    for (int e = 0; e < V; ++e) sum.v[k][e] = fmaf(weight_of(i + q), (float)r[q][k].e[e], sum.v[k][e]);
         }
-        for (; i < n; ++i) sum.add(dy_row<T>(a, __builtin_amdgcn_readlane(mine, i)), col);
+        for (; i < n; ++i) sum.add(dy_row<T>(a, __builtin_amdgcn_readlane(mine, i)), col, weight_of(i));
     }
 }
 
 // The slices' sums of rows with more tokens than a slice has: such a row runs
 // into a slice, out of it, or both. A wave a slice and stretch of columns.
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool RUNS>
 __global__ __launch_bounds__(kThreads) void embed_slices(Embed a, int from)
 {
     constexpr int kCols = 64 * W * V;
@@ -283,11 +290,11 @@ __global__ __launch_bounds__(kThreads) void embed_slices(Embed a, int from)
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const uint32_t k = a.key[from][which ? p1 - 1 : p0];
-        if (k >= a.rows) continue;
+        if (k >= a.row1 || (RUNS && k < a.row0)) continue;
         const uint32_t b = a.start[k], e = a.start[k + 1];
         if (e - b <= (uint32_t)a.slice || (which == 0 ? b > p0 : b <= p0)) continue;
         Sum<V, W> sum;
-        add_tokens<T, V, W>(a, a.at[from], max(b, p0), min(e, p1), col, sum);
+        add_tokens<T, V, W, RUNS>(a, a.at[from], max(b, p0), min(e, p1), col, sum);
         sum.store(a.part + (s * 2 + which) * a.dim, col, c0, a.dim, 1.f);
     }
 }
@@ -296,17 +303,18 @@ __global__ __launch_bounds__(kThreads) void embed_slices(Embed a, int from)
 // one's tokens looked up while one is written. The first workgroups take the rows
 // with more tokens than a slice has, each that of the slice in which it begins,
 // from the slices' sums: a quarter of them a wave, then the quarters.
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool RUNS>
 __global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from)
 {
     constexpr int kCols = 64 * W * V;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    auto to = [&](int64_t r, uint32_t b) { return RUNS ? (T*)a.runs + (int64_t)b * a.dim : (T*)a.dtable + r * a.dim; };
     if (blockIdx.x < a.slices) {
         __shared__ float red[kWaves][W][V][64];
         const int64_t s0 = blockIdx.x;
         const uint32_t p0 = (uint32_t)(s0 * a.slice), p1 = (uint32_t)min(s0 * a.slice + a.slice, a.tokens);
         const uint32_t k = a.key[from][p1 - 1];
-        if (k >= a.rows) return;
+        if (k >= a.row1 || (RUNS && k < a.row0)) return;
         const uint32_t b = a.start[k], e = a.start[k + 1];
         if (e - b <= (uint32_t)a.slice || b < p0) return;
         const int64_t s1 = (e - 1) / a.slice + 1, per = (s1 - s0 + kWaves - 1) / kWaves;
@@ -330,24 +338,24 @@ __global__ __launch_bounds__(kThreads) void embed_rows(Embed a, int from)
                     for (int q = 0; q < W; ++q)
 #pragma unroll
                         for (int i = 0; i < V; ++i) sum.v[q][i] += red[w][q][i][lane];
-                sum.store((T*)a.dtable + (int64_t)k * a.dim, col, c0 + lane * V, a.dim, a.scale);
+                sum.store(to(k, b), col, c0 + lane * V, a.dim, a.scale);
             }
         }
         return;
     }
     const int64_t waves = (gridDim.x - a.slices) * kWaves, first = (blockIdx.x - a.slices) * kWaves + wave;
-    const int64_t per = (a.rows + waves - 1) / waves, r0 = first * per, r1 = min(r0 + per, a.rows);
+    const int64_t per = (a.row1 - a.row0 + waves - 1) / waves, r0 = a.row0 + first * per, r1 = min(r0 + per, a.row1);
     if (r0 >= r1) return;
     uint32_t b = a.start[r0], e = a.start[r0 + 1];
     for (int64_t r = r0; r < r1; ++r) {
         const uint32_t next = r + 1 < r1 ? a.start[r + 2] : 0;
-        if (e - b <= (uint32_t)a.slice) {
+        if (e - b <= (uint32_t)a.slice && (!RUNS || e > b)) {
             for (int c0 = 0; c0 < a.dim; c0 += kCols) {
                 Sum<V, W> sum;
                 int col[W];
                 columns<V, W>(c0 + lane * V, a.dim, col);
-                add_tokens<T, V, W>(a, a.at[from], b, e, col, sum);
-                sum.store((T*)a.dtable + r * a.dim, col, c0 + lane * V, a.dim, a.scale);
+                add_tokens<T, V, W, RUNS>(a, a.at[from], b, e, col, sum);
+                sum.store(to(r, b), col, c0 + lane * V, a.dim, a.scale);
             }
         }
         b = e;
@@ -378,11 +386,11 @@ int check_desc(const gconv_embed_desc* d)
 
 // Columns of a lane's piece (16 bytes, or one where a row has not as many) and
 // pieces of a lane.
-void pieces(const gconv_embed_desc* d, int* v, int* w)
+void pieces(bool bf16, int64_t dim, int* v, int* w)
 {
-    const int most = d->dtype == GCONV_BF16 ? 8 : 4;
-    *v = d->dim >= most ? most : 1;
-    *w = d->dim <= 64 * *v ? 1 : 2;
+    const int most = bf16 ? 8 : 4;
+    *v = dim >= most ? most : 1;
+    *w = dim <= 64 * *v ? 1 : 2;
 }
 
 struct Layout {
@@ -393,7 +401,7 @@ void plan(const gconv_embed_desc* d, Embed* a, Layout* l)
 {
     a->tokens = d->sequences * d->tokens;
     a->per_seq = std::max<int64_t>(d->tokens, 1);
-    a->rows = d->rows;
+    a->rows = a->row1 = d->rows;
     a->dim = (int)d->dim;
     a->wide = d->index == GCONV_I64;
     a->scale = (float)d->scale;
@@ -411,7 +419,7 @@ void plan(const gconv_embed_desc* d, Embed* a, Layout* l)
     a->slice = (int)slice;
     a->slices = a->tokens > slice ? (a->tokens + slice - 1) / slice : 0;
     int v, w;
-    pieces(d, &v, &w);
+    pieces(d->dtype == GCONV_BF16, d->dim, &v, &w);
     a->stretches = (a->dim + 64 * v * w - 1) / (64 * v * w);
     Cut cut;
     for (int i = 0; i < 2; ++i) l->key[i] = cut.take(a->tokens * 4);
@@ -429,8 +437,8 @@ int width(int64_t dim, int64_t v)
     return px;
 }
 
-template <typename T>
-int backward(const gconv_embed_desc* d, Embed a, hipStream_t st)
+// The sort; which of the two orders holds its result.
+int sort(Embed a, hipStream_t st)
 {
     int bits = 1;
     while ((a.rows >> bits) > 0) ++bits;
@@ -449,23 +457,101 @@ int backward(const gconv_embed_desc* d, Embed a, hipStream_t st)
         from = to;
     }
     embed_starts<<<(unsigned)((a.rows + kThreads) / kThreads), kThreads, 0, st>>>(a, from);
+    return from;
+}
+
+template <typename T, bool RUNS>
+void sums(const Embed& a, int from, hipStream_t st)
+{
     const unsigned slices = (unsigned)((a.slices * a.stretches + kWaves - 1) / kWaves);
-    const unsigned rows = (unsigned)(a.slices + std::min<int64_t>((a.rows + kWaves - 1) / kWaves, 4096));
-    auto sums = [&](auto v, auto w) {
+    const unsigned rows = (unsigned)(a.slices + std::min<int64_t>((a.row1 - a.row0 + kWaves - 1) / kWaves, 4096));
+    auto go = [&](auto v, auto w) {
         constexpr int V = decltype(v)::value, W = decltype(w)::value;
-        if (slices) embed_slices<T, V, W><<<slices, kThreads, 0, st>>>(a, from);
-        embed_rows<T, V, W><<<rows, kThreads, 0, st>>>(a, from);
+        if (slices) embed_slices<T, V, W, RUNS><<<slices, kThreads, 0, st>>>(a, from);
+        embed_rows<T, V, W, RUNS><<<rows, kThreads, 0, st>>>(a, from);
     };
     int v, w;
-    pieces(d, &v, &w);
+    pieces(sizeof(T) == 2, a.dim, &v, &w);
     constexpr std::integral_constant<int, 16 / sizeof(T)> most;
-    if (v == 1) sums(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-    else if (w == 1) sums(most, std::integral_constant<int, 1>{});
-    else sums(most, std::integral_constant<int, 2>{});
-    return finish();
+    if (v == 1) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    else if (w == 1) go(most, std::integral_constant<int, 1>{});
+    else go(most, std::integral_constant<int, 2>{});
+}
+
+int check_launch(const Embed& a)
+{
+    if (a.slices + 4096 > max_blocks(kThreads) || a.slices * a.stretches / kWaves >= max_blocks(kThreads))
+        return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
+    return GCONV_OK;
+}
+
+void place(const Layout& l, void* workspace, Embed* a)
+{
+    char* w = (char*)workspace;
+    for (int i = 0; i < 2; ++i) {
+        a->key[i] = (uint32_t*)(w + l.key[i]);
+        a->at[i] = (uint32_t*)(w + l.at[i]);
+    }
+    a->counts = (uint32_t*)(w + l.counts);
+    a->start = (uint32_t*)(w + l.start);
+    a->part = (float*)(w + l.part);
+}
+
+gconv_embed_desc desc_of(const EmbedRuns& r)
+{
+    gconv_embed_desc d{};
+    d.dtype = GCONV_BF16;
+    d.index = r.wide ? GCONV_I64 : GCONV_I32;
+    d.sequences = 1;
+    d.tokens = r.tokens;
+    d.rows = r.rows;
+    d.dim = r.dim;
+    d.dy_stride[1] = r.pitch;
+    d.scale = 1.0;
+    return d;
 }
 
 }  // namespace
+
+size_t embed_runs_workspace(const EmbedRuns& r)
+{
+    const gconv_embed_desc d = desc_of(r);
+    Embed a{};
+    Layout l{};
+    plan(&d, &a, &l);
+    return l.bytes;
+}
+
+int embed_runs_sort(EmbedRuns* r, hipStream_t st)
+{
+    const gconv_embed_desc d = desc_of(*r);
+    Embed a{};
+    Layout l{};
+    plan(&d, &a, &l);
+    const int rc = check_launch(a);
+    if (rc != GCONV_OK) return rc;
+    place(l, r->workspace, &a);
+    a.ids = r->ids;
+    r->order = sort(a, st);
+    r->start = a.start;
+    return GCONV_OK;
+}
+
+void embed_runs_sum(const EmbedRuns& r, int64_t row0, int64_t row1, hipStream_t st)
+{
+    const gconv_embed_desc d = desc_of(r);
+    Embed a{};
+    Layout l{};
+    plan(&d, &a, &l);
+    place(l, r.workspace, &a);
+    a.dy = r.src;
+    a.weight = r.weight;
+    a.runs = r.sums;
+    a.row0 = row0;
+    a.row1 = row1;
+    sums<__bf16, true>(a, r.order, st);
+}
+
 }  // namespace gconv
 
 using namespace gconv;
@@ -501,7 +587,7 @@ int gconv_embed_fwd(const gconv_embed_desc* d, const void* table, const void* id
     a.ids = ids;
     a.y = y;
     int v, w;
-    pieces(d, &v, &w);
+    pieces(d->dtype == GCONV_BF16, d->dim, &v, &w);
     const int px = width(d->dim, v), per = kThreads / px;
     // four tokens a thread where that leaves every CU several workgroups (16384 tokens of 2048: 40 us by one, 24 by four)
     const int r = v > 1 && tokens / per >= 4 * 2048 ? 4 : 1;
@@ -539,21 +625,18 @@ int gconv_embed_bwd(const gconv_embed_desc* d, const void* dy, const void* ids, 
     plan(d, &a, &l);
     st = check_workspace(workspace, workspace_bytes, l.bytes);
     if (st != GCONV_OK) return st;
-    if (a.slices + 4096 > max_blocks(kThreads) || a.slices * a.stretches / kWaves >= max_blocks(kThreads)) return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
-    char* w = (char*)workspace;
+    st = check_launch(a);
+    if (st != GCONV_OK) return st;
+    place(l, workspace, &a);
     a.dy = dy;
     a.ids = ids;
     a.dtable = dtable;
-    for (int i = 0; i < 2; ++i) {
-        a.key[i] = (uint32_t*)(w + l.key[i]);
-        a.at[i] = (uint32_t*)(w + l.at[i]);
-    }
-    a.counts = (uint32_t*)(w + l.counts);
-    a.start = (uint32_t*)(w + l.start);
-    a.part = (float*)(w + l.part);
     (void)hipGetLastError();
-    if (d->dtype == GCONV_BF16) return backward<__bf16>(d, a, (hipStream_t)stream);
-    return backward<float>(d, a, (hipStream_t)stream);
+    hipStream_t hs = (hipStream_t)stream;
+    const int order = sort(a, hs);
+    if (d->dtype == GCONV_BF16) sums<__bf16, false>(a, order, hs);
+    else sums<float, false>(a, order, hs);
+    return finish();
 }
 
 }  // extern "C"

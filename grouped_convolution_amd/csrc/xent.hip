@@ -21,13 +21,18 @@
 // (8 bits and a sign each, so that together they are the float32), and the six
 // products of parts that count are added up in float32: what is left out is
 // 2^-23 of a product at most, two of float32's own roundings. A float32 operand that is infinite gives NaN.
-// dz is rounded to bfloat16 (or three parts) as the second products' operand.
+// dz is rounded to bfloat16 (or three parts) as the second products' operand. Of
+// bfloat16's, the target's entry, which outweighs a row's others, would be most of
+// the error in dh and dw (2.4e-3 of their norm, with the outputs' own 1.7e-3): what
+// its rounding leaves is kept in float32 for each token, and dh gets that times
+// the target's row of w, dw that times h, summed over the tokens of a target.
 //
 // Tokens that do not count (a target outside the vocabulary) have rows of zeros
 // in place of their h, so nothing in them reaches dw.
 #include <cmath>
 
 #include "device_util.h"
+#include "embed_internal.h"
 #include "seq_host.h"
 #include "seq_tokens.h"
 
@@ -64,7 +69,11 @@ struct Gemm {
     __bf16* dz;          // [parts][rows][dz_pitch]
     int64_t dz_pitch, dz_plane;
     int vocab;
+    float* left;         // DZ: [rows], what rounding left of the target's dz; DH reads it (NULL: 0)
     // DH, DW
+    Operand w;           // DH: of the whole vocabulary
+    const uint32_t* start;  // DW: where the sums of what is left begin for each column of dz, ...
+    const __bf16* fix;      // ... [tokens][cols] (NULL: none)
     float* sums;         // [splits][rows][cols]
     void* out;           // [rows][cols]: NULL while the sums go on
     int add, vec;        // sums hold something; out takes this many elements at once
@@ -407,7 +416,10 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void xent_gemm(Gemm a)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     float v = all_of * __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], up, -low));
-                    if (want == j * 16 + r) v -= dl;
+                    if (want == j * 16 + r) {
+                        v -= dl;
+                        if (kParts == 1 && counts) a.left[row] = v - (float)(__bf16)v;
+                    }
                     if (!counts || col + r >= a.cols) v = 0.f;
                     acc[i][j][r] = v;
                 }
@@ -435,6 +447,32 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void xent_gemm(Gemm a)
         }
     } else {
         float* sums = a.sums ? a.sums + (int64_t)split * a.rows * a.cols : nullptr;
+        if (sizeof(T) == 2 && split == 0 && (a.left || a.fix)) {
+#pragma unroll
+            for (int i = 0; i < FQ; ++i) {
+                const int row = row0 + i * 16;
+                if (row >= a.rows) continue;
+                const __bf16* from;
+                float weight = 1.f;
+                if constexpr (OP == DH) {
+                    const int64_t target = target_of(a, row);
+                    if (target < 0 || target >= a.vocab) continue;
+                    from = a.w.p + target * a.w.pitch;
+                    weight = a.left[row];
+                } else {
+                    if (a.start[row] == a.start[row + 1]) continue;
+                    from = a.fix + (int64_t)a.start[row] * a.cols;
+                }
+#pragma unroll
+                for (int j = 0; j < FP; ++j) {
+                    const int col = col0 + j * 16;
+                    if (col >= a.cols) continue;
+                    const Packed<__bf16, 4> v = load_piece<__bf16, 4>(from, col, a.cols);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(weight, (float)v.e[r], acc[i][j][r]);
+                }
+            }
+        }
         if (sizeof(T) == 2 && a.vec == 8 && a.out && !a.add) {
             using Out = TileOut<BQ, BP, 64 * NW>;
             __syncthreads();
@@ -634,11 +672,22 @@ struct Plan {
     int64_t lse_tiles;
     int64_t piece, pieces;     // vocabulary entries of a piece
     int dh_splits, dw_splits;
-    size_t h, w, part, picked, dzs, dh_sums, dw_sums, bytes;
+    size_t h, w, part, picked, dzs, dh_sums, dw_sums, left, runs, fix, bytes;
 };
 
 // Whether the products read w itself.
 bool as_it_is(const gconv_xent_desc* d) { return d->dtype == GCONV_BF16 && d->dim % kStepK == 0; }
+
+EmbedRuns runs_of(const gconv_xent_desc* d, const void* targets)
+{
+    EmbedRuns r{};
+    r.ids = targets;
+    r.wide = d->index == GCONV_I64;
+    r.tokens = d->sequences * d->tokens;
+    r.rows = d->vocab;
+    r.dim = d->dim;
+    return r;
+}
 
 // (whether h can be read itself is not known before its address is: the
 // workspace always has room for it)
@@ -672,8 +721,30 @@ void make_plan(const gconv_xent_desc* d, bool back, Plan* p)
         p->dzs = cut.take(p->rows * p->piece * p->parts * 2);
         p->dh_sums = cut.take(p->dh_splits > 1 || p->pieces > 1 ? p->rows * d->dim * 4 * p->dh_splits : 0);
         p->dw_sums = cut.take(p->dw_splits > 1 ? cols * d->dim * 4 * p->dw_splits : 0);
+        if (p->parts == 1) {
+            p->left = cut.take(p->rows * 4);
+            p->runs = cut.take((int64_t)embed_runs_workspace(runs_of(d, nullptr)));
+            p->fix = cut.take(p->rows * d->dim * 2);
+        }
     }
     p->bytes = cut.bytes;
+}
+
+int64_t tiles_of(const Tile& t, int64_t rows, int64_t cols) { return ((rows + t.q - 1) / t.q) * ((cols + t.p - 1) / t.p); }
+
+// Whether every launch of a call stays below what a launch takes, before any is made.
+int check_launches(const gconv_xent_desc* d, const Plan& p, bool back)
+{
+    const int64_t cols = std::min(p.piece, d->vocab), most = max_blocks(512);
+    bool fits = std::max(p.rows, d->vocab) <= max_blocks(256) / (p.pitch / 8) * 256;  // packing
+    if (!back) {
+        fits = fits && tiles_of(p.lse, p.rows, d->vocab) <= most && p.rows / 64 < max_blocks(1024);
+    } else {
+        fits = fits && tiles_of(p.dz, p.rows, cols) <= most && tiles_of(p.dh, p.rows, d->dim) * p.dh_splits <= most &&
+               tiles_of(p.dw, cols, d->dim) * p.dw_splits <= most && (d->dim / 256 + 1) * p.rows <= max_blocks(256) &&
+               (d->dim / 256 + 1) * cols <= max_blocks(256);
+    }
+    return fits ? GCONV_OK : fail(GCONV_ERR_UNSUPPORTED, "too many tokens, entries or elements for a launch");
 }
 
 template <typename T, int OP>
@@ -681,9 +752,7 @@ int launch(Gemm a, const Tile& t, hipStream_t st)
 {
     a.tq = (a.rows + t.q - 1) / t.q;
     a.tp = (a.cols + t.p - 1) / t.p;
-    const int64_t blocks = (int64_t)a.tq * a.tp * a.splits;
-    if (blocks > max_blocks(512)) return fail(GCONV_ERR_UNSUPPORTED, "too many tokens x entries for a launch");
-    const unsigned n = (unsigned)blocks;
+    const unsigned n = (unsigned)((int64_t)a.tq * a.tp * a.splits);
     if (t.kind == 0) xent_gemm<T, 256, 256, 2, 4, OP><<<n, 512, 0, st>>>(a);
     else if (t.kind == 1) xent_gemm<T, 128, 128, 2, 4, OP><<<n, 512, 0, st>>>(a);
     else if (t.kind == 2) xent_gemm<T, 64, 256, 1, 8, OP><<<n, 512, 0, st>>>(a);
@@ -696,7 +765,6 @@ int pack(const void* src, int64_t seq, int64_t tok, int64_t tokens, int64_t rows
          int64_t vocab, __bf16* dst, hipStream_t st)
 {
     const int64_t blocks = (rows * (pitch / 8) + 255) / 256;
-    if (blocks > max_blocks(256)) return fail(GCONV_ERR_UNSUPPORTED, "too many elements for a launch");
     xent_pack<T><<<(unsigned)blocks, 256, 0, st>>>((const T*)src, seq, tok, std::max<int64_t>(tokens, 1), rows, (int)dim, (int)pitch, targets,
                                                    wide, vocab, dst);
     return GCONV_OK;
@@ -749,6 +817,16 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         wp = Operand{(const __bf16*)(ws + p.w), p.pitch, d->vocab * p.pitch};
         if ((rc = pack<T>(w, 0, d->dim, d->vocab, d->vocab, d->dim, p.pitch, nullptr, 0, 0, (__bf16*)(ws + p.w), st))) return rc;
     }
+    EmbedRuns runs = runs_of(d, targets);
+    float* left = sizeof(T) == 2 ? (float*)(ws + p.left) : nullptr;
+    if (left) {
+        runs.workspace = ws + p.runs;
+        runs.src = hp.p;
+        runs.pitch = hp.pitch;
+        runs.weight = left;
+        runs.sums = ws + p.fix;
+        if ((rc = embed_runs_sort(&runs, st))) return rc;
+    }
     const Operand dz{(const __bf16*)(ws + p.dzs), p.piece, p.rows * p.piece};
     const int vec = d->dim % 8 == 0 ? 8 : d->dim % 4 == 0 ? 4 : 1;
     for (int64_t i = 0; i < p.pieces; ++i) {
@@ -773,6 +851,7 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         a.dz = (__bf16*)(ws + p.dzs);
         a.dz_pitch = dz.pitch;
         a.dz_plane = dz.plane;
+        a.left = left;
         if ((rc = launch<T, DZ>(a, p.dz, st))) return rc;
         Gemm b{};
         b.q = dz;
@@ -786,6 +865,12 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         b.add = i > 0;
         b.out = p.dh_splits == 1 && i + 1 == p.pieces ? dh : nullptr;
         b.vec = ((uintptr_t)dh & 15) == 0 ? vec : 1;
+        // (with the last piece every token has what is left of its target's)
+        b.left = i + 1 == p.pieces ? left : nullptr;
+        b.w = wp;
+        b.targets = targets;
+        b.wide = wide;
+        b.vocab = (int)d->vocab;
         if ((rc = launch<T, DH>(b, p.dh, st))) return rc;
         Gemm c{};
         c.q = dz;
@@ -799,6 +884,11 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         c.sums = p.dw_splits > 1 ? (float*)(ws + p.dw_sums) : nullptr;
         c.out = p.dw_splits > 1 ? nullptr : to;
         c.vec = ((uintptr_t)to & 15) == 0 ? vec : 1;
+        if (left) {
+            embed_runs_sum(runs, v0, v0 + cols, st);
+            c.start = runs.start + v0;
+            c.fix = (const __bf16*)runs.sums;
+        }
         if ((rc = launch<T, DW>(c, p.dw, st))) return rc;
         if (p.dw_splits > 1) {
             const int64_t count = cols * d->dim;
@@ -853,6 +943,8 @@ int gconv_xent_fwd(const gconv_xent_desc* d, const void* h, const void* w, const
     if (st != GCONV_OK) return st;
     Plan p{};
     make_plan(d, false, &p);
+    st = check_launches(d, p, false);
+    if (st != GCONV_OK) return st;
     st = check_workspace(workspace, workspace_bytes, p.bytes);
     if (st != GCONV_OK) return st;
     (void)hipGetLastError();
@@ -877,6 +969,8 @@ int gconv_xent_bwd(const gconv_xent_desc* d, const float* dloss, const float* dl
     if (st != GCONV_OK) return st;
     Plan p{};
     make_plan(d, true, &p);
+    st = check_launches(d, p, true);
+    if (st != GCONV_OK) return st;
     st = check_workspace(workspace, workspace_bytes, p.bytes);
     if (st != GCONV_OK) return st;
     hipStream_t hs = (hipStream_t)stream;

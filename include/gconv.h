@@ -609,7 +609,8 @@ int gconv_xent_fwd(const gconv_xent_desc* d, const void* h, const void* w, const
  * Gradients for dloss of loss and dlse of lse (NULL: 0), [sequences, tokens]
  * float32 dense, given the forward pass's lse: dh [sequences, tokens, dim] and
  * dw, dense, of the inputs' type. The logits' gradient is rounded to bfloat16
- * for the products that follow where h and w are bfloat16.
+ * for the products that follow where h and w are bfloat16, but for the target's
+ * entry, whose rounding is made up for.
  */
 int gconv_xent_bwd(const gconv_xent_desc* d, const float* dloss, const float* dlse, const void* h, const void* w, const void* targets,
                    const float* lse, void* dh, void* dw, void* workspace, size_t workspace_bytes, void* stream);

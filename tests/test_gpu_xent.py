@@ -148,6 +148,30 @@ def test_strides(dtype):
     assert torch.equal(loss, G.gconv_xent_fwd(s["h"].cuda(), s["w"].cuda(), s["targets"].cuda())[0])
 
 
+@pytest.mark.parametrize("vocab", [1000, 20000])
+def test_gradients_in_bfloat16_are_off_by_their_own_rounding(vocab):
+    """In the norm. A rounding to bfloat16 of values whose logarithms are spread evenly is off by sqrt(2^-14 / 12 x 3 / (8 ln 2))
+    = 1.66e-3 of them. The target's entry of the logits' gradient is not rounded; the others are, and weigh sqrt(sum p^2)
+    against it, some sqrt(e^4 / 1000) = 0.23 for logits of deviation 2: 1.66e-3 x sqrt(1 + 0.23^2) = 1.7e-3, and a fifth
+    for what random values may be off. With the target's rounded too it would be 2.35e-3."""
+    s = inputs(BF, 500, vocab, 256, ignored=0.1, seed=vocab)
+    s["dloss"] = torch.rand(500, generator=torch.Generator().manual_seed(2)) + 0.5
+    want = R.xent(s["h"], s["w"], s["targets"], 1.0, s["dloss"])
+    h, w, t = s["h"].cuda(), s["w"].cuda(), s["targets"].cuda()
+    _, lse = G.gconv_xent_fwd(h, w, t)
+    for name, v in zip(("dh", "dw"), G.gconv_xent_bwd(s["dloss"].cuda(), h, w, t, lse)):
+        off = float((v.cpu().double() - want[name][0]).norm() / want[name][0].norm())
+        assert off <= 2.0e-3, (name, off)
+
+
+def test_one_target_for_all():
+    """A row of dw that every token adds to: sums of thousands of roundings' rests, joined by slices."""
+    s = inputs(BF, 3000, 700, 72, seed=8)
+    s["targets"][:] = 5
+    s["targets"][::3] = 699
+    compare(s, 1.0)
+
+
 def test_gradient_against_differences():
     """The loss's change along random directions of h and w."""
     s = inputs(F32, 40, 500, 48, ignored=0.2, lse=True, seed=11)

@@ -232,6 +232,14 @@ def test_xent_descriptors(bad, status):
         assert e.value.status == status
 
 
+def test_launches_that_are_too_large():
+    """Refused before anything is enqueued: more tiles, or elements to pack, than one launch takes."""
+    for d in (xent_desc(sequences=1, tokens=1 << 30, vocab=1 << 30, dim=64), xent_desc(sequences=1, tokens=1 << 30, dim=1 << 18)):
+        assert xent_both(d, ws=P(0x7f0000000000000), nws=1 << 62, h=P(0x100000000000000), w=P(0x200000000000000), t=P(0x300000000000000),
+                         loss=P(0x310000000000000), lse=P(0x320000000000000), dloss=P(0x330000000000000), dh=P(0x400000000000000),
+                         dw=P(0x500000000000000)) == (6, 6)
+
+
 @pytest.mark.parametrize("empty", [dict(sequences=0), dict(tokens=0), dict(sequences=0, tokens=0)])
 def test_no_tokens_have_a_workspace_size(empty):
     for dtype in (B.F32, B.BF16):
