@@ -192,12 +192,18 @@ __global__ __launch_bounds__(256) void scan_prep(Scan a, int nw)
 // gradients likewise.
 __global__ __launch_bounds__(256) void scan_empty(Sequences seq, const float* from, float* to, int64_t size)
 {
-    const int64_t n = blockIdx.x;
-    if (seq.cu ? seq.bound((int)n + 1) > seq.bound((int)n) : seq.tokens > 0) return;
-    for (int64_t i = blockIdx.y * 256 + threadIdx.x; i < size; i += gridDim.y * 256) to[n * size + i] = from ? from[n * size + i] : 0.f;
+    for (int64_t n = blockIdx.x; n < seq.count; n += gridDim.x) {
+        if (seq.cu ? seq.bound((int)n + 1) > seq.bound((int)n) : seq.tokens > 0) continue;
+        for (int64_t i = blockIdx.y * 256 + threadIdx.x; i < size; i += gridDim.y * 256) to[n * size + i] = from ? from[n * size + i] : 0.f;
+    }
 }
 
 // ---- parts that the kernels share -------------------------------------------------
+
+// a, with -2e38 (finite times log2(e)) in place of -infinity: it leaves as little of a
+// state, but a step of 0 (of a token of no sequence, say) leaves all of it, where
+// 0 times infinity is not a number.
+__device__ __forceinline__ float rate_of(float a) { return a == -INFINITY ? -2e38f : a; }
 
 // Read-only while the kernel runs, at an address that is the same for a wave: scalar loads.
 typedef const __attribute__((address_space(4))) float* scalar_floats;
@@ -260,6 +266,13 @@ struct Mine {
         fs v;
 #pragma unroll
         for (int s = 0; s < SPW; ++s) v[s] = load_f32(r, offset(s));
+        return v;
+    }
+    __device__ __forceinline__ fs rates(const Scan& a) const
+    {
+        fs v = get(a.dim, a.states, a.a, 0);
+#pragma unroll
+        for (int s = 0; s < SPW; ++s) v[s] = rate_of(v[s]);
         return v;
     }
     __device__ __forceinline__ void put(int dim, int states, float* p, int64_t n, fs v) const
@@ -363,7 +376,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     const int quad = threadIdx.x & 15;
     const f4 bias = channel_quad(a.dt_bias, w, quad), skip = channel_quad(a.skip, w, quad);
 
-    const fs a2 = m.get(a.dim, a.states, a.a, 0) * kLog2e;
+    const fs a2 = m.rates(a) * kLog2e;
     fs h = {}, p = {}, r = {};
     p += 1.f;
     float total = 0.f;
@@ -535,7 +548,7 @@ __global__ __launch_bounds__(256) void scan_carry(Scan a, int nw, int64_t outers
     const int lane = (int)(at % kLanes), state = (int)(at / kLanes % (nw * kSpw)), block = (int)(at / kLanes / (nw * kSpw));
     const int g = block / a.gblocks, in = (block - g * a.gblocks) * kLanes + lane;
     const bool have = in < a.gdim && state < a.states;
-    const float a2 = have ? a.a[(int64_t)(g * a.gdim + in) * a.states + state] * kLog2e : 0.f;
+    const float a2 = have ? rate_of(a.a[(int64_t)(g * a.gdim + in) * a.states + state]) * kLog2e : 0.f;
     const int64_t c0 = outer * a.per;
     const float* sums = a.sums + block * kLanes + lane;
     const bool back = blockIdx.y != 0;
@@ -657,7 +670,7 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
         skip[e] = in && a.skip ? a.skip[w.c0 + col + e] : 0.f;
         s_skip[e] = s_bias[e] = 0.f;
     }
-    const fs av = m.get(a.dim, a.states, a.a, 0), a2 = av * kLog2e;
+    const fs av = m.rates(a), a2 = av * kLog2e;
     fs before0 = {}, g = {}, da = {};  // the state before the chunk; the adjoint after it
     if (a.per > 1) {
 #pragma unroll
@@ -998,7 +1011,7 @@ __global__ __launch_bounds__(256) void scan_step(Step a)
     f4 a2 = {0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < kSpw; ++s)
-        if (s < have) a2[s] = a.a[at + s] * kLog2e;
+        if (s < have) a2[s] = rate_of(a.a[at + s]) * kLog2e;
     const float skip = live && a.skip ? a.skip[ch] : 0.f, bias = live && a.dt_bias ? a.dt_bias[ch] : 0.f;
     for (int64_t i = first; i < min(first + a.along, a.batch); ++i) {
         const int64_t slot = a.slots ? a.slots[i] : i;
@@ -1278,7 +1291,7 @@ int gconv_scan_fwd(const gconv_scan_desc* d, const void* u, const void* dt, cons
     hipStream_t hs = (hipStream_t)stream;
     (void)hipGetLastError();
     if (final_state && d->sequences > 0 && (d->packed || d->tokens == 0))
-        scan_empty<<<dim3((unsigned)d->sequences, (unsigned)std::min<int64_t>(64, (d->dim * d->states + 255) / 256)), 256, 0, hs>>>(a.seq, initial_state, final_state, d->dim * d->states);
+        scan_empty<<<dim3((unsigned)std::min<int64_t>(d->sequences, 1 << 16), (unsigned)std::min<int64_t>(64, (d->dim * d->states + 255) / 256)), 256, 0, hs>>>(a.seq, initial_state, final_state, d->dim * d->states);
     if (rows == 0) return finish();
     by_type(d->dtype, [&](auto t) {
         using T = decltype(t);
@@ -1351,7 +1364,7 @@ int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, cons
     hipStream_t hs = (hipStream_t)stream;
     (void)hipGetLastError();
     if (d_initial_state && d->sequences > 0 && (d->packed || d->tokens == 0))
-        scan_empty<<<dim3((unsigned)d->sequences, (unsigned)std::min<int64_t>(64, (d->dim * d->states + 255) / 256)), 256, 0, hs>>>(a.seq, d_final_state, d_initial_state, d->dim * d->states);
+        scan_empty<<<dim3((unsigned)std::min<int64_t>(d->sequences, 1 << 16), (unsigned)std::min<int64_t>(64, (d->dim * d->states + 255) / 256)), 256, 0, hs>>>(a.seq, d_final_state, d_initial_state, d->dim * d->states);
     by_type(d->dtype, [&](auto t) {
         using T = decltype(t);
         if (rows > 0) {

@@ -163,10 +163,39 @@ def test_strong_and_no_decay():
     want = reference({**s, "a": s["a"].clamp(min=-1e30)}, lens, True)
     kw = dict(skip=s["skip"].cuda(), dt_bias=s["dt_bias"].cuda())
     y, final = G.gconv_scan_fwd(s["u"][None].cuda(), s["dt"][None].cuda(), s["a"].cuda(), s["b"][None].cuda(), s["c"][None].cuda(), **kw)
-    # (a step of 0 times an infinite decay is not a number: the channel whose steps are 0 in float32)
+    # (channel 3's steps are 0 in float32 and 1e-87 in 64 bits, which decays of 1e30 tell apart)
     keep = [i for i in range(20) if i != 3]
     R.check("y", y[0][:, keep], want["y"][0][:, keep], want["y"][1][:, keep])
     R.check("final", final[:, keep], want["final"][0][:, keep], want["final"][1][:, keep])
+    got = dict(zip(("du", "ddt", "da", "db", "dc", "dskip", "dgate", "ddt_bias", "dinit"),
+                   G.gconv_scan_bwd(s["dy"][None].cuda(), s["u"][None].cuda(), s["dt"][None].cuda(), s["a"].cuda(), s["b"][None].cuda(),
+                                    s["c"][None].cuda(), **kw)))
+    for name in ("du", "ddt"):
+        R.check(name, got[name][0][:, keep], want[name][0][:, keep], want[name][1][:, keep])
+    R.check("da", got["da"][keep], want["da"][0][keep], want["da"][1][keep])
+
+
+def test_infinite_decay_in_packed_chunks():
+    """Nothing of the state is left by any token, through chunks that end in tokens of no sequence."""
+    lens = [100, 0, 190]
+    s = inputs(F32, lens, 20, 4, seed=21)
+    s["a"][:, 1], s["a"][::3] = -float("inf"), -float("inf")
+    T, at = 3 + sum(lens) + 200, slice(3, 293)
+    want = reference({**s, "a": s["a"].clamp(min=-1e30)}, lens, True)
+    t = {k: torch.zeros((T,) + s[k].shape[1:]) for k in WIDE + NARROW}
+    for k in t:
+        t[k][at] = s[k]
+        t[k] = t[k].cuda()
+    cu = (torch.tensor([0] + lens).cumsum(0) + 3).to(torch.int32).cuda()
+    kw = dict(skip=s["skip"].cuda(), gate=t["gate"], dt_bias=s["dt_bias"].cuda(), cu_seqlens=cu, initial_state=s["init"].cuda())
+    args = (t["u"], t["dt"], s["a"].cuda(), t["b"], t["c"])
+    y, final = G.gconv_scan_fwd(*args, **kw)
+    R.check("y", y[at], *want["y"])
+    R.check("final", final, *want["final"])
+    got = dict(zip(("du", "ddt", "da", "db", "dc", "dskip", "dgate", "ddt_bias", "dinit"),
+                   G.gconv_scan_bwd(t["dy"], *args, d_final_state=s["dfinal"].cuda(), **kw)))
+    for name, v in got.items():
+        R.check(name, v[at] if name in ("du", "ddt", "db", "dc", "dgate") else v, *want[name])
 
 
 def test_what_is_not_a_number_stays_in_its_channel_and_time():
