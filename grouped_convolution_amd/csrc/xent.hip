@@ -775,7 +775,7 @@ int forward(const gconv_xent_desc* d, const Plan& p, const void* h, const void* 
             hipStream_t st)
 {
     const bool flat = d->sequences == 1 || d->tokens == 1 || d->h_stride[0] == d->tokens * d->h_stride[1];
-    const int64_t step = d->tokens == 1 ? d->h_stride[0] : d->h_stride[1];
+    const int64_t step = d->tokens == 1 && d->sequences > 1 ? d->h_stride[0] : d->h_stride[1];
     Gemm a{};
     a.q = Operand{(const __bf16*)h, step, 0};
     a.p = Operand{(const __bf16*)w, d->dim, 0};
