@@ -12,6 +12,9 @@
 // in the cache. The backward pass computes p again rather than keep it. The
 // weights' sums are float32 in registers over a chunk, over the workgroup's
 // chunks in LDS, and over workgroups in a second kernel, each in a fixed order.
+//
+// Measured (4 x 4096 tokens of 4096, bf16, four taps, silu): forward 52 us, 5.2
+// TB/s; backward 89 us, 4.5 TB/s.
 #include "seq_host.h"
 #include "seq_tokens.h"
 
@@ -527,10 +530,14 @@ int piece_of(const gconv_shortconv_desc* d, Use use)
     return use == STEP ? (d->dim % v == 0 ? v : 1) : (d->dim >= v ? v : 1);
 }
 
-// The launch: as long chunks as leave enough threads (a chunk's first K - 1
-// tokens are read by two).
-void plan(const gconv_shortconv_desc* d, Use use, bool states, int longest, Conv* a)
+// The launch: as long chunks as leave enough threads: a chunk's first K - 1 tokens
+// are read by two, and backward worked at by two (4 x 4096 tokens of 4096, bf16,
+// chunks of 32, 64 and 128: backward 111, 96 and 89 us; forward 52, 53 by 32 and
+// 64).
+void plan(const gconv_shortconv_desc* d, Use use, bool states, Conv* a)
 {
+    const int longest = use == BACKWARD ? 128 : 32;
+    const int64_t enough = (int64_t)1 << (use == BACKWARD ? 17 : 18);
     const int v = piece_of(d, use);
     const int64_t pieces = (d->dim + v - 1) / v;
     int px = 1;
@@ -538,7 +545,7 @@ void plan(const gconv_shortconv_desc* d, Use use, bool states, int longest, Conv
     a->px = px;
     a->nx = (int)((pieces + px - 1) / px);
     int chunk = longest;
-    while (chunk > 4 && pieces * outer_of(d) * ((d->tokens + chunk - 1) / chunk) < (int64_t)1 << 18) chunk /= 2;
+    while (chunk > 4 && pieces * outer_of(d) * ((d->tokens + chunk - 1) / chunk) < enough) chunk /= 2;
     a->chunk = chunk;
     a->per = std::max<int64_t>(1, (d->tokens + chunk - 1) / chunk);
     a->chunks = d->tokens > 0 ? outer_of(d) * a->per : 0;
@@ -554,8 +561,6 @@ void plan(const gconv_shortconv_desc* d, Use use, bool states, int longest, Conv
     a->dy_seq = d->packed ? 0 : d->dy_stride[0];
     a->dy_tok = d->dy_stride[1];
 }
-
-constexpr int kFwdChunk = 32, kBwdChunk = 32;
 
 int check_blocks(const Conv& a)
 {
@@ -605,7 +610,7 @@ int gconv_shortconv_workspace_size(const gconv_shortconv_desc* d, size_t* bytes)
     if (st != GCONV_OK) return st;
     if (!bytes) return fail(GCONV_ERR_NULL, "bytes pointer is NULL");
     Conv a{};
-    plan(d, BACKWARD, true, kBwdChunk, &a);
+    plan(d, BACKWARD, true, &a);
     *bytes = (size_t)a.chunk_blocks * (d->taps + 1) * d->dim * 4;
     return GCONV_OK;
 }
@@ -624,7 +629,7 @@ int gconv_shortconv_fwd(const gconv_shortconv_desc* d, const void* x, const void
     st = check_overlap(in, out);
     if (st != GCONV_OK) return st;
     Conv a{};
-    plan(d, FORWARD, final_state && d->taps > 1, kFwdChunk, &a);
+    plan(d, FORWARD, final_state && d->taps > 1, &a);
     st = check_blocks(a);
     if (st != GCONV_OK) return st;
     a.x = x;
@@ -661,7 +666,7 @@ int gconv_shortconv_bwd(const gconv_shortconv_desc* d, const void* dy, const voi
     st = check_overlap(in, out);
     if (st != GCONV_OK) return st;
     Conv a{};
-    plan(d, BACKWARD, d_initial_state && d->taps > 1, kBwdChunk, &a);
+    plan(d, BACKWARD, d_initial_state && d->taps > 1, &a);
     st = check_blocks(a);
     if (st != GCONV_OK) return st;
     st = check_workspace(workspace, workspace_bytes, (size_t)a.chunk_blocks * (d->taps + 1) * d->dim * 4);
