@@ -705,11 +705,12 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
             const int in = in0 + i * (kThreads / kRow), tok = tile * kBack + in;
             to[i].mark = -1;
             if (!works || tok >= w.n) continue;
-            to[i].mark = a.mark[w.place0 + tok];
-            load(to[i].u, pu, a.u_s[1], tok);
-            load(to[i].dt, pdt, a.dt_s[1], tok);
-            if (a.gate) load(to[i].z, pz, a.gate_s[1], tok);
-            load(to[i].dy, pdy, a.dy_s[1], tok);
+            const auto* k = again();
+            to[i].mark = k->mark[w.place0 + tok];
+            load(to[i].u, pu, k->u_s[1], tok);
+            load(to[i].dt, pdt, k->dt_s[1], tok);
+            if (k->gate) load(to[i].z, pz, k->gate_s[1], tok);
+            load(to[i].dy, pdy, k->dy_s[1], tok);
         }
     };
     auto stage = [&]() {
@@ -851,7 +852,8 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
                     fed += *(const fv*)&part[0][k][in][col];
                     moved += *(const fv*)&part[1][k][in][col];
                 }
-                const int64_t row = (w.row0 + tok) * a.dim + w.c0;
+                const auto* k = again();
+                const int64_t row = (w.row0 + tok) * k->dim + w.c0;
                 float du[V], dd[V], dz[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -874,9 +876,9 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
                     for (int e = 0; e < V; ++e) o.e[e] = (T)v[e];
                     *(Packed<T, V>*)(q + col) = o;
                 };
-                store(a.du, du);
-                store(a.ddt, dd);
-                if (a.gate) {
+                store(k->du, du);
+                store(k->ddt, dd);
+                if (k->gate) {
 #pragma unroll
                     for (int k = 0; k < NW; ++k) y += *(const fv*)&part[2][k][in][col];
 #pragma unroll
@@ -885,7 +887,7 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
                         const float v = raw[i].dy.get(e) * fmaf(skip[e], raw[i].u.get(e), y[e]) * (sg * fmaf(z, 1.f - sg, 1.f));
                         dz[e] = real ? v : 0.f;
                     }
-                    store(a.dgate, dz);
+                    store(k->dgate, dz);
                 }
             }
         }
