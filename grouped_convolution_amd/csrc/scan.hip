@@ -302,37 +302,43 @@ struct Mine {
     }
 };
 
-// A thread's quads of a tile: quad q is token q / 16, channels 4 (q % 16).
-template <typename T, int NW, int TILE>
-struct Quads {
-    static constexpr int kCount = TILE * 16, kThreads = NW * 64;
-    static constexpr int kPer = (kCount + kThreads - 1) / kThreads;
+// A workgroup's pieces of a tile of tokens, V channels each: as many as make one a
+// thread, so that all waves share what is done for (token, channel) alone.
+template <int NW, int TILE>
+struct Pieces {
+    static constexpr int V = TILE / NW < 1 ? 1 : TILE / NW > 4 ? 4 : TILE / NW;
+    static constexpr int kRow = kLanes / V, kThreads = NW * 64, kPer = TILE * kRow / kThreads;
+    static_assert(TILE * kRow % kThreads == 0, "whole rounds");
+    typedef float fv __attribute__((ext_vector_type(V)));
     static __device__ __forceinline__ int of(int i) { return i * kThreads + (int)threadIdx.x; }
 };
 
-template <typename T>
-__device__ __forceinline__ void load_quad(Bits<T, 4>& to, const void* p, const int64_t* stride, const Where& w, int64_t t, int quad)
+template <typename T, int V>
+__device__ __forceinline__ void load_at(Bits<T, V>& to, const void* p, const int64_t* stride, const Where& w, int64_t t, int col)
 {
     const T* row = (const T*)p + w.outer * stride[0] + t * stride[1] + w.c0;
-    to.load(row + quad * 4, w.left == kLanes, w.left - quad * 4);
+    to.load(row + col, w.left == kLanes, w.left - col);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_quad(const Where& w, T* row, int quad, const float (&v)[4])
+template <typename T, int V>
+__device__ __forceinline__ void store_at(const Where& w, T* row, int col, const float (&v)[V])
 {
-    if (w.left == kLanes) {
-        *(Packed<T, 4>*)(row + quad * 4) = Packed<T, 4>{{(T)v[0], (T)v[1], (T)v[2], (T)v[3]}};
+    if (w.left != kLanes) {
+        store_piece<T, V>(row, col, w.left, v);
         return;
     }
-    store_piece<T, 4>(row, quad * 4, w.left, v);
+    Packed<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o.e[e] = (T)v[e];
+    *(Packed<T, V>*)(row + col) = o;
 }
 
-// dt and dt u of a quad of channels; 0 for a token of no sequence.
-template <typename T>
-__device__ __forceinline__ void step_sizes(const Scan& a, const f4& bias, const Bits<T, 4>& raw, const Bits<T, 4>& u, bool real, f4* dt, f4* dtu)
+// dt and dt u of a piece; 0 for a token of no sequence.
+template <typename T, int V, typename F>
+__device__ __forceinline__ void step_sizes(const Scan& a, const F& bias, const Bits<T, V>& raw, const Bits<T, V>& u, bool real, F* dt, F* dtu)
 {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < V; ++e) {
         float v = raw.get(e) + bias[e];
         if (a.softplus) v = softplus_of(v);
         (*dt)[e] = real ? v : 0.f;
@@ -340,13 +346,14 @@ __device__ __forceinline__ void step_sizes(const Scan& a, const f4& bias, const 
     }
 }
 
-__device__ __forceinline__ f4 channel_quad(const float* p, const Where& w, int quad)
+template <typename F, int V>
+__device__ __forceinline__ F of_channels(const float* p, const Where& w, int col)
 {
-    f4 v = {0, 0, 0, 0};
+    F v = {};
     if (p) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (quad * 4 + e < w.left) v[e] = p[w.c0 + quad * 4 + e];
+        for (int e = 0; e < V; ++e)
+            if (col + e < w.left) v[e] = p[w.c0 + col + e];
     }
     return v;
 }
@@ -355,16 +362,18 @@ __device__ __forceinline__ f4 channel_quad(const float* p, const Where& w, int q
 __device__ __forceinline__ float sigm(float z) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -kLog2e)); }
 __device__ __forceinline__ float silu_of(float z) { return z * sigm(z); }
 
-// dy' of a quad of channels; 0 for a token of no sequence.
-template <typename T>
-__device__ __forceinline__ f4 gated(const Scan& a, const Bits<T, 4>& dy, const Bits<T, 4>& gate, bool real)
+// dy' of a piece; 0 for a token of no sequence.
+template <typename F, typename T, int V>
+__device__ __forceinline__ F gated(const Scan& a, const Bits<T, V>& dy, const Bits<T, V>& gate, bool real)
 {
-    f4 v = {dy.get(0), dy.get(1), dy.get(2), dy.get(3)};
-    if (a.gate) {
+    F v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= silu_of(gate.get(e));
+    for (int e = 0; e < V; ++e) {
+        v[e] = dy.get(e);
+        if (a.gate) v[e] *= silu_of(gate.get(e));
+        v[e] = real ? v[e] : 0.f;
     }
-    return real ? v : f4{0, 0, 0, 0};
+    return v;
 }
 
 // ---- forward ----------------------------------------------------------------------
@@ -374,7 +383,9 @@ __device__ __forceinline__ f4 gated(const Scan& a, const Bits<T, 4>& dy, const B
 template <typename T, int NW, int SPW, bool OUT, bool ADJ>
 __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
 {
-    using Q = Quads<T, NW, kTile>;
+    using Q = Pieces<NW, kTile>;
+    constexpr int V = Q::V;
+    typedef typename Q::fv fv;
     constexpr int kW = ADJ ? 3 : 2;
     __shared__ float sd[2][kTile][kW][kLanes];            // dt, dt u (, dy')
     __shared__ f4 sbc[2][NW * SPW / 4][kTile][2];          // b and c of the tile
@@ -382,8 +393,8 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     const Where w = where(a);
     const Mine<SPW> m = Mine<SPW>::of(a, w);
     typedef typename Mine<SPW>::fs fs;
-    const int quad = threadIdx.x & 15;
-    const f4 bias = channel_quad(a.dt_bias, w, quad), skip = channel_quad(a.skip, w, quad);
+    const int col = threadIdx.x % Q::kRow * V;
+    const fv bias = of_channels<fv, V>(a.dt_bias, w, col), skip = of_channels<fv, V>(a.skip, w, col);
 
     const fs a2 = m.rates(a) * kLog2e;
     fs h = {}, p = {}, r = {};
@@ -395,10 +406,10 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         for (int s = 0; s < SPW; ++s) h[s] = a.ends[m.slot(a, w.chunk, w.block, NW, s)];
     }
     struct Raw {
-        Bits<T, 4> u, dt, z, dy;
+        Bits<T, V> u, dt, z, dy;
         int mark;
     } raw[Q::kPer];
-    Bits<T, 4> cur_u[Q::kPer], cur_z[Q::kPer], old_u[Q::kPer], old_z[Q::kPer];  // of this tile and the one before
+    Bits<T, V> cur_u[Q::kPer], cur_z[Q::kPer], old_u[Q::kPer], old_z[Q::kPer];  // of this tile and the one before
     int cur_mark[Q::kPer], old_mark[Q::kPer];
     // marks of a tile, a token a lane: asked for a tile ahead, as loads come back in order
     auto mark_of = [&](int tile) { return a.mark[w.place0 + tile * kTile + (m.lane & (kTile - 1))]; };
@@ -411,28 +422,25 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
         if (brings) raw_bc = *(const f4*)(bc + tile * kTile * 8);
 #pragma unroll
         for (int i = 0; i < Q::kPer; ++i) {
-            const int q = Q::of(i), tok = min(tile * kTile + q / 16, w.n - 1);
-            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
-            raw[i].mark = a.mark[w.place0 + tile * kTile + q / 16];
-            load_quad<T>(raw[i].u, a.u, a.u_s, w, w.t0 + tok, quad);
-            load_quad<T>(raw[i].dt, a.dt, a.dt_s, w, w.t0 + tok, quad);
-            if ((OUT || ADJ) && a.gate) load_quad<T>(raw[i].z, a.gate, a.gate_s, w, w.t0 + tok, quad);
-            if (ADJ) load_quad<T>(raw[i].dy, a.dy, a.dy_s, w, w.t0 + tok, quad);
+            const int q = Q::of(i), in = q / Q::kRow, tok = min(tile * kTile + in, w.n - 1);
+            raw[i].mark = a.mark[w.place0 + tile * kTile + in];
+            load_at<T, V>(raw[i].u, a.u, a.u_s, w, w.t0 + tok, col);
+            load_at<T, V>(raw[i].dt, a.dt, a.dt_s, w, w.t0 + tok, col);
+            if ((OUT || ADJ) && a.gate) load_at<T, V>(raw[i].z, a.gate, a.gate_s, w, w.t0 + tok, col);
+            if (ADJ) load_at<T, V>(raw[i].dy, a.dy, a.dy_s, w, w.t0 + tok, col);
         }
     };
     auto stage = [&](int tile) {  // of what was fetched
         if (brings) (&sbc[tile & 1][0][0][0])[threadIdx.x] = raw_bc;
 #pragma unroll
         for (int i = 0; i < Q::kPer; ++i) {
-            const int q = Q::of(i);
-            if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
             const bool real = raw[i].mark >= 0;
-            f4 dt, dtu;
-            step_sizes<T>(a, bias, raw[i].dt, raw[i].u, real, &dt, &dtu);
-            float(*row)[kLanes] = sd[tile & 1][q / 16];
-            *(f4*)&row[0][quad * 4] = dt;
-            *(f4*)&row[1][quad * 4] = dtu;
-            if constexpr (ADJ) *(f4*)&row[kW - 1][quad * 4] = gated<T>(a, raw[i].dy, raw[i].z, real);
+            fv dt, dtu;
+            step_sizes<T, V>(a, bias, raw[i].dt, raw[i].u, real, &dt, &dtu);
+            float(*row)[kLanes] = sd[tile & 1][Q::of(i) / Q::kRow];
+            *(fv*)&row[0][col] = dt;
+            *(fv*)&row[1][col] = dtu;
+            if constexpr (ADJ) *(fv*)&row[kW - 1][col] = gated<fv, T, V>(a, raw[i].dy, raw[i].z, real);
             if (OUT) {
                 old_u[i] = cur_u[i];
                 old_z[i] = cur_z[i];
@@ -507,25 +515,24 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
             const bool last = tile == tiles;  // nothing has been staged since
 #pragma unroll
             for (int i = 0; i < Q::kPer; ++i) {
-                const int q = Q::of(i), tok = (tile - 1) * kTile + q / 16;
-                if (Q::kCount < Q::kThreads && q >= Q::kCount) break;
+                const int in = Q::of(i) / Q::kRow, tok = (tile - 1) * kTile + in;
                 if (tok >= w.n) continue;
-                const Bits<T, 4> u = last ? cur_u[i] : old_u[i];
-                f4 v = {0, 0, 0, 0};
+                const Bits<T, V> u = last ? cur_u[i] : old_u[i];
+                fv v = {};
 #pragma unroll
-                for (int k = 0; k < NW; ++k) v += *(const f4*)&yp[OUT ? (tile - 1) & 1 : 0][OUT ? k : 0][OUT ? q / 16 : 0][quad * 4];
+                for (int k = 0; k < NW; ++k) v += *(const fv*)&yp[OUT ? (tile - 1) & 1 : 0][OUT ? k : 0][OUT ? in : 0][col];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fmaf(skip[e], u.get(e), v[e]);
+                for (int e = 0; e < V; ++e) v[e] = fmaf(skip[e], u.get(e), v[e]);
                 if (a.gate) {
-                    const Bits<T, 4> z = last ? cur_z[i] : old_z[i];
+                    const Bits<T, V> z = last ? cur_z[i] : old_z[i];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] *= silu_of(z.get(e));
+                    for (int e = 0; e < V; ++e) v[e] *= silu_of(z.get(e));
                 }
                 const bool real = (last ? cur_mark[i] : old_mark[i]) >= 0;
-                float o[4];
+                float o[V];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = real ? v[e] : 0.f;
-                store_quad<T>(w, (T*)a.y + (w.row0 + tok) * a.dim + w.c0, quad, o);
+                for (int e = 0; e < V; ++e) o[e] = real ? v[e] : 0.f;
+                store_at<T, V>(w, (T*)a.y + (w.row0 + tok) * a.dim + w.c0, col, o);
             }
         }
         if (tile + 1 < tiles) {
