@@ -652,7 +652,7 @@ int check_desc(const gconv_xent_desc* d)
 struct Tile {
     int kind, q, p;
 };
-constexpr Tile kTiles[] = {{0, 256, 256}, {1, 128, 128}, {2, 64, 256}, {3, 128, 256}};
+constexpr Tile kTiles[] = {{0, 256, 256}, {1, 128, 128}, {2, 64, 256}, {3, 128, 256}, {4, 128, 192}};
 
 // Parts of a reduction that a product with few tiles is cut into: as many as
 // there are CUs without work, each at least 8 stages long.
@@ -663,15 +663,16 @@ int splits_of(const Tile& t, int64_t rows, int64_t cols, int64_t stages)
 }
 
 // The tile that takes least: whole rounds of 256 workgroups, each a tile's area
-// over the rate it reaches (8192 tokens x 65536 entries of 2048: 1814, 2665, 3154
-// and 2142 us) for each stage, 65536 of which take 1.8 us; and the splits' sums,
-// which are written and read at 4 TB/s. stages: 0 where there are no splits.
+// over the rate it reaches (8192 tokens x 65536 entries of 2048: LSE 1814, 2665,
+// 3154, 2142 and 2285 us; DH and DW 1700, 2620, 2760, 2000 and 2270) for each
+// stage, 65536 of which take 1.8 us; and the splits' sums, which are written and
+// read at 4 TB/s. stages: 0 for LSE and DZ, which have no splits.
 Tile tile_of(int64_t rows, int64_t cols, int64_t stages)
 {
-    constexpr double rate[] = {1.0, 0.68, 0.57, 0.85};
+    const double rate[] = {1.0, 0.68, 0.57, 0.85, stages ? 0.72 : 0.82};
     int best = 0;
     double least = 0;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 5; ++i) {
         const Tile& t = kTiles[i];
         const int64_t count = ((rows + t.q - 1) / t.q) * ((cols + t.p - 1) / t.p);
         const int splits = stages ? splits_of(t, rows, cols, stages) : 1;
@@ -779,7 +780,8 @@ int launch(Gemm a, const Tile& t, hipStream_t st)
     if (t.kind == 0) xent_gemm<T, 256, 256, 2, 4, OP><<<n, 512, 0, st>>>(a);
     else if (t.kind == 1) xent_gemm<T, 128, 128, 2, 4, OP><<<n, 512, 0, st>>>(a);
     else if (t.kind == 2) xent_gemm<T, 64, 256, 1, 8, OP><<<n, 512, 0, st>>>(a);
-    else xent_gemm<T, 128, 256, 2, 4, OP><<<n, 512, 0, st>>>(a);
+    else if (t.kind == 3) xent_gemm<T, 128, 256, 2, 4, OP><<<n, 512, 0, st>>>(a);
+    else xent_gemm<T, 128, 192, 2, 4, OP><<<n, 512, 0, st>>>(a);
     return GCONV_OK;
 }
 

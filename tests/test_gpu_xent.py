@@ -65,6 +65,13 @@ def test_large_tiles(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("tokens,vocab", [(500, 10007), (10007, 500)])
+def test_tiles_of_192_columns(dtype, tokens, vocab):
+    """Products of 79 x 3 or 4 x 53 tiles, which take one round of workgroups as such and two of smaller ones."""
+    compare(inputs(dtype, tokens, vocab, 576, ignored=0.1, lse=True, seed=4), 1.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 def test_no_token_counts(dtype):
     s = inputs(dtype, 70, 400, 96, ignored=1.1, lse=True)
     s["h"][3] = float("nan")
