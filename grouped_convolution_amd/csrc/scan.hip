@@ -35,11 +35,11 @@
 // Tokens carry marks (first or last of a sequence, or of none), made beforehand
 // with b and c in float32, four states side by side.
 //
-// Measured (bf16, 16 states): forward of 4 x 2048 tokens of 4096 channels 275 us,
-// of one sequence of 32768 tokens of 2048 channels, in chunks, 250 + 340 under the
-// profiler and 509 in all without, the vector pipes 91% busy; backward of 4 x 2048
-// of 4096 820 us, 600 of them in the last kernel (82% busy). A token of 256
-// sequences of 4096: 33 us, 4.3 TB/s of states.
+// Measured (bf16, 16 states, under the profiler): forward of 4 x 2048 tokens of
+// 4096 channels 275 us; of one sequence of 32768 tokens of 2048 channels, in chunks,
+// 250 + 340 (513 in all without the profiler), the vector pipes 91% busy; backward
+// of 4 x 2048 of 4096 850, 605 of them in the last kernel (84% busy); both ways 1000
+// without the profiler. A token of 256 sequences of 4096: 34 us, 4.2 TB/s of states.
 #include "device_util.h"
 #include "seq_host.h"
 #include "seq_tokens.h"
@@ -1110,7 +1110,7 @@ struct Layout {
 
 // Workgroups of the forward pass. A sequence is cut, and then run over twice, only
 // where there is less than one workgroup a CU; then into as many chunks as make
-// three, as many as run at once (32768 tokens of 2048 channels: 509 us in chunks
+// three, as many as run at once (32768 tokens of 2048 channels: 513 us in chunks
 // for 768 workgroups, 640 for 512; 4 x 2048 of 4096, 256 workgroups uncut: 265,
 // and 280 in three chunks).
 constexpr int64_t kForwardBlocks = 768;

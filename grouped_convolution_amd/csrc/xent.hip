@@ -34,7 +34,7 @@
 //
 // Measured: 8192 bfloat16 tokens of 2048 against 65536 entries, LSE 1.9 ms (1.17
 // PFLOP/s), DZ 2.2, DH 1.7 and DW 1.8 (1.25), with the sort and the targets' sums
-// 7.4 in all; a large library product of random bfloat16 takes 1.21 on this card.
+// 7.3 in all; a large library product of random bfloat16 takes 1.21 on this card.
 #include <cmath>
 
 #include "device_util.h"
