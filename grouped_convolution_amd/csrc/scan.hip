@@ -1115,7 +1115,10 @@ struct Layout {
 // and 280 in three chunks).
 constexpr int64_t kForwardBlocks = 768;
 // ... and the backward pass, whose longer chunks carry fewer states from one to
-// the next but need as many workgroups.
+// the next but need as many workgroups: 128 tokens, else 64 (4 x 2048 of 4096: 1141
+// and 1175 us; 3 x 613 of 300: the last kernel 47 and 27), or 32 where there is less
+// than one a CU (3 x 613 of 300, 180 of 64: 21; 2048 of 1024, 512 of 64: 86 in all
+// by 64 and 95 by 32).
 constexpr int64_t kBackBlocks = 1024;
 
 void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
@@ -1133,7 +1136,8 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
     a->seq.count = (int)d->sequences;
     int64_t chunk;
     if (back) {
-        chunk = outer_of(d) * a->blocks * ((d->tokens + 127) / 128) >= kBackBlocks ? 128 : 64;
+        auto blocks = [&](int64_t of) { return outer_of(d) * a->blocks * ((d->tokens + of - 1) / of); };
+        chunk = blocks(128) >= kBackBlocks ? 128 : blocks(64) >= kCus ? 64 : 32;
     } else {
         const int64_t have = std::max<int64_t>(1, outer_of(d) * a->blocks);
         const int64_t per = have >= kCus ? 1 : (kForwardBlocks + have - 1) / have;
@@ -1163,7 +1167,8 @@ void plan(const gconv_scan_desc* d, bool back, Scan* a, Layout* l)
 }
 
 // Whether the forward pass gives a wave two states: twice the waves where there
-// is no more than a workgroup a CU.
+// is no more than a workgroup a CU (4 x 2048 of 4096: 278 us, by four states 292;
+// by one, with 16 waves, 311).
 bool narrow_forward(const Scan& a) { return a.chunks * a.blocks <= kCus; }
 
 void place(const Layout& l, void* workspace, Scan* a)
