@@ -397,7 +397,10 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
     const fv bias = of_channels<fv, V>(a.dt_bias, w, col), skip = of_channels<fv, V>(a.skip, w, col);
 
     const fs a2 = m.rates(a) * kLog2e;
-    fs h = {}, p = {}, r = {};
+    // What the chunk adds to the adjoint before it is `r` as it is when a sequence begins: no later token can reach that
+    // adjoint, and one that is not finite would, as 0 times it. (Kept aside rather than not computed further: loops for
+    // chunks in which none has begun and others cost 1 to 2% of the whole backward pass, this nothing.)
+    fs h = {}, p = {}, r = {}, reached = {};
     p += 1.f;
     float total = 0.f;
     int broken = 0;
@@ -475,7 +478,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
                 }
                 if (decltype(marked)::value && (firsts >> i & 1)) {
                     h = m.get(again()->dim, again()->states, again()->init, __builtin_amdgcn_readlane(mk, i) >> 2);
-                    p = fs{};
+                    if (ADJ && !broken) reached = r;
                     broken = 1;
                 }
                 const float dt = sd[tile & 1][i][0][m.lane], dtu = sd[tile & 1][i][1][m.lane];
@@ -545,7 +548,7 @@ __global__ __launch_bounds__(NW * 64) void scan_run(Scan a)
 #pragma unroll
         for (int s = 0; s < SPW; ++s) {
             a.ends[m.slot(a, w.chunk, w.block, NW, s)] = h[s];
-            if (ADJ) a.adds[m.slot(a, w.chunk, w.block, NW, s)] = r[s];
+            if (ADJ) a.adds[m.slot(a, w.chunk, w.block, NW, s)] = broken ? reached[s] : r[s];
         }
         if (m.wave == 0) a.sums[(w.chunk * a.blocks + w.block) * kLanes + m.lane] = total;
         if (w.block == 0 && threadIdx.x == 0) a.breaks[w.chunk] = broken;
