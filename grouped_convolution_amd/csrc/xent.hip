@@ -36,6 +36,7 @@
 // PFLOP/s), DZ 2.2, DH 1.7 and DW 1.8 (1.25), with the sort and the targets' sums
 // 7.3 in all; a large library product of random bfloat16 takes 1.21 on this card.
 #include <cmath>
+#include <limits>
 
 #include "device_util.h"
 #include "embed_internal.h"
@@ -380,8 +381,9 @@ __global__ __launch_bounds__(64 * WQ * WP, 1) void xent_gemm(Gemm a)
                 }
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            // (values that are all -infinity, or hold +infinity, are taken as they are)
-            const float below = fabsf(top) == INFINITY ? 0.f : top;
+            // (values that are all -infinity have a sum of 0, those that hold +infinity one of infinity; the latter's is taken
+            // below the largest float, so that in a join it is not multiplied by an exponential that has become 0)
+            const float below = top == INFINITY ? std::numeric_limits<float>::max() : top == -INFINITY ? 0.f : top;
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < FP; ++j)
