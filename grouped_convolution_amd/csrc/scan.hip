@@ -689,7 +689,15 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
         skip[e] = in && a.skip ? a.skip[w.c0 + col + e] : 0.f;
         s_skip[e] = s_bias[e] = 0.f;
     }
-    const fs av = m.rates(a), a2 = av * kLog2e;
+    const fs rate = m.get(a.dim, a.states, a.a, 0);
+    // a of the decay's gradient: 0 for -infinity, whose decay is 0 or 1 and has none (-2e38 in its place would take the
+    // gradient of a step of 0, where the decay is 1, out of float32's range, and softplus's slope of 0 with it)
+    fs av, a2;
+#pragma unroll
+    for (int s = 0; s < SPW; ++s) {
+        av[s] = rate[s] == -INFINITY ? 0.f : rate[s];
+        a2[s] = rate_of(rate[s]) * kLog2e;
+    }
     fs before0 = {}, g = {}, da = {};  // the state before the chunk; the adjoint after it
     if (a.per > 1) {
 #pragma unroll
