@@ -209,10 +209,17 @@ __global__ __launch_bounds__(256) void scan_empty(Sequences seq, const float* fr
 
 // ---- parts that the kernels share -------------------------------------------------
 
-// a, with -2e38 (finite times log2(e)) in place of -infinity: it leaves as little of a
-// state, but a step of 0 (of a token of no sequence, say) leaves all of it, where
-// 0 times infinity is not a number.
-__device__ __forceinline__ float rate_of(float a) { return a == -INFINITY ? -2e38f : a; }
+// Rates up to this one, whose product with log2(e) leaves float32's range or comes near its end, count as -infinity.
+constexpr float kNoMemory = -2e38f;
+
+// a, with kNoMemory in place of what counts as -infinity: it leaves as little of a state (of steps above 1e-36), but a
+// step of 0 (of a token of no sequence, say) leaves all of it, where 0 times infinity is not a number.
+__device__ __forceinline__ float rate_of(float a) { return a < kNoMemory ? kNoMemory : a; }
+
+// a as a factor of the step's gradient: 0 for what counts as -infinity, whose decay is 0 or 1 and has none (kNoMemory in
+// its place would take the gradient of a step of 0, where the decay is 1, out of float32's range, and softplus's slope
+// of 0 with it).
+__device__ __forceinline__ float rate_factor(float a) { return a <= kNoMemory ? 0.f : a; }
 
 // Read-only while the kernel runs, at an address that is the same for a wave: scalar loads.
 typedef const __attribute__((address_space(4))) float* scalar_floats;
@@ -690,12 +697,10 @@ __global__ __launch_bounds__(NW * 64, SPW == 2 ? 4 : 1) void scan_back(Scan a)
         s_skip[e] = s_bias[e] = 0.f;
     }
     const fs rate = m.get(a.dim, a.states, a.a, 0);
-    // a of the decay's gradient: 0 for -infinity, whose decay is 0 or 1 and has none (-2e38 in its place would take the
-    // gradient of a step of 0, where the decay is 1, out of float32's range, and softplus's slope of 0 with it)
     fs av, a2;
 #pragma unroll
     for (int s = 0; s < SPW; ++s) {
-        av[s] = rate[s] == -INFINITY ? 0.f : rate[s];
+        av[s] = rate_factor(rate[s]);
         a2[s] = rate_of(rate[s]) * kLog2e;
     }
     fs before0 = {}, g = {}, da = {};  // the state before the chunk; the adjoint after it

@@ -488,9 +488,9 @@ int gconv_shortconv_step(const gconv_shortconv_desc* d, const void* x, const voi
  * states], shared by the dim / groups channels of a group; strides in elements
  * ([0] between sequences, [1] between tokens, [2] between groups, the last
  * axis contiguous), outputs dense. a [dim, states], skip, dt_bias [dim]
- * float32; a of -infinity is valid (no memory, but for a step of 0; its decay
- * has no gradient). gate, skip and dt_bias may be NULL (1, 0 and 0 in their
- * place).
+ * float32; a of -infinity is valid and any below -2e38 counts as it: no memory
+ * after a step above 1e-36, all of it after one of 0, and no gradient of the
+ * decay. gate, skip and dt_bias may be NULL (1, 0 and 0 in their place).
  * States [sequences, dim, states] float32, dense; initial_state (NULL: 0) and
  * final_state may be NULL. Packed sequences as in linear attention. states up
  * to 64, dim up to 2^20, 2^31 tokens of all sequences together (2^30 of one).

@@ -51,3 +51,25 @@ def against_definition(s, lens):
 def test_steps_of_zero_under_an_infinite_decay():
     s, lens = skipped(-float("inf"), 31)
     against_definition(s, lens)
+
+
+@pytest.mark.parametrize("rate", [-2.4e38, -3e38, torch.finfo(torch.float32).min])
+def test_rates_at_the_end_of_float32(rate):
+    """Times log2(e) such a rate is past float32: it counts as -infinity."""
+    s, lens = skipped(rate, 32)
+    against_definition(s, lens)
+
+
+@pytest.mark.parametrize("rate", [-3e38, torch.finfo(torch.float32).min, -float("inf")])
+def test_rates_at_the_end_of_float32_one_token(rate):
+    """... and in a step, where a token of step 0 leaves the state as it was and another leaves nothing of it."""
+    gen = torch.Generator().manual_seed(5)
+    n = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    u, b, c, state = n(3, 10), n(3, 1, 4), n(3, 1, 4), n(3, 10, 4)
+    dt = torch.tensor([-200.0, 0.5, -200.0], device="cuda")[:, None].expand(3, 10).contiguous()
+    before = state.clone()
+    G.gconv_scan_step(u, dt, torch.full((10, 4), rate, device="cuda"), b, c, state)
+    assert torch.equal(state[[0, 2]], before[[0, 2]])
+    step = torch.log1p(torch.exp(torch.tensor(0.5, dtype=torch.float64)))
+    want = step * (u[1, :, None] * b[1]).double().cpu()
+    R.check("state", state[1], want, 12 * R.U * want.abs())
