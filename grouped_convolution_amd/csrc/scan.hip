@@ -1203,11 +1203,16 @@ void place(const Layout& l, void* workspace, Scan* a)
     a->part_bc = (float*)(w + l.part_bc);
 }
 
-int check_blocks(const Scan& a, int nw)
+// Whether every launch of a call stays below what a launch takes, before any is made.
+int check_blocks(const Scan& a, int nw, bool back)
 {
-    if (a.chunks > max_blocks(nw * 64) / a.blocks || a.places > max_blocks(256) / (a.groups * nw) * 256 ||
+    // (the backward pass's last kernel has twice the waves, up to 16, and its sums of da a workgroup of 1024 threads for
+    // every 64 states of the workgroups' lanes)
+    const int waves = back ? std::min(2 * nw, 16) : nw;
+    if (a.chunks > max_blocks(waves * 64) / a.blocks || a.places > max_blocks(256) / (a.groups * nw) * 256 ||
         a.chunks / a.per * a.blocks * nw >= max_blocks(256))
         return fail(GCONV_ERR_UNSUPPORTED, "too many rows");
+    if (back && (int64_t)a.blocks * nw * kSpw > max_blocks(1024)) return fail(GCONV_ERR_UNSUPPORTED, "too many groups and states");
     return GCONV_OK;
 }
 
@@ -1307,7 +1312,7 @@ int gconv_scan_fwd(const gconv_scan_desc* d, const void* u, const void* dt, cons
     Scan a{};
     Layout l{};
     plan(d, false, &a, &l);
-    st = check_blocks(a, l.nw);
+    st = check_blocks(a, l.nw, false);
     if (st != GCONV_OK) return st;
     st = check_workspace(workspace, workspace_bytes, l.bytes);
     if (st != GCONV_OK) return st;
@@ -1378,7 +1383,7 @@ int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, cons
     Scan a{};
     Layout l{};
     plan(d, true, &a, &l);
-    st = check_blocks(a, l.nw);
+    st = check_blocks(a, l.nw, true);
     if (st != GCONV_OK) return st;
     st = check_workspace(workspace, workspace_bytes, l.bytes);
     if (st != GCONV_OK) return st;
