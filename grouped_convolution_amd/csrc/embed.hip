@@ -385,7 +385,7 @@ int check_desc(const gconv_embed_desc* d)
     if (d->dim > kMaxDim) return fail(GCONV_ERR_UNSUPPORTED, "dim=%lld above %lld", (long long)d->dim, (long long)kMaxDim);
     if (d->sequences > kMaxTokens || d->tokens > kMaxTokens || (d->tokens > 0 && d->sequences > kMaxTokens / d->tokens))
         return fail(GCONV_ERR_UNSUPPORTED, "too many ids");
-    if (!std::isfinite(d->scale)) return fail(GCONV_ERR_ARG, "scale must be finite");
+    if (!std::isfinite((float)d->scale)) return fail(GCONV_ERR_ARG, "scale must be finite as float32");
     return GCONV_OK;
 }
 

@@ -647,7 +647,7 @@ int check_desc(const gconv_xent_desc* d)
     if (d->vocab > kMaxVocab) return fail(GCONV_ERR_UNSUPPORTED, "vocab=%lld above %lld", (long long)d->vocab, (long long)kMaxVocab);
     if (d->sequences > kMaxRows || d->tokens > kMaxRows || (d->tokens > 0 && d->sequences > kMaxRows / d->tokens))
         return fail(GCONV_ERR_UNSUPPORTED, "too many tokens");
-    if (!std::isfinite(d->scale)) return fail(GCONV_ERR_ARG, "scale must be finite");
+    if (!std::isfinite((float)d->scale)) return fail(GCONV_ERR_ARG, "scale must be finite as float32");
     return GCONV_OK;
 }
 
