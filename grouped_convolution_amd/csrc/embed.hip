@@ -536,19 +536,16 @@ size_t embed_runs_workspace(const EmbedRuns& r)
     return l.bytes;
 }
 
-int embed_runs_sort(EmbedRuns* r, hipStream_t st)
+void embed_runs_sort(EmbedRuns* r, hipStream_t st)
 {
     const gconv_embed_desc d = desc_of(*r);
     Embed a{};
     Layout l{};
     plan(&d, &a, &l);
-    const int rc = check_launch(a);
-    if (rc != GCONV_OK) return rc;
     place(l, r->workspace, &a);
     a.ids = r->ids;
     r->order = sort(a, st);
     r->start = a.start;
-    return GCONV_OK;
 }
 
 void embed_runs_sum(const EmbedRuns& r, int64_t row0, int64_t row1, hipStream_t st)

@@ -25,7 +25,7 @@ struct EmbedRuns {
 };
 
 size_t embed_runs_workspace(const EmbedRuns& r);
-int embed_runs_sort(EmbedRuns* r, hipStream_t st);
+void embed_runs_sort(EmbedRuns* r, hipStream_t st);
 // For the ids row0..row1-1.
 void embed_runs_sum(const EmbedRuns& r, int64_t row0, int64_t row1, hipStream_t st);
 

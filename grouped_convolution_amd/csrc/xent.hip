@@ -758,7 +758,8 @@ void make_plan(const gconv_xent_desc* d, bool back, Plan* p)
 
 int64_t tiles_of(const Tile& t, int64_t rows, int64_t cols) { return ((rows + t.q - 1) / t.q) * ((cols + t.p - 1) / t.p); }
 
-// Whether every launch of a call stays below what a launch takes, before any is made.
+// Whether every launch of a call stays below what a launch takes, before any is made. (The sums by target have a
+// workgroup for some 32 tokens or more and 1024 columns: fewer than the sums' folding has.)
 int check_launches(const gconv_xent_desc* d, const Plan& p, bool back)
 {
     const int64_t cols = std::min(p.piece, d->vocab), most = max_blocks(512);
@@ -774,7 +775,7 @@ int check_launches(const gconv_xent_desc* d, const Plan& p, bool back)
 }
 
 template <typename T, int OP>
-int launch(Gemm a, const Tile& t, hipStream_t st)
+void launch(Gemm a, const Tile& t, hipStream_t st)
 {
     a.tq = (a.rows + t.q - 1) / t.q;
     a.tp = (a.cols + t.p - 1) / t.p;
@@ -784,17 +785,15 @@ int launch(Gemm a, const Tile& t, hipStream_t st)
     else if (t.kind == 2) xent_gemm<T, 64, 256, 1, 8, OP><<<n, 512, 0, st>>>(a);
     else if (t.kind == 3) xent_gemm<T, 128, 256, 2, 4, OP><<<n, 512, 0, st>>>(a);
     else xent_gemm<T, 128, 192, 2, 4, OP><<<n, 512, 0, st>>>(a);
-    return GCONV_OK;
 }
 
 template <typename T>
-int pack(const void* src, int64_t seq, int64_t tok, int64_t tokens, int64_t rows, int64_t dim, int64_t pitch, const void* targets, int wide,
-         int64_t vocab, __bf16* dst, hipStream_t st)
+void pack(const void* src, int64_t seq, int64_t tok, int64_t tokens, int64_t rows, int64_t dim, int64_t pitch, const void* targets, int wide,
+          int64_t vocab, __bf16* dst, hipStream_t st)
 {
     const int64_t blocks = (rows * (pitch / 8) + 255) / 256;
     xent_pack<T><<<(unsigned)blocks, 256, 0, st>>>((const T*)src, seq, tok, std::max<int64_t>(tokens, 1), rows, (int)dim, (int)pitch, targets,
                                                    wide, vocab, dst);
-    return GCONV_OK;
 }
 
 template <typename T>
@@ -806,15 +805,14 @@ int forward(const gconv_xent_desc* d, const Plan& p, const void* h, const void* 
     Gemm a{};
     a.q = Operand{(const __bf16*)h, step, 0};
     a.p = Operand{(const __bf16*)w, d->dim, 0};
-    int rc;
     // h is read itself where it is bfloat16 rows of whole stages at 16-byte boundaries, one after another
     if (!as_it_is(d) || !flat || step % 8 || step < d->dim || step > kMaxDim || ((uintptr_t)h & 15)) {
         a.q = Operand{(const __bf16*)(ws + p.h), p.pitch, p.rows * p.pitch};
-        if ((rc = pack<T>(h, d->h_stride[0], d->h_stride[1], d->tokens, p.rows, d->dim, p.pitch, nullptr, 0, 0, (__bf16*)(ws + p.h), st))) return rc;
+        pack<T>(h, d->h_stride[0], d->h_stride[1], d->tokens, p.rows, d->dim, p.pitch, nullptr, 0, 0, (__bf16*)(ws + p.h), st);
     }
     if (!as_it_is(d)) {
         a.p = Operand{(const __bf16*)(ws + p.w), p.pitch, d->vocab * p.pitch};
-        if ((rc = pack<T>(w, 0, d->dim, d->vocab, d->vocab, d->dim, p.pitch, nullptr, 0, 0, (__bf16*)(ws + p.w), st))) return rc;
+        pack<T>(w, 0, d->dim, d->vocab, d->vocab, d->dim, p.pitch, nullptr, 0, 0, (__bf16*)(ws + p.w), st);
     }
     a.rows = (int)p.rows;
     a.cols = a.vocab = (int)d->vocab;
@@ -826,7 +824,7 @@ int forward(const gconv_xent_desc* d, const Plan& p, const void* h, const void* 
     a.scale = (float)d->scale;
     a.part = (float2*)(ws + p.part);
     a.picked = (float*)(ws + p.picked);
-    if ((rc = launch<T, LSE>(a, p.lse, st))) return rc;
+    launch<T, LSE>(a, p.lse, st);
     xent_join<<<(unsigned)((p.rows + 63) / 64), 1024, 0, st>>>(a.part, (int)p.lse_tiles, (int)p.rows, a.picked, targets, a.wide, d->vocab, loss, lse);
     return finish();
 }
@@ -838,11 +836,10 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
     const int wide = d->index == GCONV_I64;
     const Operand hp{(const __bf16*)(ws + p.h), p.pitch, p.rows * p.pitch};
     Operand wp{(const __bf16*)w, d->dim, 0};
-    int rc;
-    if ((rc = pack<T>(h, d->h_stride[0], d->h_stride[1], d->tokens, p.rows, d->dim, p.pitch, targets, wide, d->vocab, (__bf16*)(ws + p.h), st))) return rc;
+    pack<T>(h, d->h_stride[0], d->h_stride[1], d->tokens, p.rows, d->dim, p.pitch, targets, wide, d->vocab, (__bf16*)(ws + p.h), st);
     if (!as_it_is(d)) {
         wp = Operand{(const __bf16*)(ws + p.w), p.pitch, d->vocab * p.pitch};
-        if ((rc = pack<T>(w, 0, d->dim, d->vocab, d->vocab, d->dim, p.pitch, nullptr, 0, 0, (__bf16*)(ws + p.w), st))) return rc;
+        pack<T>(w, 0, d->dim, d->vocab, d->vocab, d->dim, p.pitch, nullptr, 0, 0, (__bf16*)(ws + p.w), st);
     }
     EmbedRuns runs = runs_of(d, targets);
     float* left = sizeof(T) == 2 ? (float*)(ws + p.left) : nullptr;
@@ -852,7 +849,7 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         runs.pitch = hp.pitch;
         runs.weight = left;
         runs.sums = ws + p.fix;
-        if ((rc = embed_runs_sort(&runs, st))) return rc;
+        embed_runs_sort(&runs, st);
     }
     const Operand dz{(const __bf16*)(ws + p.dzs), p.piece, p.rows * p.piece};
     const int vec = d->dim % 8 == 0 ? 8 : d->dim % 4 == 0 ? 4 : 1;
@@ -882,7 +879,7 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         // where dz would not stay in the 256 MB cache behind the L2s, past it: the operands stay (537 MB: 2 x 1088 and
         // 2 x 843 us for DZ and DH, 2 x 1108 and 2 x 866 through it)
         a.stream = p.rows * p.piece * p.parts * 2 >= (int64_t)160 << 20;
-        if ((rc = launch<T, DZ>(a, p.dz, st))) return rc;
+        launch<T, DZ>(a, p.dz, st);
         Gemm b{};
         b.q = dz;
         b.p = rows;
@@ -901,7 +898,7 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
         b.targets = targets;
         b.wide = wide;
         b.vocab = (int)d->vocab;
-        if ((rc = launch<T, DH>(b, p.dh, st))) return rc;
+        launch<T, DH>(b, p.dh, st);
         Gemm c{};
         c.q = dz;
         c.p = hp;
@@ -919,7 +916,7 @@ int backward(const gconv_xent_desc* d, const Plan& p, const float* dloss, const 
             c.start = runs.start + v0;
             c.fix = (const __bf16*)runs.sums;
         }
-        if ((rc = launch<T, DW>(c, p.dw, st))) return rc;
+        launch<T, DW>(c, p.dw, st);
         if (p.dw_splits > 1) {
             const int64_t count = cols * d->dim;
             xent_fold<T><<<(unsigned)((count + 255) / 256), 256, 0, st>>>(c.sums, p.dw_splits, count, to);
