@@ -40,13 +40,12 @@
 
 #include "device_util.h"
 #include "embed_internal.h"
+#include "lds_copy.h"
 #include "seq_host.h"
 #include "seq_tokens.h"
 
 namespace gconv {
 namespace {
-
-typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kStepK = 64;  // reduction length of a stage
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -103,32 +102,6 @@ __device__ __forceinline__ int wanted(int64_t target, int col0)
 // (past the last, which the loads of stages that are not there ask for, the last)
 __device__ __forceinline__ int part_q(int parts, int seg) { return parts == 1 ? 0 : 0x201100 >> (20 - 4 * min(seg, 5)) & 3; }
 __device__ __forceinline__ int part_p(int parts, int seg) { return parts == 1 ? 0 : 0x021010 >> (20 - 4 * min(seg, 5)) & 3; }
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// 64 lanes' 16 bytes from global memory straight to 1024 bytes of LDS (in
-// assembly, as it writes no register and the compiler would wait for it before
-// any read of LDS; it writes M0, which no one needs kept).
-__device__ __forceinline__ void copy_lds(u4 rsrc, uint32_t lds, uint32_t off)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// Waits until at most N of this wave's loads are still under way.
-template <int N>
-__device__ __forceinline__ void wait_loads()
-{
-    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
-}
-
-__device__ __forceinline__ u4 resource(const void* p, uint32_t bytes)
-{
-    const uint64_t v = (uint64_t)p;
-    return u4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v), (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)),
-              (uint32_t)__builtin_amdgcn_readfirstlane(bytes), 0x00020000u};
-}
 
 // Stages are loaded from a base that moves on with them, at offsets that stay:
 // no operand is too large for 32 bits, and a stage past the last has a size of 0.
