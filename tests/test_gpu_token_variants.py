@@ -178,3 +178,28 @@ def test_pieces_of_the_vocabulary_with_cut_reductions(dtype, tokens, vocab, dim)
     want = R.xent(h, w, targets, 0.7, dloss, dlse)
     for name, v in (("loss", loss), ("lse", lse), ("dh", dh), ("dw", dw)):
         R.check(name, v, *want[name])
+
+
+# ---- nothing to do
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_no_sequences(dtype):
+    """Batches of no sequence: empty results, and gradients of 0 for what all sequences share."""
+    D, S, K = 40, 5, 4
+    x, b = torch.zeros(0, 7, D, dtype=dtype, device="cuda"), torch.zeros(0, 7, 2, S, dtype=dtype, device="cuda")
+    w, a, ids = torch.randn(D, K, device="cuda").to(dtype), -torch.rand(D, S, device="cuda"), torch.zeros(0, 7, dtype=torch.int64, device="cuda")
+    d, held = torch.randn(D, device="cuda"), torch.zeros(0, D, S, device="cuda")
+    y, final = G.gconv_shortconv_fwd(x, w, w[:, 0].contiguous(), initial_state=x.new_zeros(0, K - 1, D))
+    dx, dw, dbias, dinit = G.gconv_shortconv_bwd(x, x, w, w[:, 0].contiguous(), initial_state=x.new_zeros(0, K - 1, D))
+    assert y.shape == dx.shape == x.shape and final.shape == dinit.shape == (0, K - 1, D) and not dw.any() and not dbias.any()
+    kw = dict(skip=d, gate=x, dt_bias=d, initial_state=held)
+    y, final = G.gconv_scan_fwd(x, x, a, b, b, **kw)
+    got = G.gconv_scan_bwd(x, x, x, a, b, b, d_final_state=held, **kw)
+    assert y.shape == got[0].shape == x.shape and final.shape == got[8].shape == (0, D, S)
+    assert not any(got[i].any() for i in (2, 5, 7)) and got[2].shape == (D, S)
+    assert G.gconv_shortconv_step(x[:, 0], w, x.new_zeros(3, K - 1, D)).shape == (0, D)
+    assert G.gconv_scan_step(x[:, 0], x[:, 0], a, b[:, 0], b[:, 0], held.new_zeros(3, D, S)).shape == (0, D)
+    assert G.gconv_embed_fwd(w, ids).shape == (0, 7, K) and not G.gconv_embed_bwd(x, ids, 9).any()
+    loss, lse = G.gconv_xent_fwd(x, w.new_ones(11, D), ids)
+    dh, dw = G.gconv_xent_bwd(loss, x, w.new_ones(11, D), ids, lse)
+    assert loss.shape == lse.shape == (0, 7) and dh.shape == x.shape and not dw.any()
