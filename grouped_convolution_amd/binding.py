@@ -1011,7 +1011,8 @@ def gconv_scan_bwd(dy, u, dt, a, b, c, *, skip=None, gate=None, dt_bias=None, so
                    d_final_state=None, workspace=None):
     """Gradients of gconv_scan_fwd for dy of y and d_final_state of the final state (None: 0). Returns du,
     ddt, da, db, dc, dskip, dgate, ddt_bias and the gradient of initial_state, of the inputs' shapes and
-    types (None for those that are None)."""
+    types (None for those that are None). The workspace takes about 0.76 bytes for each token, channel and
+    state."""
     def make():
         d, _ = _scan_desc(u, dt, a, b, c, skip, gate, dt_bias, softplus, cu_seqlens, initial_state, _seq(dy, "dy"), d_final_state)
         return ctypes.byref(d), gconv_scan_workspace_size(d, SCAN_BWD)
@@ -1106,7 +1107,7 @@ def gconv_embed_fwd(table, ids, *, scale=1.0):
 
 def gconv_embed_bwd(dy, ids, rows, *, scale=1.0, workspace=None):
     """The gradient [rows, D] of gconv_embed_fwd's table for dy of its result (any strides with a
-    contiguous last axis): each row the sum over its tokens, in their order; rows without tokens are 0."""
+    contiguous last axis): each row the sum over its tokens, in a fixed order; rows without tokens are 0."""
     def make():
         _seq(dy, "dy")
         index = _names(ids, "ids", dy.device)
@@ -1143,7 +1144,7 @@ def gconv_xent_workspace_size(desc: gconv_xent_desc, op: int) -> int:
 def gconv_xent_fwd(h, w, targets, *, scale=1.0, workspace=None):
     """Softmax cross entropy of tokens against a vocabulary, whose logits scale * h w^T are not kept.
     h [T, D] or [N, T, D] (float32 or bfloat16, any strides with a contiguous last axis), w [vocab, D]
-    of the same type, targets int32 or int64 [T] or [N, T]; a target outside the vocabulary does not
+    of the same type (at a 16-byte boundary where it is bfloat16 and D a multiple of 64), targets int32 or int64 [T] or [N, T]; a target outside the vocabulary does not
     count. Returns loss (0 where it does not count) and lse, the logarithm of the sum of the logits'
     exponentials, of targets' shape in float32."""
     def make():

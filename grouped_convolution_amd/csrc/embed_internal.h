@@ -21,7 +21,9 @@ struct EmbedRuns {
     const void* src;      // [tokens] rows
     int64_t pitch;        // elements between them
     const float* weight;  // [tokens]
-    void* sums;           // [tokens][dim] in bfloat16: that of id v, of weight x row over its tokens, at start[v]
+    // [tokens][dim]: that of id v, of weight x row over its tokens, at start[v]; taken in float32 and rounded to bfloat16,
+    // as what they make up for is itself a rounding to it of another number
+    void* sums;
 };
 
 size_t embed_runs_workspace(const EmbedRuns& r);

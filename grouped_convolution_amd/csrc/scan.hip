@@ -37,9 +37,10 @@
 //
 // Measured (bf16, 16 states, under the profiler): forward of 4 x 2048 tokens of
 // 4096 channels 275 us; of one sequence of 32768 tokens of 2048 channels, in chunks,
-// 250 + 340 (513 in all without the profiler), the vector pipes 91% busy; backward
-// of 4 x 2048 of 4096 850, 605 of them in the last kernel (84% busy); both ways 1000
-// without the profiler. A token of 256 sequences of 4096: 34 us, 4.2 TB/s of states.
+// 256 + 346 (508 in all without the profiler), the vector pipes 91% busy; backward
+// of 4 x 2048 of 4096 850, 601 of them in the last kernel (84% busy); without the
+// profiler 750, and both ways 993. A token of 256 sequences of 4096: 34 us, 4.2 TB/s
+// of states.
 #include "device_util.h"
 #include "seq_host.h"
 #include "seq_tokens.h"
@@ -113,8 +114,9 @@ __device__ __forceinline__ Where where(const Scan& a)
 
 // softplus(x) = max(x, 0) + log(1 + w), w = exp(-|x|): the logarithm of 1 + w as
 // it was rounded, and what the rounding left of w (at most 2^-24, where w is near
-// 1 and half as much would be right; exact where w is small), so right to the last
-// bits however small w is.
+// 1 and half as much would be right; exact where w is small), so no less exact
+// relative to it than w is: off by some |x| half steps, from the rounding of the
+// exponential's argument.
 __device__ __forceinline__ float softplus_of(float x)
 {
     const float w = __builtin_amdgcn_exp2f(fabsf(x) * -kLog2e), v = 1.f + w;

@@ -27,14 +27,18 @@
 // bfloat16's, the target's entry, which outweighs a row's others, would be most of
 // the error in dh and dw (2.4e-3 of their norm, with the outputs' own 1.7e-3): what
 // its rounding leaves is kept in float32 for each token, and dh gets that times
-// the target's row of w, dw that times h, summed over the tokens of a target.
+// the target's row of w, dw that times h, summed over the tokens of a target (in
+// float32; the sums wait in bfloat16, whose 2^-9 of them are 2^-18 of the entry).
+// What is left of dz's rounding is 2.3e-5 of the norm of dh and dw, whose own
+// rounding is 1.66e-3.
 //
 // Tokens that do not count (a target outside the vocabulary) have rows of zeros
 // in place of their h, so nothing in them reaches dw.
 //
-// Measured: 8192 bfloat16 tokens of 2048 against 65536 entries, LSE 1.9 ms (1.17
-// PFLOP/s), DZ 2.2, DH 1.7 and DW 1.8 (1.25), with the sort and the targets' sums
-// 7.3 in all; a large library product of random bfloat16 takes 1.21 on this card.
+// Measured: 8192 bfloat16 tokens of 2048 against 65536 entries, under the profiler
+// LSE 1.85 ms (1.19 PFLOP/s), DZ 2.16, DH 1.66 and DW 1.75 (1.26), with the sort and
+// the targets' sums 7.54 in all; without it 7.2 to 7.6, by the card. A large library
+// product of random bfloat16 reaches 1.21 PFLOP/s.
 #include <cmath>
 #include <limits>
 

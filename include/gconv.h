@@ -523,6 +523,11 @@ int gconv_scan_fwd(const gconv_scan_desc* d, const void* u, const void* dt, cons
  * ddt, db, dc, dgate of the inputs' type, dense; da, dskip, ddt_bias summed
  * over all tokens in float32; d_initial_state may be NULL. dskip, dgate and
  * ddt_bias are given exactly when their inputs are.
+ *
+ * The workspace holds the states before every eighth token and sums over 64
+ * channels each of db and dc: about 0.76 bytes for each token, channel and state
+ * (up to three times as many where sequences or groups are short), 0.41 GB for
+ * 4 x 2048 tokens of 4096 x 16, 25 GB for 65536 of 8192 x 64.
  */
 int gconv_scan_bwd(const gconv_scan_desc* d, const void* dy, const void* u, const void* dt, const float* a, const void* b, const void* c,
                    const float* skip, const void* gate, const float* dt_bias, const int32_t* cu_seqlens, const float* initial_state,
@@ -565,8 +570,10 @@ int gconv_embed_workspace_size(const gconv_embed_desc* d, size_t* bytes);
 int gconv_embed_fwd(const gconv_embed_desc* d, const void* table, const void* ids, void* y, void* stream);
 
 /*
- * dtable [rows, dim], dense, for dy of y: each row the sum over its tokens, in
- * their order, in float32 and rounded once; rows without tokens are 0.
+ * dtable [rows, dim], dense, for dy of y: each row the sum over its tokens in
+ * float32, rounded once; rows without tokens are 0. The order of the sums is
+ * fixed by the ids: that of the tokens, for rows with many of them by slices
+ * whose sums are then added up, so equal calls give equal results.
  */
 int gconv_embed_bwd(const gconv_embed_desc* d, const void* dy, const void* ids, void* dtable, void* workspace, size_t workspace_bytes,
                     void* stream);
@@ -612,7 +619,9 @@ int gconv_xent_fwd(const gconv_xent_desc* d, const void* h, const void* w, const
  * float32 dense, given the forward pass's lse: dh [sequences, tokens, dim] and
  * dw, dense, of the inputs' type. The logits' gradient is rounded to bfloat16
  * for the products that follow where h and w are bfloat16, but for the target's
- * entry, whose rounding is made up for.
+ * entry, whose rounding is made up for: by what it left in float32 for dh, and
+ * for dw by the sums of that times h over a target's tokens, taken in float32
+ * and rounded to bfloat16 (2^-9 of a rest that is 2^-9 of the entry at most).
  */
 int gconv_xent_bwd(const gconv_xent_desc* d, const float* dloss, const float* dlse, const void* h, const void* w, const void* targets,
                    const float* lse, void* dh, void* dw, void* workspace, size_t workspace_bytes, void* stream);
